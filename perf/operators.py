@@ -1,0 +1,406 @@
+"""What the microscaled fp4 linears and the expert sort are measured on.
+
+Four operators, each in several sizes:
+
+  quantize   rows (or columns) of a matrix to MXFP4 and back to the values the codes stand for
+  linear     y = Q(x) W^T with W held in MXFP4; as a training step also dx and dW
+  grouped    the same product with one weight per expert, over rows sorted by expert
+  dispatch   tokens sorted by expert, gathered, combined with weights; and the gradients
+
+``own`` False computes them with elementary torch operations in 32 bits, ``own``
+True through the library. Tensors in MXFP4 are held as the library holds them:
+codes uint8 [R][C / 2] (element 2i in the low nibble) and scales uint8
+[C / 128][R][4] (byte b of word (g, r): block 4 g + b of row r).
+"""
+import math
+
+import torch
+
+own = False
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+SIZE = {"f16": 2, "bf16": 2, "f32": 4}
+E2M1 = [0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0]
+
+
+# ---------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # the activations of one small batch on their way into a 4-bit layer: launch latency
+        {"name": "quantize 16 rows", "op": "quantize", "rows": 16, "cols": 4096, "dtype": "f16", "transpose": False},
+        # a training batch's activations
+        {"name": "quantize 16384 rows", "op": "quantize", "rows": 16384, "cols": 4096, "dtype": "bf16",
+         "transpose": False},
+        # a gradient on its way into the weight's gradient: blocks along the tokens, a ragged count
+        {"name": "quantize columns f32", "op": "quantize", "rows": 4111, "cols": 5120, "dtype": "f32",
+         "transpose": True},
+        # decode, one token
+        {"name": "linear 1 token", "op": "linear", "M": 1, "K": 4096, "N": 4096, "dtype": "f16"},
+        # decode, a batch of 16, the widest matrix of the dense stack
+        {"name": "linear 16 tokens", "op": "linear", "M": 16, "K": 4096, "N": 28672, "dtype": "bf16"},
+        # a prompt of odd length on the FFN pair's first matrix
+        {"name": "linear 1777 tokens", "op": "linear", "M": 1777, "K": 5120, "N": 17408, "dtype": "f16"},
+        # a training step of one linear: forward, the input's gradient, the weight's
+        {"name": "train 8192 tokens", "op": "train", "M": 8192, "K": 4096, "N": 14336, "dtype": "bf16"},
+        # the MoE block's gate|up at decode: about one row per expert
+        {"name": "grouped decode", "op": "grouped", "M": 32, "E": 256, "top_k": 8, "K": 2048, "N": 2048,
+         "dtype": "f16"},
+        # the same block with a prompt: about 64 rows per expert
+        {"name": "grouped 2048 tokens", "op": "grouped", "M": 2048, "E": 256, "top_k": 8, "K": 2048, "N": 2048,
+         "dtype": "bf16"},
+        # few, large experts and a long batch
+        {"name": "grouped 8192 tokens", "op": "grouped", "M": 8192, "E": 8, "top_k": 2, "K": 4096, "N": 28672,
+         "dtype": "bf16"},
+        # dispatch and combine of one decode step
+        {"name": "dispatch 32 tokens", "op": "dispatch", "M": 32, "E": 256, "top_k": 8, "H": 2048, "dtype": "f16",
+         "drop": 0.0, "backward": False},
+        # a training batch, forward and backward, some picks dropped
+        {"name": "dispatch 16384 tokens", "op": "dispatch", "M": 16384, "E": 256, "top_k": 8, "H": 2048,
+         "dtype": "bf16", "drop": 0.05, "backward": True},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["quantize", "linear", "train", "grouped", "dispatch"])
+    if op == "quantize":
+        cols = 128 * _log(rng, 1, 128)
+        rows = _log(rng, 1, max(1, min(1 << 17, (1 << 26) // cols)))
+        return {"op": op, "rows": rows, "cols": cols, "dtype": rng.choice(["f16", "bf16", "f32"]),
+                "transpose": rng.random() < 0.4}
+    if op == "linear":
+        K, N = 128 * _log(rng, 1, 136), _log(rng, 1, 28672)
+        M = _log(rng, 1, min(4096, (1 << 40) // (K * N)))
+        return {"op": op, "M": M, "K": K, "N": N, "dtype": rng.choice(["f16", "bf16"])}
+    if op == "train":
+        K, N, M = 128 * _log(rng, 1, 32), 128 * _log(rng, 1, 112), _log(rng, 2, 8192)
+        return {"op": op, "M": M, "K": K, "N": N, "dtype": rng.choice(["f16", "bf16"])}
+    if op == "grouped":
+        E = _log(rng, 1, 256)
+        K, N = 128 * _log(rng, 1, 32), _log(rng, 8, max(8, min(28672, (1 << 28) // (E * 512))))
+        top_k = rng.randint(1, min(8, E))
+        M = _log(rng, 1, min(4096, (1 << 40) // (top_k * K * N)))
+        return {"op": op, "M": M, "E": E, "top_k": top_k, "K": K, "N": N,
+                "dtype": rng.choice(["f16", "bf16"])}
+    E, H = _log(rng, 1, 1024), _log(rng, 8, 8192)
+    top_k = rng.randint(1, min(16, E))
+    M = _log(rng, 1, max(1, min(32768, (1 << 28) // (H * top_k))))
+    return {"op": op, "M": M, "E": E, "top_k": top_k, "H": H, "dtype": rng.choice(["f16", "bf16", "f32"]),
+            "drop": rng.choice([0.0, 0.1, 0.6]), "backward": rng.random() < 0.6}
+
+
+# ---------------------------------------------------------------- inputs
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _activations(rows, cols, dtype, g):
+    """Normal values; one channel in about 64 is twenty times the rest, as in a transformer's residual
+    stream, and one row in 16 starts with a block of zeros."""
+    x = torch.randn(rows, cols, device="cuda", generator=g)
+    x *= torch.where(torch.rand(cols, device="cuda", generator=g) < 1 / 64, 20.0, 1.0)
+    x[::16, :32] = 0
+    return x.to(DT[dtype])
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    s = dict(case)
+    op = case["op"]
+
+    def weight(rows, cols):
+        """An MXFP4 weight (codes, scales) of normal values with standard deviation 0.02, made in pieces."""
+        codes = torch.empty(rows, cols // 2, dtype=torch.uint8, device="cuda")
+        scales = torch.empty(cols // 128, rows, 4, dtype=torch.uint8, device="cuda")
+        step = max(1, (1 << 26) // cols)
+        for r in range(0, rows, step):
+            n = min(step, rows - r)
+            codes[r:r + n], scales[:, r:r + n] = _encode(0.02 * torch.randn(n, cols, device="cuda", generator=g))
+        return codes, scales
+
+    if op == "quantize":
+        s["x"] = _activations(case["rows"], case["cols"], case["dtype"], g)
+    elif op == "linear":
+        s["x"] = _activations(case["M"], case["K"], case["dtype"], g)
+        s["codes"], s["scales"] = weight(case["N"], case["K"])
+    elif op == "train":
+        dt = DT[case["dtype"]]
+        s["x"] = _activations(case["M"], case["K"], case["dtype"], g)
+        s["w"] = (0.02 * torch.randn(case["N"], case["K"], device="cuda", generator=g)).to(dt)
+        # gradients as a loss scaled for 16 bits gives them
+        s["dy"] = (0.01 * torch.randn(case["M"], case["N"], device="cuda", generator=g)).to(dt)
+    elif op == "grouped":
+        M, E, k = case["M"], case["E"], case["top_k"]
+        s["x"] = _activations(M, case["K"], case["dtype"], g)
+        s["codes"], s["scales"] = weight(E * case["N"], case["K"])
+        # some experts are preferred
+        lean = 0.5 * torch.randn(E, device="cuda", generator=g)
+        ids = torch.topk(torch.randn(M, E, device="cuda", generator=g) + lean, k, dim=1).indices.reshape(-1)
+        counts = torch.bincount(ids, minlength=E)
+        s["perm"] = torch.sort(ids, stable=True).indices.to(torch.int32)
+        s["offsets"] = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+        s["most"] = int(counts.max())   # rows of the fullest expert
+    else:
+        M, E, k, H = case["M"], case["E"], case["top_k"], case["H"]
+        dt = DT[case["dtype"]]
+        lean = 0.5 * torch.randn(E, device="cuda", generator=g)
+        ids = torch.topk(torch.randn(M, E, device="cuda", generator=g) + lean, k, dim=1).indices.to(torch.int32)
+        ids[torch.rand(M, k, device="cuda", generator=g) < case["drop"]] = -1
+        s["ids"] = ids
+        s["weights"] = torch.softmax(torch.randn(M, k, device="cuda", generator=g), 1)
+        s["x"] = _activations(M, H, case["dtype"], g)
+        s["o"] = torch.randn(M * k, H, device="cuda", generator=g).to(dt)      # what the experts gave
+        # the buffers a training program keeps: rows behind the last pick stay zero
+        s["xs"] = torch.zeros(M * k, H, device="cuda", dtype=dt)
+        if case["backward"]:
+            s["do"] = torch.zeros(M * k, H, device="cuda", dtype=dt)
+            s["dy"] = (0.01 * torch.randn(M, H, device="cuda", generator=g)).to(dt)
+            s["dxs"] = (0.01 * torch.randn(M * k, H, device="cuda", generator=g)).to(dt)
+    return s
+
+
+# ---------------------------------------------------------------- plain form
+
+def _two_to(e):
+    """2^e in 32 bits for whole e in [-127, 127], put together from its bits."""
+    bits = torch.where(e == -127, torch.full_like(e, 0x00400000), (e + 127) << 23)
+    return bits.to(torch.int32).view(torch.float32)
+
+
+def _round_blocks(x):
+    """x [R][C] in blocks of 32 along C: e2m1 magnitudes' numbers, signs, scale exponents (128: not a number)."""
+    v = x.float().reshape(x.shape[0], -1, 32)
+    m = v.abs().amax(-1)
+    bad = ~torch.isfinite(m)
+    e = (torch.frexp(torch.where(bad, 1.0, m)).exponent - 3).clamp(-127, 125)
+    e = torch.where(m == 0, -127, e)
+    a = (v * _two_to(-e)[..., None]).abs()
+    # a middle goes to the even number
+    n = ((a > 0.25).to(torch.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5))
+    return n, torch.signbit(v), torch.where(bad, 128, e)
+
+
+def _encode(x):
+    """(codes [R][C / 2], scales [C / 128][R][4]) of x [R][C]."""
+    n, neg, e = _round_blocks(x)
+    n = (n + 8 * neg).to(torch.uint8).reshape(x.shape[0], -1)
+    scales = (e + 127).to(torch.uint8).reshape(x.shape[0], -1, 4).transpose(0, 1).contiguous()
+    return n[:, 0::2] | (n[:, 1::2] << 4), scales
+
+
+def _rounded(x):
+    """x [R][C] after quantisation, in 32 bits."""
+    n, neg, e = _round_blocks(x)
+    v = torch.tensor(E2M1, device=x.device)[n.long()] * torch.where(neg, -1.0, 1.0)
+    s = torch.where(e == 128, torch.nan, _two_to(e.clamp(max=127)))
+    return (v * s[..., None]).reshape(x.shape)
+
+
+def _values(codes, scales):
+    """The 32-bit values [R][C] that codes and scales stand for."""
+    table = torch.tensor(E2M1 + [-v for v in E2M1], device=codes.device)
+    v = torch.stack([table[(codes & 15).long()], table[(codes >> 4).long()]], -1).reshape(codes.shape[0], -1, 32)
+    s = _two_to(scales.to(torch.int32).transpose(0, 1).reshape(codes.shape[0], -1) - 127)
+    return (v * s[..., None]).reshape(codes.shape[0], -1)
+
+
+def _columns(x):
+    """x^T [C][R padded with zeros to a multiple of 128]."""
+    return torch.nn.functional.pad(x, (0, 0, 0, -x.shape[0] % 128)).t().contiguous()
+
+
+def _plain_grouped(s):
+    E, K, N, most = s["E"], s["K"], s["N"], s["most"]
+    w = _values(s["codes"], s["scales"]).reshape(E, N, K).transpose(1, 2).contiguous()
+    rows = s["x"].shape[0] * s["top_k"]
+    at = torch.arange(rows, device="cuda", dtype=torch.int32)
+    e = torch.searchsorted(s["offsets"][1:].contiguous(), at, right=True)
+    slot = e * most + (at - s["offsets"][e])
+    xs = torch.zeros(E * most, K, device="cuda")
+    xs[slot] = _rounded(s["x"])[(s["perm"] // s["top_k"]).long()]
+    return torch.bmm(xs.reshape(E, most, K), w).reshape(E * most, N)[slot].to(s["x"].dtype)
+
+
+def _plain_dispatch(s):
+    M, E, k, H = s["M"], s["E"], s["top_k"], s["H"]
+    dt = s["x"].dtype
+    ids = s["ids"].reshape(-1)
+    kept = (ids >= 0) & (ids < E)
+    perm = torch.sort(torch.where(kept, ids, E), stable=True).indices
+    pos = torch.empty_like(perm)
+    pos[perm] = torch.arange(M * k, device="cuda")
+    counts = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    counts.index_add_(0, torch.where(kept, ids, E).long(), torch.ones_like(ids))
+    offsets = torch.cat([counts.new_zeros(1), counts[:E].cumsum(0).to(torch.int32)])
+    there = kept[perm][:, None]
+    out = {"offsets": offsets, "pos": torch.where(kept, pos, -1).to(torch.int32).reshape(M, k)}
+    out["xs"] = torch.where(there, s["x"][perm // k], 0)
+    w = torch.where(kept.reshape(M, k), s["weights"], 0)
+    o = s["o"][pos].reshape(M, k, H).float()
+    out["y"] = (w[..., None] * o).sum(1).to(dt)
+    if s["backward"]:
+        dy = s["dy"].float()
+        out["do"] = torch.where(there, w.reshape(-1)[perm][:, None] * dy[perm // k], 0).to(dt)
+        out["dw"] = torch.where(kept.reshape(M, k), (o * dy[:, None]).sum(-1), 0)
+        dxs = torch.where(kept[:, None], s["dxs"][pos].float(), 0)
+        out["dx"] = dxs.reshape(M, k, H).sum(1).to(dt)
+    return out
+
+
+def _plain(s):
+    op = s["op"]
+    if op == "quantize":
+        return _rounded(_columns(s["x"]) if s["transpose"] else s["x"]).to(s["x"].dtype)
+    if op == "linear":
+        return (_rounded(s["x"]) @ _values(s["codes"], s["scales"]).t()).to(s["x"].dtype)
+    if op == "train":
+        x, w, dy = s["x"], s["w"], s["dy"]
+        y = _rounded(x) @ _rounded(w).t()
+        dx = _rounded(dy) @ _rounded(_columns(w)).t()
+        dw = _rounded(_columns(dy)) @ _rounded(_columns(x)).t()
+        return {"y": y.to(x.dtype), "dx": dx.to(x.dtype), "dw": dw}
+    return _plain_grouped(s) if op == "grouped" else _plain_dispatch(s)
+
+
+# ---------------------------------------------------------------- the library
+
+def _own(s):
+    from bit_weight_only_amd import lbq
+
+    op = s["op"]
+    if op == "quantize":
+        return lbq.mx_dequantize(lbq.mx_quantize(s["x"], transpose=s["transpose"]), s["x"].dtype)
+    if op == "linear":
+        return lbq.mx_linear_forward(lbq.MxTensor(s["codes"], s["scales"]), s["x"])
+    if op == "train":
+        x, w, dy = s["x"], s["w"], s["dy"]
+        y = lbq.mx_matmul(lbq.mx_quantize(x), lbq.mx_quantize(w), x.dtype)
+        dx = lbq.mx_matmul(lbq.mx_quantize(dy), lbq.mx_quantize(w, transpose=True), x.dtype)
+        dw = lbq.mx_matmul(lbq.mx_quantize(dy, transpose=True), lbq.mx_quantize(x, transpose=True), torch.float32)
+        return {"y": y, "dx": dx, "dw": dw}
+    if op == "grouped":
+        w = lbq.MxTensor(s["codes"], s["scales"])
+        return lbq.mx_grouped_forward(w, s["E"], s["x"], s["offsets"], s["perm"], s["top_k"])
+    counts, offsets, perm, pos = lbq.moe_sort(s["ids"], s["E"])
+    out = {"offsets": offsets, "pos": pos}
+    out["xs"] = lbq.moe_gather(s["x"], offsets, perm, s["top_k"], out=s["xs"])
+    out["y"] = lbq.moe_combine(s["o"], pos, s["weights"])
+    if s["backward"]:
+        out["do"], out["dw"] = lbq.moe_combine_backward(s["dy"], s["o"], pos, s["weights"], d_o=s["do"])
+        out["dx"] = lbq.moe_gather_backward(s["dxs"], pos)
+    return out
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ---------------------------------------------------------------- floors and 64 bits
+
+def _mx_bytes(rows, cols):
+    return rows * cols // 2 + rows * cols // 32
+
+
+def work(case):
+    op = case["op"]
+    if op == "quantize":
+        R, C = case["rows"], case["cols"]
+        out = C * (-(-R // 128) * 128) if case["transpose"] else R * C
+        return {"bytes": (R * C + out) * SIZE[case["dtype"]], "flops": 3 * R * C}
+    M = case["M"]
+    if op == "linear":
+        K, N, z = case["K"], case["N"], SIZE[case["dtype"]]
+        return {"bytes": _mx_bytes(N, K) + M * (K + N) * z, "flops": 2 * M * N * K}
+    if op == "train":
+        K, N, z = case["K"], case["N"], SIZE[case["dtype"]]
+        return {"bytes": (2 * M * K + 2 * M * N + N * K) * z + N * K * 4, "flops": 6 * M * N * K}
+    T, z = M * case["top_k"], SIZE[case["dtype"]]
+    if op == "grouped":
+        E, K, N = case["E"], case["K"], case["N"]
+        seen = E * (1 - (1 - case["top_k"] / E) ** M)     # experts that get a row
+        return {"bytes": int(seen * _mx_bytes(N, K)) + M * K * z + T * N * z + 4 * (T + E + 1), "flops": 2 * T * N * K}
+    H, kept = case["H"], int(T * (1 - case["drop"]))
+    rows = 2 * M + 2 * kept                      # x and y; xs and o
+    flops = 2 * kept * H
+    if case["backward"]:
+        rows += 2 * M + 2 * kept                 # dy and dx; do and dxs (o is counted above)
+        flops += 4 * kept * H
+    return {"bytes": rows * H * z + T * 16, "flops": flops}
+
+
+def _exact_round(x):
+    """x [R][C] after quantisation, in 64 bits: each element's nearest value, by its distance to all of them."""
+    v = x.double().reshape(x.shape[0], -1, 32)
+    m = v.abs().amax(-1, keepdim=True)
+    e = torch.floor(torch.log2(m))
+    e = torch.where(torch.exp2(e) > m, e - 1, torch.where(torch.exp2(e + 1) <= m, e + 1, e))
+    s = torch.exp2(torch.where(m > 0, e - 2, torch.zeros_like(m)).clamp(-127, 125))
+    u = v / s
+    # even numbers first: of two that are equally near the even one is taken
+    grid = u.new_tensor([E2M1[i] for i in (0, 2, 4, 6, 1, 3, 5, 7)])
+    at = grid[(u.abs()[..., None] - grid).abs().argmin(-1)]
+    return (torch.sign(u) * at * s).reshape(x.shape)
+
+
+def _exact_values(codes, scales):
+    n = torch.stack([codes % 16, codes // 16], -1).reshape(codes.shape[0], -1).long()
+    sign, exponent, mantissa = 1.0 - 2.0 * (n // 8), (n // 2) % 4, n % 2
+    v = sign * torch.where(exponent > 0, torch.exp2(exponent - 1.0).double() * (1 + 0.5 * mantissa), 0.5 * mantissa)
+    s = torch.exp2(scales.double() - 127).permute(1, 0, 2).reshape(codes.shape[0], -1)
+    return v * s.repeat_interleave(32, 1)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "quantize":
+        if s["x"].numel() > 1 << 28:
+            return None
+        x = s["x"].double()
+        if case["transpose"]:
+            x = torch.cat([x, x.new_zeros(-x.shape[0] % 128, x.shape[1])]).t()
+        return _exact_round(x)
+    if op == "linear":
+        return _exact_round(s["x"]) @ _exact_values(s["codes"], s["scales"]).t()
+    if op == "train":
+        def pad(a):
+            return torch.cat([a, a.new_zeros(-a.shape[0] % 128, a.shape[1])]).t()
+        x, w, dy = s["x"], s["w"], s["dy"]
+        return {"y": _exact_round(x) @ _exact_round(w).t(), "dx": _exact_round(dy) @ _exact_round(pad(w)).t(),
+                "dw": _exact_round(pad(dy)) @ _exact_round(pad(x)).t()}
+    if op == "grouped":
+        N, x = case["N"], _exact_round(s["x"])
+        y = x.new_zeros(case["M"] * case["top_k"], N)
+        ends = s["offsets"].tolist()
+        for e in range(case["E"]):
+            rows = (s["perm"][ends[e]:ends[e + 1]] // case["top_k"]).long()
+            if len(rows):
+                w = _exact_values(s["codes"][e * N:(e + 1) * N], s["scales"][:, e * N:(e + 1) * N])
+                y[ends[e]:ends[e + 1]] = x[rows] @ w.t()
+        return y
+    M, k, H = case["M"], case["top_k"], case["H"]
+    w = s["weights"].double()
+    flat = s["ids"].reshape(-1).tolist()
+    order = sorted((a for a, i in enumerate(flat) if i >= 0), key=lambda a: flat[a])   # stable
+    a = torch.tensor(order, dtype=torch.long, device="cuda")
+    t, n = a // k, len(order)
+    out = {"offsets": None, "pos": None}
+    out["xs"] = torch.zeros(M * k, H, dtype=torch.double, device="cuda")
+    out["xs"][:n] = s["x"].double()[t]
+    wa = w.reshape(-1)[a][:, None]
+    out["y"] = torch.zeros(M, H, dtype=torch.double, device="cuda").index_add_(0, t, wa * s["o"][:n].double())
+    if case["backward"]:
+        out["do"] = torch.zeros(M * k, H, dtype=torch.double, device="cuda")
+        out["do"][:n] = wa * s["dy"].double()[t]
+        out["dw"] = torch.zeros(M * k, dtype=torch.double, device="cuda")
+        out["dw"][a] = (s["o"][:n].double() * s["dy"].double()[t]).sum(-1)
+        out["dw"] = out["dw"].reshape(M, k)
+        out["dx"] = torch.zeros(M, H, dtype=torch.double, device="cuda").index_add_(0, t, s["dxs"][:n].double())
+    return out
