@@ -290,7 +290,7 @@ def _own(s):
         return lbq.mx_grouped_forward(w, s["E"], s["x"], s["offsets"], s["perm"], s["top_k"])
     counts, offsets, perm, pos = lbq.moe_sort(s["ids"], s["E"])
     out = {"offsets": offsets, "pos": pos}
-    out["xs"] = lbq.moe_gather(s["x"], offsets, perm, s["top_k"], out=s["xs"])
+    out["xs"] = lbq.moe_gather(s["x"], pos, out=s["xs"])
     out["y"] = lbq.moe_combine(s["o"], pos, s["weights"])
     if s["backward"]:
         out["do"], out["dw"] = lbq.moe_combine_backward(s["dy"], s["o"], pos, s["weights"], d_o=s["do"])
