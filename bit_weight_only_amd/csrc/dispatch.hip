@@ -1,0 +1,310 @@
+// Tokens sorted by expert and back: the counting sort of (token, slot) picks,
+// the gather of token rows into sorted order, the weighted combine, and the
+// gradients of both. Nothing uses atomics on floating-point data and every sum
+// has a fixed order, so repeated calls give identical bits.
+#include "device.h"
+#include "kernels.h"
+#include "mxfp4.h"
+
+#include <algorithm>
+
+namespace lbq {
+
+namespace {
+
+using namespace mxfp4;
+
+// ------------------------------------------------------------------ sort
+
+constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
+constexpr int kMaxBlocks = 64;
+
+// Assignments per workgroup: whole 1024-chunks, at most kMaxBlocks workgroups.
+int sort_chunk(int n) {
+  const int per = (n + kMaxBlocks - 1) / kMaxBlocks;
+  return std::max(16 * 1024, (per + kSortThreads - 1) / kSortThreads * kSortThreads);
+}
+
+__device__ __forceinline__ int expert_of(const int32_t *ids, int a, int end, int E) {
+  if (a >= end) return -1;
+  const int e = ids[a];
+  return e >= 0 && e < E ? e : -1;
+}
+
+// Counts of one workgroup's chunk (integer sums: the order does not matter).
+__global__ void __launch_bounds__(kSortThreads) moe_hist_kernel(const int32_t *__restrict__ ids, int n, int E, int chunk,
+                                                                int32_t *__restrict__ hist) {
+  __shared__ int32_t cnt[kMoeMaxExperts];
+  for (int i = threadIdx.x; i < E; i += kSortThreads) cnt[i] = 0;
+  __syncthreads();
+  const int lo = blockIdx.x * chunk, hi = min(n, lo + chunk);
+  for (int a = lo + threadIdx.x; a < hi; a += kSortThreads) {
+    const int e = expert_of(ids, a, hi, E);
+    if (e >= 0) atomicAdd(&cnt[e], 1);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < E; i += kSortThreads) hist[static_cast<size_t>(blockIdx.x) * E + i] = cnt[i];
+}
+
+// Places one workgroup's chunk. Wave w owns the w-th sixteenth of the chunk and
+// walks it in order, 64 picks at a time: a pick's place is its expert's start
+// plus the picks of that expert before it (other workgroups' from hist, other
+// waves' from the LDS counts, its own wave's earlier ones from the running
+// count, and among the 64 by a ballot over the bits of the expert number).
+// hist is null where one workgroup holds every pick.
+__global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int chunk,
+                                                                 const int32_t *__restrict__ hist,
+                                                                 int32_t *__restrict__ counts,
+                                                                 int32_t *__restrict__ offsets,
+                                                                 int32_t *__restrict__ perm, int32_t *__restrict__ pos) {
+  __shared__ int32_t s_cnt[kSortWaves * kMoeMaxExperts];   // per (wave, expert): count, then the running place
+  __shared__ int32_t s_wave[kSortWaves];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lo = blockIdx.x * chunk, hi = min(n, lo + chunk);
+  const int per_wave = (chunk + kSortWaves - 1) / kSortWaves;
+  const int w_lo = min(hi, lo + wave * per_wave), w_hi = min(hi, w_lo + per_wave);
+  for (int i = tid; i < kSortWaves * E; i += kSortThreads) s_cnt[i] = 0;
+  __syncthreads();
+  for (int a = w_lo + lane; a < w_hi; a += 64) {
+    const int e = expert_of(ids, a, w_hi, E);
+    if (e >= 0) atomicAdd(&s_cnt[wave * E + e], 1);
+  }
+  __syncthreads();
+  // thread e: the expert's picks in all, and those before this workgroup
+  int total = 0, before = 0;
+  if (tid < E) {
+    if (hist) {
+      for (int b = 0; b < static_cast<int>(gridDim.x); ++b) {
+        const int c = hist[static_cast<size_t>(b) * E + tid];
+        if (b < static_cast<int>(blockIdx.x)) before += c;
+        total += c;
+      }
+    } else {
+      for (int w = 0; w < kSortWaves; ++w) total += s_cnt[w * E + tid];
+    }
+  }
+  // exclusive scan of the totals over the experts (one per thread)
+  int incl = total;
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(incl, d);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) s_wave[wave] = incl;
+  __syncthreads();
+  int base = 0, all = 0;
+  for (int w = 0; w < kSortWaves; ++w) {
+    if (w < wave) base += s_wave[w];
+    all += s_wave[w];
+  }
+  const int start = base + incl - total;
+  if (tid < E) {
+    int run = start + before;
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = s_cnt[w * E + tid];
+      s_cnt[w * E + tid] = run;
+      run += c;
+    }
+    if (blockIdx.x == 0) {
+      counts[tid] = total;
+      offsets[tid] = start;
+      if (tid == 0) offsets[E] = all;
+    }
+  }
+  __syncthreads();
+  const int bits = 32 - __builtin_clz(max(E - 1, 1));
+  for (int a0 = w_lo; a0 < w_hi; a0 += 64) {
+    const int a = a0 + lane;
+    const int e = expert_of(ids, a, w_hi, E);
+    uint64_t same = __ballot(e >= 0);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t bal = __ballot((e >> b) & 1);
+      same &= ((e >> b) & 1) ? bal : ~bal;
+    }
+    if (e >= 0) {
+      const int rank = __builtin_popcountll(same & ((1ull << lane) - 1));
+      const int p = s_cnt[wave * E + e] + rank;
+      // the last of the equal lanes moves the running place on (the reads
+      // above are done: a wave's LDS operations complete in order)
+      __builtin_amdgcn_wave_barrier();
+      if ((same >> lane) == 1) s_cnt[wave * E + e] = p + 1;
+      perm[p] = a;
+      pos[a] = p;
+    } else if (a < w_hi) {
+      pos[a] = -1;
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  // places behind the last pick
+  for (int a = lo + tid; a < hi; a += kSortThreads)
+    if (a >= all) perm[a] = -1;
+}
+
+// ------------------------------------------------------------------ rows
+
+// V values of a row at once: eight (16-byte vectors) where rows are whole
+// vectors, else one.
+template <int DT, int V>
+struct Row {
+  using T = typename Elem<DT>::type;
+  T v[V];
+  static __device__ __forceinline__ Row load(const void *p, size_t at) {
+    Row r;
+    if constexpr (V == 1) {
+      r.v[0] = static_cast<const T *>(p)[at];
+    } else {
+      constexpr int kVecs = V * sizeof(T) / 16;
+      uint4 *q = reinterpret_cast<uint4 *>(r.v);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) q[i] = reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + at)[i];
+    }
+    return r;
+  }
+  __device__ __forceinline__ void store(void *p, size_t at) const {
+    if constexpr (V == 1) {
+      static_cast<T *>(p)[at] = v[0];
+    } else {
+      constexpr int kVecs = V * sizeof(T) / 16;
+      const uint4 *q = reinterpret_cast<const uint4 *>(v);
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4 *>(static_cast<T *>(p) + at)[i] = q[i];
+    }
+  }
+};
+
+constexpr int kRowThreads = 256;
+
+// out[pos[t][j]] = x[t]: each token row is read once and written top_k times.
+template <int DT, int V>
+__global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const void *__restrict__ x, int M, int H, int T,
+                                                                 const int32_t *__restrict__ pos, int top_k,
+                                                                 void *__restrict__ out) {
+  const int t = blockIdx.x;
+  for (int c = (blockIdx.y * kRowThreads + threadIdx.x) * V; c < H; c += gridDim.y * kRowThreads * V) {
+    const auto r = Row<DT, V>::load(x, static_cast<size_t>(t) * H + c);
+    for (int j = 0; j < top_k; ++j) {
+      const int p = pos[static_cast<size_t>(t) * top_k + j];
+      if (p >= 0 && p < T) r.store(out, static_cast<size_t>(p) * H + c);
+    }
+  }
+}
+
+// y[t] = sum_j w[t][j] o[pos[t][j]] in fp32, slot order; w null: all ones.
+template <int DT, int V>
+__global__ void __launch_bounds__(kRowThreads) moe_combine_kernel(const void *__restrict__ o, int T, int H,
+                                                                  const int32_t *__restrict__ pos,
+                                                                  const float *__restrict__ w, int top_k,
+                                                                  void *__restrict__ y) {
+  const int t = blockIdx.x;
+  for (int c = (blockIdx.y * kRowThreads + threadIdx.x) * V; c < H; c += gridDim.y * kRowThreads * V) {
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int j = 0; j < top_k; ++j) {
+      const int p = pos[static_cast<size_t>(t) * top_k + j];
+      if (p < 0 || p >= T) continue;
+      const float wj = w ? w[static_cast<size_t>(t) * top_k + j] : 1.f;
+      const auto r = Row<DT, V>::load(o, static_cast<size_t>(p) * H + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = fmaf(wj, to_f32<DT>(r.v[i]), acc[i]);
+    }
+    Row<DT, V> r;
+#pragma unroll
+    for (int i = 0; i < V; ++i) r.v[i] = from_f32<DT>(acc[i]);
+    r.store(y, static_cast<size_t>(t) * H + c);
+  }
+}
+
+// d_o[pos[t][j]] = w[t][j] dy[t];  d_w[t][j] = <dy[t], o[pos[t][j]]>, summed per
+// thread over its columns, then over the wave, then over the waves in order.
+// d_o may be o (each value is read before its place is written).
+template <int DT, int V>
+__global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(
+    const void *__restrict__ dy, const void *o, int T, int H, const int32_t *__restrict__ pos,
+    const float *__restrict__ w, int top_k, void *d_o, float *__restrict__ d_w) {
+  constexpr int kWaves = kRowThreads / 64;
+  __shared__ float part[kWaves];
+  const int t = blockIdx.x;
+  for (int j = 0; j < top_k; ++j) {
+    const size_t a = static_cast<size_t>(t) * top_k + j;
+    const int p = pos[a];
+    const bool there = p >= 0 && p < T;
+    float dot = 0.f;
+    if (there) {
+      const float wj = w[a];
+      for (int c = threadIdx.x * V; c < H; c += kRowThreads * V) {
+        const auto g = Row<DT, V>::load(dy, static_cast<size_t>(t) * H + c);
+        const auto r = Row<DT, V>::load(o, static_cast<size_t>(p) * H + c);
+        Row<DT, V> d;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float gi = to_f32<DT>(g.v[i]);
+          dot = fmaf(gi, to_f32<DT>(r.v[i]), dot);
+          d.v[i] = from_f32<DT>(wj * gi);
+        }
+        d.store(d_o, static_cast<size_t>(p) * H + c);
+      }
+    }
+    for (int d = 32; d > 0; d /= 2) dot += __shfl_xor(dot, d);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = dot;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      float sum = 0.f;
+      for (int i = 0; i < kWaves; ++i) sum += part[i];
+      d_w[a] = sum;
+    }
+    __syncthreads();
+  }
+}
+
+unsigned chunks(int H, int v) { return static_cast<unsigned>(std::min((H + kRowThreads * v - 1) / (kRowThreads * v), 64)); }
+
+}  // namespace
+
+size_t moe_sort_ws_bytes(int n, int E) {
+  const int chunk = sort_chunk(n);
+  return n <= chunk ? 0 : static_cast<size_t>((n + chunk - 1) / chunk) * E * 4;
+}
+
+hipError_t launch_moe_sort(const int32_t *ids, int n, int E, int32_t *counts, int32_t *offsets, int32_t *perm,
+                           int32_t *pos, void *ws, hipStream_t s) {
+  const int chunk = sort_chunk(n);
+  const int blocks = std::max(1, (n + chunk - 1) / chunk);
+  int32_t *hist = blocks > 1 ? static_cast<int32_t *>(ws) : nullptr;
+  if (hist) hipLaunchKernelGGL(moe_hist_kernel, dim3(blocks), dim3(kSortThreads), 0, s, ids, n, E, chunk, hist);
+  hipLaunchKernelGGL(moe_place_kernel, dim3(blocks), dim3(kSortThreads), 0, s, ids, n, E, chunk, hist, counts, offsets,
+                     perm, pos);
+  return hipGetLastError();
+}
+
+// eight values a lane where every row starts on a 16-byte boundary
+#define LBQ_ROWS(KERNEL, GRIDY, ...)                                                                                  \
+  do {                                                                                                                \
+    const bool vec = H % 8 == 0;                                                                                      \
+    const dim3 grid(static_cast<unsigned>(M), GRIDY ? chunks(H, vec ? 8 : 1) : 1);                                    \
+    if (dtype == kF16 && vec) hipLaunchKernelGGL((KERNEL<kF16, 8>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);      \
+    else if (dtype == kF16) hipLaunchKernelGGL((KERNEL<kF16, 1>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);        \
+    else if (dtype == kBF16 && vec) hipLaunchKernelGGL((KERNEL<kBF16, 8>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__); \
+    else if (dtype == kBF16) hipLaunchKernelGGL((KERNEL<kBF16, 1>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);      \
+    else if (vec) hipLaunchKernelGGL((KERNEL<kF32, 8>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);                  \
+    else hipLaunchKernelGGL((KERNEL<kF32, 1>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);                           \
+  } while (0)
+
+hipError_t launch_moe_gather(const void *x, int dtype, int M, int H, int T, const int32_t *pos, int top_k, void *out,
+                             hipStream_t s) {
+  LBQ_ROWS(moe_gather_kernel, true, x, M, H, T, pos, top_k, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const void *o, int dtype, int T, int H, const int32_t *pos, const float *weights, int M,
+                              int top_k, void *y, hipStream_t s) {
+  LBQ_ROWS(moe_combine_kernel, true, o, T, H, pos, weights, top_k, y);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_backward(const void *dy, const void *o, int dtype, int T, int H, const int32_t *pos,
+                                       const float *weights, int M, int top_k, void *d_o, float *d_w, hipStream_t s) {
+  LBQ_ROWS(moe_combine_backward_kernel, false, dy, o, T, H, pos, weights, top_k, d_o, d_w);
+  return hipGetLastError();
+}
+
+}  // namespace lbq

@@ -186,4 +186,41 @@ constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxAssignments = 1 << 20;
 constexpr int kMoeMaxTopK = 32;
 
+// MXFP4 tensors (mxfp4.hip): quantisation of x [rows][cols] along the columns
+// of each row, or of x^T along x's rows (padded with zeros to 128), and the
+// values back. dtype: lbq_dtype.
+hipError_t launch_mx_quantize(const void *x, int dtype, int rows, int cols, void *codes, void *scales, hipStream_t s);
+hipError_t launch_mx_quantize_t(const void *x, int dtype, int rows, int cols, void *codes, void *scales,
+                                hipStream_t s);
+hipError_t launch_mx_dequantize(const void *codes, const void *scales, int rows, int cols, void *out, int dtype,
+                                hipStream_t s);
+
+// Products of MXFP4 tensors (mx_gemm.hip): y [M][N] = A B^T. E = 0: A has M
+// rows, B has N. E > 0: B holds E blocks of N rows; list row i of y belongs to
+// the expert whose range [offsets[e], offsets[e + 1]) holds i and takes A's row
+// perm[i] / top_k (perm null: i); rows from offsets[E] on are not written.
+struct MxGemm {
+  const void *a_codes, *a_scales, *b_codes, *b_scales;
+  void *y;
+  int dtype;
+  int a_rows, M, N, K;
+  const int32_t *offsets, *perm;
+  int E, top_k;
+  void *scratch;   // mx_gemm_scratch_bytes of it
+};
+size_t mx_gemm_scratch_bytes(const MxGemm &p);
+hipError_t launch_mx_gemm(const MxGemm &p, hipStream_t s);
+
+// Expert dispatch (dispatch.hip). The sort of n picks; the row moves over
+// M tokens of top_k picks with pos [M][top_k] places in a list of T rows.
+size_t moe_sort_ws_bytes(int n, int E);
+hipError_t launch_moe_sort(const int32_t *ids, int n, int E, int32_t *counts, int32_t *offsets, int32_t *perm,
+                           int32_t *pos, void *ws, hipStream_t s);
+hipError_t launch_moe_gather(const void *x, int dtype, int M, int H, int T, const int32_t *pos, int top_k, void *out,
+                             hipStream_t s);
+hipError_t launch_moe_combine(const void *o, int dtype, int T, int H, const int32_t *pos, const float *weights, int M,
+                              int top_k, void *y, hipStream_t s);
+hipError_t launch_moe_combine_backward(const void *dy, const void *o, int dtype, int T, int H, const int32_t *pos,
+                                       const float *weights, int M, int top_k, void *d_o, float *d_w, hipStream_t s);
+
 }  // namespace lbq

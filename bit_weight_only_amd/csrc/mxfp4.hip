@@ -1,0 +1,255 @@
+// MXFP4 tensors: quantisation along rows or columns, and the values back.
+//
+// A block is 32 values along the axis a product will sum over. With m the
+// block's largest magnitude, e = clamp(floor(log2 m) - 2, -127, 125) (-127 for
+// m = 0) and a value is held as e2m1(x / 2^e): round to nearest, ties to the
+// even code, magnitudes past 6 saturated (the largest is below 8). The scale
+// byte is e + 127 (E8M0). A block with a NaN or an infinity has byte 255 and
+// zero codes; everything it meets in a product is NaN.
+//
+// Exact throughout: the division is by a power of two inside the conversion
+// instruction (v_cvt_scalef32_pk_fp4_*: rounds once, saturates, keeps signs,
+// takes the subnormal scale 2^-127), so codes are bit-equal to the definition.
+//
+// Bound: HBM. 16-bit input moves 2 + 17/32 bytes per value and a lane spends
+// about two instructions per value.
+#include "device.h"
+#include "kernels.h"
+#include "mxfp4.h"
+
+namespace lbq {
+
+namespace {
+
+using namespace mxfp4;
+
+constexpr int kThreads = 256;
+
+// Magnitude bits of eight values as 32-bit patterns that order like the
+// magnitudes, infinities and NaN last; and the fp32 exponent field of one.
+template <int DT>
+struct In;
+template <>
+struct In<kF16> {
+  uint4 v;
+  static __device__ __forceinline__ In load(const void *p, size_t unit) {
+    return In{static_cast<const uint4 *>(p)[unit]};
+  }
+  __device__ __forceinline__ uint32_t mag() const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
+    return m;
+  }
+  static __device__ __forceinline__ bool finite(uint32_t m) { return m < 0x7C00u; }
+  static __device__ __forceinline__ uint32_t exponent(uint32_t m) { return __float_as_uint(f16_bits_to_f32(m)) >> 23; }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t o = 0;
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.x), s, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.y), s, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.z), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.w), s, 3);
+  }
+};
+template <>
+struct In<kBF16> {
+  uint4 v;
+  static __device__ __forceinline__ In load(const void *p, size_t unit) {
+    return In{static_cast<const uint4 *>(p)[unit]};
+  }
+  __device__ __forceinline__ uint32_t mag() const { return In<kF16>{v}.mag(); }
+  static __device__ __forceinline__ bool finite(uint32_t m) { return m < 0x7F80u; }
+  static __device__ __forceinline__ uint32_t exponent(uint32_t m) { return m >> 7; }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t o = 0;
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.x), s, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.y), s, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.z), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.w), s, 3);
+  }
+};
+template <>
+struct In<kF32> {
+  float4_t a, b;
+  static __device__ __forceinline__ In load(const void *p, size_t unit) {
+    return In{static_cast<const float4_t *>(p)[2 * unit], static_cast<const float4_t *>(p)[2 * unit + 1]};
+  }
+  __device__ __forceinline__ uint32_t mag() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m = max(m, max(__float_as_uint(a[i]) & 0x7FFFFFFFu, __float_as_uint(b[i]) & 0x7FFFFFFFu));
+    return m;
+  }
+  static __device__ __forceinline__ bool finite(uint32_t m) { return m < 0x7F800000u; }
+  static __device__ __forceinline__ uint32_t exponent(uint32_t m) { return m >> 23; }
+  __device__ __forceinline__ uint32_t codes(float s) const {
+    uint32_t o = 0;
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, a[0], a[1], s, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, a[2], a[3], s, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, b[0], b[1], s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, b[2], b[3], s, 3);
+  }
+};
+
+// The scale byte of a block whose largest magnitude pattern is m. Values below
+// fp32's normal range have exponent field 0 and get byte 0 like every block
+// whose exponent clamps at -127.
+template <int DT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
+  return In<DT>::finite(m) ? static_cast<uint32_t>(max(static_cast<int>(In<DT>::exponent(m)) - 2, 0)) : 255u;
+}
+
+// ------------------------------------------------------------------ along rows
+
+// Four lanes per block, eight values each: sixteen lanes make one 128-group of
+// one row, whose four scale bytes leave as one word. Unit u is eight values;
+// group u / 16.
+template <int DT>
+__global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const void *__restrict__ x, uint32_t *__restrict__ codes,
+                                                               uint32_t *__restrict__ scales, int rows,
+                                                               uint32_t groups, long units) {
+  const long step = static_cast<long>(gridDim.x) * kThreads;
+  // units is a multiple of 16, so the sixteen lanes of a group stay together
+  for (long u = static_cast<long>(blockIdx.x) * kThreads + threadIdx.x; u < units; u += step) {
+    const In<DT> in = In<DT>::load(x, static_cast<size_t>(u));
+    uint32_t m = in.mag();
+    m = max(m, xor_lane_u32<1>(m));
+    m = max(m, xor_lane_u32<2>(m));
+    const uint32_t byte = scale_byte<DT>(m);
+    const uint32_t c = in.codes(scale_value(byte));
+    codes[u] = byte == 255u ? 0u : c;
+    uint32_t word = byte << (8 * ((threadIdx.x >> 2) & 3));
+    word |= xor_lane_u32<4>(word);
+    word |= xor_lane_u32<8>(word);
+    if ((threadIdx.x & 15) == 0) {
+      const uint32_t gi = static_cast<uint32_t>(u >> 4), row = gi / groups;   // fewer than 2^31 groups
+      scales[static_cast<size_t>(gi - row * groups) * rows + row] = word;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ along columns
+
+// The transposed tensor: blocks of 32 rows of x. A workgroup takes 128 rows by
+// 64 columns of x through LDS; a thread then owns one column's block of 32.
+// Rows past the end count as zeros.
+constexpr int kTileCols = 64;
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) mx_quantize_t_kernel(const void *__restrict__ x, uint4 *__restrict__ codes,
+                                                                 uint32_t *__restrict__ scales, int rows, int cols,
+                                                                 int row_groups) {
+  using T = typename Elem<DT>::type;
+  __shared__ T tile[128][kTileCols + (DT == kF32 ? 1 : 2)];
+  const int c0 = blockIdx.x * kTileCols;
+  const int g = blockIdx.y;
+  const T *src = static_cast<const T *>(x);
+  for (int i = threadIdx.x; i < 128 * kTileCols; i += kThreads) {
+    const int r = i / kTileCols, c = i % kTileCols;
+    const long row = static_cast<long>(g) * 128 + r;
+    tile[r][c] = row < rows && c0 + c < cols ? src[row * cols + c0 + c] : T(0);
+  }
+  __syncthreads();
+  const int c = threadIdx.x & 63, b = threadIdx.x >> 6;   // one wave per block of 32 rows
+  __shared__ uint8_t bytes[4][kTileCols];
+  uint32_t m = 0;
+  float v[32];
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    v[i] = to_f32<DT>(tile[32 * b + i][c]);
+    m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+  }
+  const uint32_t byte = scale_byte<kF32>(m);
+  const float s = scale_value(byte);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t o = 0;
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i], v[8 * i + 1], s, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i + 2], v[8 * i + 3], s, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i + 4], v[8 * i + 5], s, 2);
+    w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i + 6], v[8 * i + 7], s, 3);
+    if (byte == 255u) w[i] = 0;
+  }
+  if (c0 + c < cols)
+    codes[(static_cast<long>(c0 + c) * row_groups + g) * 4 + b] = make_uint4(w[0], w[1], w[2], w[3]);
+  bytes[b][c] = static_cast<uint8_t>(byte);
+  __syncthreads();
+  if (b == 0 && c0 + c < cols)
+    scales[static_cast<long>(g) * cols + c0 + c] = bytes[0][c] | (bytes[1][c] << 8) | (bytes[2][c] << 16) |
+                                                   (static_cast<uint32_t>(bytes[3][c]) << 24);
+}
+
+// ------------------------------------------------------------------ values
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads) mx_dequantize_kernel(const uint32_t *__restrict__ codes,
+                                                                 const uint32_t *__restrict__ scales,
+                                                                 void *__restrict__ out, int rows, uint32_t groups,
+                                                                 long units) {
+  const long step = static_cast<long>(gridDim.x) * kThreads;
+  for (long u = static_cast<long>(blockIdx.x) * kThreads + threadIdx.x; u < units; u += step) {
+    const uint32_t gi = static_cast<uint32_t>(u >> 4), row = gi / groups;
+    const uint32_t word = scales[static_cast<size_t>(gi - row * groups) * rows + row];
+    const uint32_t byte = (word >> (8 * ((u >> 2) & 3))) & 0xFFu;
+    const float s = byte == 255u ? __uint_as_float(0x7FC00000u) : scale_value(byte);
+    const uint32_t c = codes[u];
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = s * e2m1_value((c >> (4 * i)) & 15u);
+    store8<DT>(out, static_cast<size_t>(u), v);
+  }
+}
+
+int grid_of(long units) {
+  const long g = (units + kThreads - 1) / kThreads;
+  return static_cast<int>(g < 16384 ? g : 16384);
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const void *x, int dtype, int rows, int cols, void *codes, void *scales, hipStream_t s) {
+  const long units = static_cast<long>(rows) * cols / 8;
+  const int grid = grid_of(units), groups = cols / kGroup;
+  uint32_t *c = static_cast<uint32_t *>(codes), *e = static_cast<uint32_t *>(scales);
+  if (dtype == kF16)
+    hipLaunchKernelGGL(mx_quantize_kernel<kF16>, dim3(grid), dim3(kThreads), 0, s, x, c, e, rows, groups, units);
+  else if (dtype == kBF16)
+    hipLaunchKernelGGL(mx_quantize_kernel<kBF16>, dim3(grid), dim3(kThreads), 0, s, x, c, e, rows, groups, units);
+  else
+    hipLaunchKernelGGL(mx_quantize_kernel<kF32>, dim3(grid), dim3(kThreads), 0, s, x, c, e, rows, groups, units);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_quantize_t(const void *x, int dtype, int rows, int cols, void *codes, void *scales,
+                                hipStream_t s) {
+  const int rg = static_cast<int>((static_cast<long>(rows) + 127) / 128);
+  const dim3 grid((cols + kTileCols - 1) / kTileCols, rg);
+  uint4 *c = static_cast<uint4 *>(codes);
+  uint32_t *e = static_cast<uint32_t *>(scales);
+  if (dtype == kF16)
+    hipLaunchKernelGGL(mx_quantize_t_kernel<kF16>, grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg);
+  else if (dtype == kBF16)
+    hipLaunchKernelGGL(mx_quantize_t_kernel<kBF16>, grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg);
+  else
+    hipLaunchKernelGGL(mx_quantize_t_kernel<kF32>, grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg);
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const void *codes, const void *scales, int rows, int cols, void *out, int dtype,
+                                hipStream_t s) {
+  const long units = static_cast<long>(rows) * cols / 8;
+  const int grid = grid_of(units), groups = cols / kGroup;
+  const uint32_t *c = static_cast<const uint32_t *>(codes), *e = static_cast<const uint32_t *>(scales);
+  if (dtype == kF16)
+    hipLaunchKernelGGL(mx_dequantize_kernel<kF16>, dim3(grid), dim3(kThreads), 0, s, c, e, out, rows, groups, units);
+  else if (dtype == kBF16)
+    hipLaunchKernelGGL(mx_dequantize_kernel<kBF16>, dim3(grid), dim3(kThreads), 0, s, c, e, out, rows, groups, units);
+  else
+    hipLaunchKernelGGL(mx_dequantize_kernel<kF32>, dim3(grid), dim3(kThreads), 0, s, c, e, out, rows, groups, units);
+  return hipGetLastError();
+}
+
+}  // namespace lbq

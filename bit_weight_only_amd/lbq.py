@@ -32,6 +32,10 @@ EXPORTS = [
     "lbq_linear_forward_path", "lbq_linear_forward_timed", "lbq_moe_workspace", "lbq_moe_forward", "lbq_moe_route", "lbq_unpack_codes",
     "lbq_rotate", "lbq_linear_forward_noalloc", "lbq_stream_read", "lbq_gptq_factor",
     "lbq_pack_gptq", "lbq_moe_forward_path", "lbq_split_nibbles", "lbq_readout_workspace", "lbq_readout_screened",
+    "lbq_mx_bytes", "lbq_mx_quantize", "lbq_mx_quantize_t", "lbq_mx_dequantize", "lbq_mx_matmul_workspace",
+    "lbq_mx_matmul", "lbq_mx_linear_workspace", "lbq_mx_linear_forward", "lbq_mx_grouped_workspace",
+    "lbq_mx_grouped_forward", "lbq_moe_sort_workspace", "lbq_moe_sort", "lbq_moe_gather", "lbq_moe_gather_backward",
+    "lbq_moe_combine", "lbq_moe_combine_backward",
 ]
 
 
@@ -58,6 +62,11 @@ class Readout(ctypes.Structure):
     _fields_ = [("K", ctypes.c_int32), ("N", ctypes.c_int32), ("hi_planes", ctypes.c_void_p),
                 ("lo_planes", ctypes.c_void_p), ("hi_meta", ctypes.c_void_p), ("meta", ctypes.c_void_p),
                 ("signs", ctypes.c_void_p)]
+
+
+class Mx(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -98,6 +107,25 @@ def lib() -> ctypes.CDLL:
         L.lbq_readout_workspace.argtypes = [ctypes.POINTER(Readout), c_i32, c_i32, p_sz]
         L.lbq_readout_screened.argtypes = [ctypes.POINTER(Readout), c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_sz,
                                            c_vp]
+        p_mx = ctypes.POINTER(Mx)
+        L.lbq_mx_bytes.argtypes = [c_i32, c_i32, p_sz, p_sz]
+        L.lbq_mx_quantize.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]
+        L.lbq_mx_quantize_t.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp]
+        L.lbq_mx_dequantize.argtypes = [p_mx, c_vp, c_i32, c_vp]
+        L.lbq_mx_matmul_workspace.argtypes = [p_mx, p_mx, p_sz]
+        L.lbq_mx_matmul.argtypes = [p_mx, p_mx, c_vp, c_i32, c_vp, c_sz, c_vp]
+        L.lbq_mx_linear_workspace.argtypes = [p_mx, c_i32, p_sz]
+        L.lbq_mx_linear_forward.argtypes = [p_mx, c_vp, c_i32, c_vp, c_i32, c_vp, c_sz, c_vp]
+        L.lbq_mx_grouped_workspace.argtypes = [p_mx, c_i32, c_i32, c_i32, p_sz]
+        L.lbq_mx_grouped_forward.argtypes = [p_mx, c_i32, c_vp, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_i32, c_vp, c_sz,
+                                             c_vp]
+        L.lbq_moe_sort_workspace.argtypes = [c_i32, c_i32, c_i32, p_sz]
+        L.lbq_moe_sort.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
+        L.lbq_moe_gather.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_vp]
+        L.lbq_moe_gather_backward.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_i32, c_i32, c_vp, c_vp]
+        L.lbq_moe_combine.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp]
+        L.lbq_moe_combine_backward.argtypes = [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp,
+                                               c_vp]
         for name in EXPORTS:
             if name != "lbq_status_string":
                 getattr(L, name).restype = c_i32
@@ -411,3 +439,327 @@ def moe_from_host(packed: dict, bits, signs_hidden, signs_ffn, hidden: int, ffn:
                      up(packed["dn_plane_off"].view(np.int64)), up(packed["dn_meta_off"].view(np.int64)),
                      up(packed["planes"]), up(packed["meta"]), up(np.asarray(signs_hidden, np.int8)),
                      up(np.asarray(signs_ffn, np.int8)))
+
+
+# ------------------------------------------------------------------ MXFP4 tensors, expert dispatch
+#
+# These take torch tensors as they are used in a program, so they check them:
+# one device, contiguous, the right type and shape (LbqError otherwise, nothing
+# launched). They run on the tensors' device whatever the current one is, on
+# the given stream or that device's current one; what they allocate belongs to
+# that stream.
+
+F16, BF16, F32 = 0, 1, 2
+_DTYPES: dict = {}
+
+
+def _dtype(t, where: str) -> int:
+    if not _DTYPES:
+        import torch
+
+        _DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+    code = _DTYPES.get(t)
+    if code is None:
+        raise LbqError(-8, f"{where}: {t}")
+    return code
+
+
+def _need(where: str, device, dtype, shape, *tensors):
+    """Every tensor is contiguous, on device, of this dtype and (where given) shape."""
+    for t in tensors:
+        if t.device != device or not t.is_cuda:
+            raise LbqError(-8, f"{where}: tensors on {t.device} and {device}")
+        if t.dtype != dtype:
+            raise LbqError(-8, f"{where}: {t.dtype} instead of {dtype}")
+        if not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
+            raise LbqError(-2, f"{where}: shape {tuple(t.shape)}, strides {t.stride()}")
+
+
+class _On:
+    """The device and stream of a call: entered around its allocations and its launch."""
+
+    def __init__(self, device, stream):
+        self.device, self.stream, self.guards = device, stream, None
+
+    def __enter__(self):
+        import torch
+
+        if self.stream is not None:
+            if self.stream.device != self.device:
+                raise LbqError(-8, f"stream on {self.stream.device}, tensors on {self.device}")
+            self.guards = [torch.cuda.stream(self.stream)]   # also makes its device the current one
+        elif torch.cuda.current_device() != self.device.index:
+            self.guards = [torch.cuda.device(self.device)]
+        if self.guards:
+            self.guards[0].__enter__()
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.guards:
+            self.guards[0].__exit__(*exc)
+
+
+def _workspace(ws, need: int, device, where: str):
+    import torch
+
+    if ws is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    if ws.device != device or not ws.is_contiguous():
+        raise LbqError(-5, where)
+    return ws
+
+
+def _bytes_of(t) -> int:
+    return t.numel() * t.element_size()
+
+
+class MxTensor:
+    """An MXFP4 tensor (see include/lbq.h): codes uint8 [rows][cols/2] and scales uint8 [cols/128][rows][4]."""
+
+    __slots__ = ("rows", "cols", "codes", "scales", "_t")
+
+    def __init__(self, codes, scales):
+        import torch
+
+        if codes.dim() != 2:
+            raise LbqError(-2, "MxTensor: codes are [rows][cols/2]")
+        self.rows, self.cols = codes.shape[0], 2 * codes.shape[1]
+        _need("MxTensor", codes.device, torch.uint8, None, codes)
+        _need("MxTensor", codes.device, torch.uint8, (self.cols // 128, self.rows, 4), scales)
+        self.codes, self.scales = codes, scales
+        self._t = Mx(self.rows, self.cols, codes.data_ptr(), scales.data_ptr())
+
+    @property
+    def struct(self) -> Mx:
+        return self._t
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def mx_quantize(x, transpose: bool = False, stream=None) -> MxTensor:
+    """lbq_mx_quantize (transpose: lbq_mx_quantize_t) of x [rows][cols] in float16, bfloat16 or float32."""
+    import torch
+
+    if x.dim() != 2:
+        raise LbqError(-2, "mx_quantize: x is [rows][cols]")
+    _need("mx_quantize", x.device, x.dtype, None, x)
+    dt = _dtype(x.dtype, "mx_quantize")
+    rows, cols = x.shape
+    tr, tc = (cols, -(-rows // 128) * 128) if transpose else (rows, cols)
+    if tc % 128 or tc == 0:
+        raise LbqError(-2, "mx_quantize: blocks run along a multiple of 128 values")
+    with _On(x.device, stream) as s:
+        codes = torch.empty((tr, tc // 2), dtype=torch.uint8, device=x.device)
+        scales = torch.empty((tc // 128, tr, 4), dtype=torch.uint8, device=x.device)
+        f = lib().lbq_mx_quantize_t if transpose else lib().lbq_mx_quantize
+        st = f(x.data_ptr(), dt, rows, cols, codes.data_ptr(), scales.data_ptr(), s)
+    _check(st, "lbq_mx_quantize_t" if transpose else "lbq_mx_quantize")
+    return MxTensor(codes, scales)
+
+
+def mx_dequantize(t: MxTensor, dtype, out=None, stream=None):
+    """lbq_mx_dequantize: the values of t as a [rows][cols] tensor of dtype."""
+    import torch
+
+    dt = _dtype(dtype, "mx_dequantize")
+    with _On(t.device, stream) as s:
+        if out is None:
+            out = torch.empty((t.rows, t.cols), dtype=dtype, device=t.device)
+        else:
+            _need("mx_dequantize", t.device, dtype, (t.rows, t.cols), out)
+        st = lib().lbq_mx_dequantize(ctypes.byref(t.struct), out.data_ptr(), dt, s)
+    _check(st, "lbq_mx_dequantize")
+    return out
+
+
+def mx_matmul(a: MxTensor, b: MxTensor, dtype=None, y=None, ws=None, stream=None):
+    """lbq_mx_matmul: y [a.rows][b.rows] = A B^T in dtype (float32 if neither it nor y is given)."""
+    import torch
+
+    L, need = lib(), ctypes.c_size_t()
+    _check(L.lbq_mx_matmul_workspace(ctypes.byref(a.struct), ctypes.byref(b.struct), ctypes.byref(need)),
+           "lbq_mx_matmul_workspace")
+    if b.device != a.device:
+        raise LbqError(-8, f"mx_matmul: tensors on {a.device} and {b.device}")
+    dtype = dtype if dtype is not None else (torch.float32 if y is None else y.dtype)
+    dt = _dtype(dtype, "mx_matmul")
+    with _On(a.device, stream) as s:
+        if y is None:
+            y = torch.empty((a.rows, b.rows), dtype=dtype, device=a.device)
+        else:
+            _need("mx_matmul", a.device, dtype, (a.rows, b.rows), y)
+        ws = _workspace(ws, need.value, a.device, "mx_matmul")
+        st = L.lbq_mx_matmul(ctypes.byref(a.struct), ctypes.byref(b.struct), y.data_ptr(), dt, ws.data_ptr(),
+                             _bytes_of(ws), s)
+    _check(st, "lbq_mx_matmul")
+    return y
+
+
+def mx_linear_forward(w: MxTensor, x, y=None, ws=None, stream=None):
+    """lbq_mx_linear_forward: y [M][w.rows] = Q(x) W^T, x [M][w.cols] in float16 or bfloat16, y in x's type."""
+    import torch
+
+    if x.dim() != 2 or x.shape[1] != w.cols:
+        raise LbqError(-2, "mx_linear_forward: x is [M][w.cols]")
+    M = x.shape[0]
+    dt = _dtype(x.dtype, "mx_linear_forward")
+    _need("mx_linear_forward", w.device, x.dtype, None, x)
+    L, need = lib(), ctypes.c_size_t()
+    _check(L.lbq_mx_linear_workspace(ctypes.byref(w.struct), M, ctypes.byref(need)), "lbq_mx_linear_workspace")
+    with _On(w.device, stream) as s:
+        if y is None:
+            y = torch.empty((M, w.rows), dtype=x.dtype, device=w.device)
+        else:
+            _need("mx_linear_forward", w.device, x.dtype, (M, w.rows), y)
+        ws = _workspace(ws, need.value, w.device, "mx_linear_forward")
+        st = L.lbq_mx_linear_forward(ctypes.byref(w.struct), x.data_ptr(), M, y.data_ptr(), dt, ws.data_ptr(),
+                                     _bytes_of(ws), s)
+    _check(st, "lbq_mx_linear_forward")
+    return y
+
+
+def mx_grouped_forward(w: MxTensor, E: int, x, offsets, perm=None, top_k: int = 1, y=None, ws=None, stream=None):
+    """lbq_mx_grouped_forward: w holds E experts of w.rows / E rows; y [T][w.rows / E], T the length of perm
+    (of x without perm). Rows of y from offsets[E] on are left as they were (uninitialised if y is not given)."""
+    import torch
+
+    if x.dim() != 2 or x.shape[1] != w.cols:
+        raise LbqError(-2, "mx_grouped_forward: x is [M][w.cols]")
+    if E < 1 or w.rows % E:
+        raise LbqError(-2, "mx_grouped_forward: w holds E experts of equal rows")
+    M, N = x.shape[0], w.rows // E
+    T = M if perm is None else perm.numel()
+    dt = _dtype(x.dtype, "mx_grouped_forward")
+    _need("mx_grouped_forward", w.device, x.dtype, None, x)
+    _need("mx_grouped_forward", w.device, torch.int32, (E + 1,), offsets)
+    if perm is not None:
+        _need("mx_grouped_forward", w.device, torch.int32, None, perm)
+    L, need = lib(), ctypes.c_size_t()
+    _check(L.lbq_mx_grouped_workspace(ctypes.byref(w.struct), E, M, T, ctypes.byref(need)),
+           "lbq_mx_grouped_workspace")
+    with _On(w.device, stream) as s:
+        if y is None:
+            y = torch.empty((T, N), dtype=x.dtype, device=w.device)
+        else:
+            _need("mx_grouped_forward", w.device, x.dtype, (T, N), y)
+        ws = _workspace(ws, need.value, w.device, "mx_grouped_forward")
+        st = L.lbq_mx_grouped_forward(ctypes.byref(w.struct), E, x.data_ptr(), M, offsets.data_ptr(),
+                                      None if perm is None else perm.data_ptr(), top_k, T, y.data_ptr(), dt,
+                                      ws.data_ptr(), _bytes_of(ws), s)
+    _check(st, "lbq_mx_grouped_forward")
+    return y
+
+
+def moe_sort(ids, E: int, stream=None):
+    """lbq_moe_sort of ids int32 [M][top_k]: (counts [E], offsets [E+1], perm [M*top_k], pos [M][top_k])."""
+    import torch
+
+    if ids.dim() != 2:
+        raise LbqError(-2, "moe_sort: ids are [M][top_k]")
+    _need("moe_sort", ids.device, torch.int32, None, ids)
+    M, k = ids.shape
+    L, need = lib(), ctypes.c_size_t()
+    _check(L.lbq_moe_sort_workspace(M, E, k, ctypes.byref(need)), "lbq_moe_sort_workspace")
+    with _On(ids.device, stream) as s:
+        n = M * k
+        sizes = [n, n, E, E + 1, need.value // 4]
+        pos, perm, counts, offsets, ws = torch.empty(sum(sizes), dtype=torch.int32, device=ids.device).split(sizes)
+        st = L.lbq_moe_sort(ids.data_ptr(), M, E, k, counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
+                            pos.data_ptr(), ws.data_ptr(), need.value, s)
+    _check(st, "lbq_moe_sort")
+    return counts, offsets, perm, pos.view(M, k)
+
+
+def _places(where: str, pos, device, *weights):
+    import torch
+
+    if pos.dim() != 2:
+        raise LbqError(-2, f"{where}: pos is [M][top_k]")
+    _need(where, device, torch.int32, None, pos)
+    if weights:
+        _need(where, device, torch.float32, tuple(pos.shape), *weights)
+    return pos.shape
+
+
+def _rows(where: str, x, rows=None):
+    if x.dim() != 2 or (rows is not None and x.shape[0] != rows):
+        raise LbqError(-2, f"{where}: rows {tuple(x.shape)}")
+    _need(where, x.device, x.dtype, None, x)
+    return _dtype(x.dtype, where)
+
+
+def moe_gather(x, pos, out=None, stream=None):
+    """lbq_moe_gather: out[pos[t][j]] = x[t]. out [T][H] is [M * top_k][H] if not given; rows that no place
+    names are left as they were (uninitialised if out is not given)."""
+    import torch
+
+    M, k = _places("moe_gather", pos, x.device)
+    dt, H = _rows("moe_gather", x, M), x.shape[-1]
+    with _On(x.device, stream) as s:
+        if out is None:
+            out = torch.empty((M * k, H), dtype=x.dtype, device=x.device)
+        else:
+            _need("moe_gather", x.device, x.dtype, (out.shape[0], H), out)
+        st = lib().lbq_moe_gather(x.data_ptr(), dt, M, H, pos.data_ptr(), k, out.shape[0], out.data_ptr(), s)
+    _check(st, "lbq_moe_gather")
+    return out
+
+
+def moe_gather_backward(d_out, pos, dx=None, stream=None):
+    """lbq_moe_gather_backward: dx[t] = sum_j d_out[pos[t][j]]."""
+    import torch
+
+    M, k = _places("moe_gather_backward", pos, d_out.device)
+    dt = _rows("moe_gather_backward", d_out)
+    T, H = d_out.shape
+    with _On(d_out.device, stream) as s:
+        if dx is None:
+            dx = torch.empty((M, H), dtype=d_out.dtype, device=d_out.device)
+        else:
+            _need("moe_gather_backward", d_out.device, d_out.dtype, (M, H), dx)
+        st = lib().lbq_moe_gather_backward(d_out.data_ptr(), dt, T, H, pos.data_ptr(), M, k, dx.data_ptr(), s)
+    _check(st, "lbq_moe_gather_backward")
+    return dx
+
+
+def moe_combine(o, pos, weights, y=None, stream=None):
+    """lbq_moe_combine: y[t] = sum_j weights[t][j] o[pos[t][j]] (weights float32 [M][top_k])."""
+    import torch
+
+    M, k = _places("moe_combine", pos, o.device, weights)
+    dt = _rows("moe_combine", o)
+    T, H = o.shape
+    with _On(o.device, stream) as s:
+        if y is None:
+            y = torch.empty((M, H), dtype=o.dtype, device=o.device)
+        else:
+            _need("moe_combine", o.device, o.dtype, (M, H), y)
+        st = lib().lbq_moe_combine(o.data_ptr(), dt, T, H, pos.data_ptr(), weights.data_ptr(), M, k, y.data_ptr(), s)
+    _check(st, "lbq_moe_combine")
+    return y
+
+
+def moe_combine_backward(dy, o, pos, weights, d_o=None, d_weights=None, stream=None):
+    """lbq_moe_combine_backward: (d_o [T][H], d_weights float32 [M][top_k]). Rows of d_o that no place names are
+    left as they were (uninitialised if d_o is not given)."""
+    import torch
+
+    M, k = _places("moe_combine_backward", pos, o.device, weights)
+    dt = _rows("moe_combine_backward", o)
+    T, H = o.shape
+    _need("moe_combine_backward", o.device, o.dtype, (M, H), dy)
+    with _On(o.device, stream) as s:
+        if d_o is None:
+            d_o = torch.empty_like(o)
+        else:
+            _need("moe_combine_backward", o.device, o.dtype, (T, H), d_o)
+        if d_weights is None:
+            d_weights = torch.empty((M, k), dtype=torch.float32, device=o.device)
+        else:
+            _need("moe_combine_backward", o.device, torch.float32, (M, k), d_weights)
+        st = lib().lbq_moe_combine_backward(dy.data_ptr(), o.data_ptr(), dt, T, H, pos.data_ptr(), weights.data_ptr(),
+                                            M, k, d_o.data_ptr(), d_weights.data_ptr(), s)
+    _check(st, "lbq_moe_combine_backward")
+    return d_o, d_weights

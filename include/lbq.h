@@ -397,6 +397,138 @@ lbq_status lbq_readout_screened(const lbq_readout *r, const uint16_t *x, int32_t
 lbq_status lbq_stream_read(const void *buf, size_t bytes, int32_t grid, int32_t block, uint32_t *sink,
                            void *stream, void *start_event, void *stop_event);
 
+/* ---- MXFP4 tensors and their products ----
+ *
+ * Microscaled 4-bit floating point as the OCP Microscaling Formats (MX)
+ * specification v1.0 defines it: blocks of 32 values share an 8-bit power of
+ * two (E8M0: byte b is 2^(b - 127), 255 is NaN), each value is an e2m1 code
+ * (magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6 for the low three bits, sign in bit 3).
+ * A tensor of R rows and C columns, C a multiple of 128, has its blocks along
+ * the columns:
+ *   codes:  uint8 [R][C/2]; byte i of a row holds value 2i in its low nibble
+ *           and 2i + 1 in its high nibble.
+ *   scales: uint8 [C/128][R][4]; byte b of word (g, r) belongs to values
+ *           128 g + 32 b .. 128 g + 32 b + 31 of row r.
+ * R * (C/128) stays below 2^31 (LBQ_ERR_SHAPE otherwise). These calls take no
+ * rotation signs: lbq_rotate the activations, and the weights before they are
+ * quantized, where a rotated basis is wanted.
+ */
+
+/* Value types of the buffers that are not in a packed format. */
+typedef enum { LBQ_F16 = 0, LBQ_BF16 = 1, LBQ_F32 = 2 } lbq_dtype;
+
+/* An MXFP4 tensor: a plain view of caller-owned device buffers. */
+typedef struct {
+  int32_t rows, cols;
+  const void *codes;
+  const void *scales;
+} lbq_mx;
+
+/* Byte sizes of an MXFP4 tensor (host query). Errors: LBQ_ERR_NULL, LBQ_ERR_SHAPE
+ * (rows < 0, cols not a positive multiple of 128, too many groups). */
+lbq_status lbq_mx_bytes(int32_t rows, int32_t cols, size_t *code_bytes, size_t *scale_bytes);
+
+/* Quantize x [rows][cols] (dtype) into the MXFP4 tensor of rows x cols. Per
+ * block, with m its largest magnitude: e = clamp(floor(log2 m) - 2, -127, 125)
+ * (-127 for m = 0), scale byte e + 127, codes e2m1(x / 2^e) rounded to nearest,
+ * ties to the even code, saturated at 6, zeros keeping their sign. A block that
+ * holds a NaN or an infinity gets scale byte 255 and zero codes. Errors:
+ * LBQ_ERR_SHAPE, LBQ_ERR_FORMAT (dtype), LBQ_ERR_NULL, LBQ_ERR_ALIGN, LBQ_ERR_HIP. */
+lbq_status lbq_mx_quantize(const void *x, int32_t dtype, int32_t rows, int32_t cols, void *codes, void *scales,
+                           void *stream);
+
+/* The same for x^T: x [rows][cols] (any rows >= 0 and cols > 0) into the MXFP4
+ * tensor of cols rows and Rp = rows rounded up to a multiple of 128 columns,
+ * the columns past rows zero. What a product needs whose sum runs over x's
+ * rows (the weight's gradient sums over tokens, the input's over outputs). */
+lbq_status lbq_mx_quantize_t(const void *x, int32_t dtype, int32_t rows, int32_t cols, void *codes, void *scales,
+                             void *stream);
+
+/* The values of an MXFP4 tensor: x [rows][cols] (dtype), each rounded once
+ * (exact in fp32 and bf16; in fp16 wherever the value is in its range). */
+lbq_status lbq_mx_dequantize(const lbq_mx *t, void *x, int32_t dtype, void *stream);
+
+/* Workspace bytes of lbq_mx_matmul (host query). Errors as its argument checks. */
+lbq_status lbq_mx_matmul_workspace(const lbq_mx *a, const lbq_mx *b, size_t *bytes);
+
+/* y [a.rows][b.rows] (dtype) = A B^T of two MXFP4 tensors with equal cols:
+ * exact products, fp32 accumulation, one rounding. A NaN block makes every
+ * result it meets NaN. rows = 0 on either side is a no-op. Repeat calls give
+ * identical bits. Errors: LBQ_ERR_NULL, _SHAPE, _FORMAT, _ALIGN, _WORKSPACE,
+ * before any launch; LBQ_ERR_HIP. */
+lbq_status lbq_mx_matmul(const lbq_mx *a, const lbq_mx *b, void *y, int32_t dtype, void *ws, size_t ws_bytes,
+                         void *stream);
+
+/* Workspace bytes of lbq_mx_linear_forward for M tokens (host query). */
+lbq_status lbq_mx_linear_workspace(const lbq_mx *w, int32_t M, size_t *bytes);
+
+/* y [M][w.rows] (dtype) = Q(x) W^T: x [M][w.cols] (dtype LBQ_F16 or LBQ_BF16)
+ * is quantized as lbq_mx_quantize does, then multiplied as lbq_mx_matmul does.
+ * Errors as lbq_mx_matmul. */
+lbq_status lbq_mx_linear_forward(const lbq_mx *w, const void *x, int32_t M, void *y, int32_t dtype, void *ws,
+                                 size_t ws_bytes, void *stream);
+
+/* Workspace bytes of lbq_mx_grouped_forward (host query). */
+lbq_status lbq_mx_grouped_workspace(const lbq_mx *w, int32_t E, int32_t M, int32_t T, size_t *bytes);
+
+/* Rows sorted by expert times their expert's weight: w holds E blocks of
+ * N = w.rows / E rows; list row i (0 <= i < T) with offsets[e] <= i <
+ * offsets[e + 1] gets y[i] = Q(x[perm[i] / top_k]) W_e^T, y [T][N] (dtype).
+ *   x: [M][w.cols] (dtype LBQ_F16 or LBQ_BF16); offsets: device int32 [E + 1];
+ *   perm: device int32 [T], or NULL for x already in list order (then M = T).
+ * offsets and perm as lbq_moe_route or lbq_moe_sort write them; rows of y from
+ * offsets[E] on are left as they were. offsets are clamped to [0, T] and x's
+ * row numbers to [0, M): contents out of range give wrong rows, never an access
+ * out of bounds. Limits: E <= 1024. Errors as lbq_mx_matmul. */
+lbq_status lbq_mx_grouped_forward(const lbq_mx *w, int32_t E, const void *x, int32_t M, const int32_t *offsets,
+                                  const int32_t *perm, int32_t top_k, int32_t T, void *y, int32_t dtype, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/* ---- Expert dispatch: picks sorted by expert, rows there and back ----
+ *
+ * A pick is assignment a = t * top_k + j: slot j of token t goes to expert
+ * ids[t][j]. Limits as lbq_moe_route's: E <= 1024, top_k <= 32, M * top_k <=
+ * 2^20 (LBQ_ERR_SHAPE). Row buffers hold H values of dtype each (any H > 0). */
+
+/* Workspace bytes of lbq_moe_sort (host query). */
+lbq_status lbq_moe_sort_workspace(int32_t M, int32_t E, int32_t top_k, size_t *bytes);
+
+/* Sort given picks by expert: lbq_moe_route's sort for ids of the caller's own.
+ *   ids: int32 [M][top_k]; an id outside [0, E) is no pick (a dropped token, an
+ *     expert of another rank). A token may name an expert twice.
+ *   counts int32 [E], offsets int32 [E+1]: picks per expert, their exclusive sum;
+ *   perm int32 [M*top_k]: the picks grouped by expert, increasing within one; -1
+ *     from offsets[E] on;
+ *   pos int32 [M][top_k]: where each pick went (perm[pos[a]] = a), -1 for none. */
+lbq_status lbq_moe_sort(const int32_t *ids, int32_t M, int32_t E, int32_t top_k, int32_t *counts, int32_t *offsets,
+                        int32_t *perm, int32_t *pos, void *ws, size_t ws_bytes, void *stream);
+
+/* out[pos[t][j]] = x[t] for every place in [0, T): x [M][H], out [T][H]; rows
+ * that no place names are left as they were. pos names no row twice (as
+ * lbq_moe_sort writes it). */
+lbq_status lbq_moe_gather(const void *x, int32_t dtype, int32_t M, int32_t H, const int32_t *pos, int32_t top_k,
+                          int32_t T, void *out, void *stream);
+
+/* The gather's gradient: dx[t] = sum over j of d_out[pos[t][j]] (places outside
+ * [0, T) count nothing; a token without any gets zeros), summed in fp32 in slot
+ * order, rounded once. d_out [T][H], dx [M][H]. */
+lbq_status lbq_moe_gather_backward(const void *d_out, int32_t dtype, int32_t T, int32_t H, const int32_t *pos,
+                                   int32_t M, int32_t top_k, void *dx, void *stream);
+
+/* y[t] = sum over j of weights[t][j] o[pos[t][j]], summed in fp32 in slot order,
+ * rounded once: o [T][H], weights fp32 [M][top_k], y [M][H]. Places outside
+ * [0, T) count nothing, whatever their weight; a token without any gets zeros. */
+lbq_status lbq_moe_combine(const void *o, int32_t dtype, int32_t T, int32_t H, const int32_t *pos,
+                           const float *weights, int32_t M, int32_t top_k, void *y, void *stream);
+
+/* The combine's gradients: d_o[pos[t][j]] = weights[t][j] dy[t] (rows that no
+ * place names are left as they were) and d_weights[t][j] = <dy[t], o[pos[t][j]]>
+ * in fp32 (0 where there is no place). dy [M][H], o and d_o [T][H]; d_o may be
+ * o itself. pos names no row twice. */
+lbq_status lbq_moe_combine_backward(const void *dy, const void *o, int32_t dtype, int32_t T, int32_t H,
+                                    const int32_t *pos, const float *weights, int32_t M, int32_t top_k, void *d_o,
+                                    float *d_weights, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
