@@ -17,7 +17,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblbq.so")
 
 HIP_SOURCES = ["api.hip", "rotate.hip", "gemv.hip", "gemv_mfma.hip", "gemm.hip", "gemm_rtn.hip", "gemm_mx.hip", "pvq.hip", "pvq_mx.hip", "moe.hip", "moe_mx.hip", "unpack.hip", "measure.hip", "readout.hip",
-               "mxfp4.hip", "mx_gemm.hip", "dispatch.hip", "api_mx.hip"]
+               "mxfp4.hip", "mx_gemm.hip", "mx_stream.hip", "dispatch.hip", "api_mx.hip"]
 HOST_SOURCES = ["pack.cpp", "gptq.cpp"]
 
 ARCH = os.environ.get("LBQ_OFFLOAD_ARCH", "gfx950")
@@ -31,6 +31,9 @@ HIP_FLAGS = [
     "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wno-unused-result",
 ]
+# mx_gemm.hip: a wave's accumulators (up to 256 registers) live in AGPRs, next
+# to operands in the 256 VGPRs an instruction can name
+AGPR_SOURCES = {"mx_gemm.hip"}
 HOST_FLAGS = ["-O2", "-fPIC", "-std=c++17", "-ffp-contract=off", "-pthread",
               "-I/opt/rocm/include", "-D__HIP_PLATFORM_AMD__"]
 
@@ -66,7 +69,8 @@ def build(verbose: bool = False, jobs: int | None = None, sanitize: bool = False
     for src in HIP_SOURCES:
         obj = os.path.join(bdir, src + ".o")
         san = [f for flag in SAN_HOST for f in ("-Xarch_host", flag)] if sanitize else []
-        cmds.append([HIPCC, *HIP_FLAGS, *san, "-c", os.path.join(CSRC, src), "-o", obj])
+        flags = [f for f in HIP_FLAGS if f not in ("-mllvm", "-amdgpu-mfma-vgpr-form")] if src in AGPR_SOURCES else HIP_FLAGS
+        cmds.append([HIPCC, *flags, *san, "-c", os.path.join(CSRC, src), "-o", obj])
         objs.append(obj)
     for src in HOST_SOURCES:
         obj = os.path.join(bdir, src + ".o")

@@ -201,6 +201,7 @@ hipError_t launch_mx_dequantize(const void *codes, const void *scales, int rows,
 // perm[i] / top_k (perm null: i); rows from offsets[E] on are not written.
 struct MxGemm {
   const void *a_codes, *a_scales, *b_codes, *b_scales;
+  const void *x;   // 16-bit activations in place of A (mx_stream.hip), or null
   void *y;
   int dtype;
   int a_rows, M, N, K;
@@ -209,6 +210,11 @@ struct MxGemm {
   void *scratch;   // mx_gemm_scratch_bytes of it
 };
 size_t mx_gemm_scratch_bytes(const MxGemm &p);
+// Few rows (per expert): the weight streamed once (mx_stream.hip). With x given
+// the activations come in 16 bits (dtype) and are quantized on the way; a_codes
+// and a_scales are not read.
+bool mx_stream_supported(int rows, int K);
+hipError_t launch_mx_stream(const MxGemm &g, int rows, hipStream_t s);
 hipError_t launch_mx_gemm(const MxGemm &p, hipStream_t s);
 
 // Expert dispatch (dispatch.hip). The sort of n picks; the row moves over

@@ -7,8 +7,10 @@
 // block's scale byte; result register i of lane (c, h) is row
 // 8 (i / 4) + 4 h + i % 4, column c.
 #include "device.h"
+#include "gemm_common.h"
 #include "kernels.h"
 #include "mxfp4.h"
+#include "mx_tiles.h"
 
 #include <algorithm>
 
@@ -18,60 +20,7 @@ namespace {
 
 using namespace mxfp4;
 
-typedef int v8i_t __attribute__((ext_vector_type(8)));
 typedef float v16f_t __attribute__((ext_vector_type(16)));
-
-constexpr int kThreads = 256;
-constexpr int kTile = 128;   // rows and columns of a workgroup: four waves of 64 x 64
-
-// Row tile `slot` of the expert-sorted list: its expert, first row and rows
-// (0 rows past the last tile). Every lane of the wave gets the same answer.
-// offsets is taken as it comes: ranges are clamped to [0, T].
-struct GroupTile {
-  int e, i0, n;
-};
-__device__ __forceinline__ GroupTile find_tile(const int32_t *offsets, int E, int T, int bm, int slot) {
-  const int lane = threadIdx.x & 63;
-  const int per = (E + 63) / 64, e0 = lane * per;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = e0 + i;
-    if (e >= E) break;
-    const int lo = min(max(offsets[e], 0), T), hi = min(max(offsets[e + 1], lo), T);
-    mine += (hi - lo + bm - 1) / bm;
-  }
-  int incl = mine;
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
-  const uint64_t past = __ballot(slot < incl);
-  GroupTile t{0, 0, 0};
-  if (past == 0) return t;
-  const int src = __builtin_ctzll(past);
-  int k = slot - (incl - mine);   // the lane's own tile number, if src
-  if (lane == src) {
-    for (int i = 0; i < per; ++i) {
-      const int e = e0 + i;
-      if (e >= E) break;
-      const int lo = min(max(offsets[e], 0), T), hi = min(max(offsets[e + 1], lo), T);
-      const int tiles = (hi - lo + bm - 1) / bm;
-      if (k < tiles) {
-        t = GroupTile{e, lo + k * bm, min(hi - lo - k * bm, bm)};
-        break;
-      }
-      k -= tiles;
-    }
-  }
-  t.e = __shfl(t.e, src);
-  t.i0 = __shfl(t.i0, src);
-  t.n = __shfl(t.n, src);
-  return t;
-}
-
-__device__ __forceinline__ v8i_t operand(uint4 v) {
-  return v8i_t{static_cast<int>(v.x), static_cast<int>(v.y), static_cast<int>(v.z), static_cast<int>(v.w), 0, 0, 0, 0};
-}
 
 struct GemmArgs {
   const uint8_t *a_codes;      // [a_rows][K / 2]
@@ -83,87 +32,382 @@ struct GemmArgs {
   // grouped: list rows by expert; perm[i] / top_k (or i) is the activation row
   const int32_t *offsets, *perm;
   int E, top_k;
+  int tiles_m, tiles_n;
 };
 
-// 128 x 128 per workgroup, operands straight from memory (each lane's 16 bytes).
-template <int DT, bool GROUPED>
-__global__ void __launch_bounds__(kThreads) mx_gemm_kernel(GemmArgs g) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// A workgroup of GM x GN waves; a wave owns MB x NB blocks of 32 tokens by 32
+// weight rows. The weight is the instruction's first operand, so a lane's four
+// consecutive result registers are four neighbouring outputs of one token.
+//
+// Stages of one 128-group of K (64 bytes a row, and a scale word a row) go
+// global -> LDS by asynchronous copies into a ring of RING buffers. In stage s
+// the copies of stages s + 2 .. s + RING - 1 are in flight and the operands of
+// the next 64-long step are read from LDS while one step is multiplied, across
+// the stage's border too: stage s starts when s + 1 has landed. One barrier per
+// stage. Vector v (16 bytes) of row r lies in slot v ^ ((r >> 2) & 3) of the
+// row: the sixteen rows that a quarter of an operand read touches fall in
+// sixteen distinct 16-byte bank groups.
+template <int MB, int NB, int GM, int GN>
+struct Tile {
+  static constexpr int kThreads = 64 * GM * GN;
+  static constexpr int kM = 32 * MB * GM, kN = 32 * NB * GN;
+  static constexpr int kCopiesA = kM * 4 / kThreads, kCopiesB = kN * 4 / kThreads;
+  static_assert(kCopiesA * kThreads == kM * 4 && kCopiesB * kThreads == kN * 4, "whole copies");
+  // scale words: where a tile has fewer rows than threads, waves copy the same words
+  static constexpr int kScalesA = kM < kThreads ? 1 : kM / kThreads, kScalesB = kN < kThreads ? 1 : kN / kThreads;
+  static_assert(kM % 64 == 0 && kN % 64 == 0, "a wave copies 64 scale words");
+  static constexpr int kLoads = kCopiesA + kCopiesB + kScalesA + kScalesB;   // per wave and stage
+};
+
+// One stage's buffer, an object of its own: the compiler tells reads of one
+// from copies in flight into another.
+template <class Tl>
+struct Stage {
+  uint4 a[Tl::kM * 4], b[Tl::kN * 4];
+  uint32_t sa[Tl::kM], sb[Tl::kN];
+};
+
+// Workgroup number -> (row tile, column tile). Workgroups go to the eight XCDs
+// in turn, each with an L2 of its own: XCD i gets the i-th eighth of the tile
+// sequence, which walks `group` row tiles down each column before the next.
+__device__ __forceinline__ void place_tile(int pid, int tm, int tn, int group, int &m, int &n) {
+  const int total = tm * tn, q = total / 8, rem = total % 8;
+  const int xcd = pid & 7;
+  const int id = xcd * q + min(xcd, rem) + (pid >> 3);
+  const int width = group * tn, g = id / width, first = g * group;
+  const int rows = min(tm - first, group), in = id - g * width;
+  m = first + in % rows;
+  n = in / rows;
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  return from_f32<DT>(a) | (static_cast<uint32_t>(from_f32<DT>(b)) << 16);
+}
+
+// One 32 x 32 result block: token row m (the lane's), outputs n0 .. n0 + 31.
+// VEC: N is a multiple of 8, so eight neighbouring outputs (four in fp32) are
+// one aligned 16-byte store. The halves of a token's outputs sit in lanes
+// (m, 0) and (m, 1); a lane swap gives each eight neighbours.
+template <int DT, bool VEC>
+__device__ __forceinline__ void store_block(void *y, size_t row, bool ok, int n0, int N, int h, const v16f_t &acc) {
+  using T = typename Elem<DT>::type;
+  if constexpr (VEC && DT != kF32) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      uint32_t a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i] = pack2<DT>(acc[8 * q + 2 * i], acc[8 * q + 2 * i + 1]);
+        b[i] = pack2<DT>(acc[8 * q + 4 + 2 * i], acc[8 * q + 4 + 2 * i + 1]);
+        const auto sw = __builtin_amdgcn_permlane32_swap(a[i], b[i], false, false);
+        a[i] = sw[0];
+        b[i] = sw[1];
+      }
+      const int n = n0 + 16 * q + 8 * h;
+      if (ok && n < N) *reinterpret_cast<uint4 *>(static_cast<T *>(y) + row * N + n) = make_uint4(a[0], a[1], b[0], b[1]);
+    }
+  } else if constexpr (VEC) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int n = n0 + 8 * q + 4 * h;
+      if (ok && n < N)
+        *reinterpret_cast<float4_t *>(static_cast<T *>(y) + row * N + n) =
+            float4_t{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int n = n0 + 8 * (k / 4) + 4 * h + k % 4;
+      if (ok && n < N) static_cast<T *>(y)[row * N + n] = from_f32<DT>(acc[k]);
+    }
+  }
+}
+
+template <int MB, int NB, int GM, int GN, int RING, int DT, bool GROUPED>
+__global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
+  using Tl = Tile<MB, NB, GM, GN>;
+  constexpr int TH = Tl::kThreads, CA = Tl::kCopiesA, CB = Tl::kCopiesB;
+  static_assert(RING == 3 || RING == 4, "ring");
+  __shared__ __attribute__((aligned(16))) Stage<Tl> q0, q1, q2, q3;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  int i0 = blockIdx.y * kTile, n_rows = g.M - i0, e = 0;
+  int tile_m, tile_n;
+  place_tile(blockIdx.x, g.tiles_m, g.tiles_n, 4, tile_m, tile_n);
+  int i0 = tile_m * Tl::kM, n_rows = g.M - i0, e = 0;
   if constexpr (GROUPED) {
-    const GroupTile t = find_tile(g.offsets, g.E, g.M, kTile, blockIdx.y);
+    const GroupTile t = find_tile(g.offsets, g.E, g.M, Tl::kM, tile_m);
     if (t.n == 0) return;
     i0 = t.i0;
     n_rows = t.n;
     e = t.e;
   }
-  const int wm = (wave >> 1) * 64, wn = blockIdx.x * kTile + (wave & 1) * 64;
-  const uint8_t *pa[2], *pb[2];
-  const uint32_t *sa[2], *sb[2];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    // rows past the end repeat the last one; their results are not stored
-    int ia = i0 + min(wm + 32 * t + r, n_rows - 1);
+  const int col0 = tile_n * Tl::kN;
+  // K slice blockIdx.y: groups [first, first + G)
+  const int all = g.K / kGroup, first = static_cast<int>(static_cast<long>(all) * blockIdx.y / gridDim.y);
+  const int G = static_cast<int>(static_cast<long>(all) * (blockIdx.y + 1) / gridDim.y) - first;
+  // activation row of list row i0 + i (rows past the end repeat the last one;
+  // their results are not stored)
+  auto act_row = [&](int i) {
+    int ia = i0 + min(i, n_rows - 1);
     if constexpr (GROUPED)
       if (g.perm) ia = g.perm[ia] / g.top_k;
-    ia = min(max(ia, 0), g.a_rows - 1);
-    const int ib = e * g.N + min(wn + 32 * t + r, g.N - 1);
-    pa[t] = g.a_codes + static_cast<size_t>(ia) * (g.K / 2) + 16 * h;
-    pb[t] = g.b_codes + static_cast<size_t>(ib) * (g.K / 2) + 16 * h;
-    sa[t] = g.a_scales + ia;
-    sb[t] = g.b_scales + ib;
-  }
-  v16f_t acc[2][2];
+    return static_cast<size_t>(min(max(ia, 0), g.a_rows - 1));
+  };
+  auto weight_row = [&](int n) { return static_cast<size_t>(e) * g.N + min(col0 + n, g.N - 1); };
+  const int vec = (tid & 3) ^ ((tid >> 4) & 3);
+  const uint8_t *pa[CA], *pb[CB];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[0][0][i] = acc[0][1][i] = acc[1][0][i] = acc[1][1][i] = 0.f;
-  for (int kg = 0; kg < g.K / kGroup; ++kg) {
-    int va[2], vb[2];
+  for (int it = 0; it < CA; ++it) 
+    pa[it] = g.a_codes + act_row(it * (TH / 4) + (tid >> 2)) * (g.K / 2) + 64 * first + 16 * vec;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      va[t] = static_cast<int>(sa[t][static_cast<size_t>(kg) * g.a_rows] >> (8 * h));
-      vb[t] = static_cast<int>(sb[t][static_cast<size_t>(kg) * g.b_rows] >> (8 * h));
+  for (int it = 0; it < CB; ++it) 
+    pb[it] = g.b_codes + weight_row(it * (TH / 4) + (tid >> 2)) * (g.K / 2) + 64 * first + 16 * vec;
+  const uint32_t *psa[Tl::kScalesA], *psb[Tl::kScalesB];
+#pragma unroll
+  for (int it = 0; it < Tl::kScalesA; ++it) 
+    psa[it] = g.a_scales + static_cast<size_t>(first) * g.a_rows + act_row((it * TH + tid) % Tl::kM);
+#pragma unroll
+  for (int it = 0; it < Tl::kScalesB; ++it) 
+    psb[it] = g.b_scales + static_cast<size_t>(first) * g.b_rows + weight_row((it * TH + tid) % Tl::kN);
+
+  // copies of the next stage in line; past the last one it repeats, so that
+  // every stage has the same number of copies in flight (never multiplied)
+  int ahead = 0;
+  auto issue = [&](Stage<Tl> &q) {
+#pragma unroll
+    for (int it = 0; it < CA; ++it) copy16_to_lds(pa[it], q.a + it * TH + wave * 64);
+#pragma unroll
+    for (int it = 0; it < CB; ++it) copy16_to_lds(pb[it], q.b + it * TH + wave * 64);
+#pragma unroll
+    for (int it = 0; it < Tl::kScalesA; ++it) copy4_to_lds(psa[it], q.sa + (it * TH + wave * 64) % Tl::kM);
+#pragma unroll
+    for (int it = 0; it < Tl::kScalesB; ++it) copy4_to_lds(psb[it], q.sb + (it * TH + wave * 64) % Tl::kN);
+    const bool more = ++ahead < G;
+    const int by = more ? 64 : 0;
+    const size_t da = more ? g.a_rows : 0, db = more ? g.b_rows : 0;
+#pragma unroll
+    for (int it = 0; it < CA; ++it) pa[it] += by;
+#pragma unroll
+    for (int it = 0; it < CB; ++it) pb[it] += by;
+#pragma unroll
+    for (int it = 0; it < Tl::kScalesA; ++it) psa[it] += da;
+#pragma unroll
+    for (int it = 0; it < Tl::kScalesB; ++it) psb[it] += db;
+  };
+
+  const int wm = (wave / GN) * 32 * MB, wn = (wave % GN) * 32 * NB;
+  const int key = (r >> 2) & 3;
+  v16f_t acc[MB][NB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+#pragma unroll
+      for (int k = 0; k < 16; ++k) acc[i][j][k] = 0.f;
+
+  struct Step {
+    v8i_t a[MB], b[NB];
+  };
+  uint32_t va[MB], vb[NB];   // scale words: bytes 0 and 2 are this lane's blocks of the two steps
+  auto read = [&](Step &f, const Stage<Tl> &q, int s) {
+    const int at = (2 * s + h) ^ key;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) f.b[j] = operand(q.b[(wn + 32 * j + r) * 4 + at]);
+#pragma unroll
+    for (int i = 0; i < MB; ++i) f.a[i] = operand(q.a[(wm + 32 * i + r) * 4 + at]);
+  };
+  auto read_scales = [&](const Stage<Tl> &q) {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) va[i] = q.sa[wm + 32 * i + r] >> (8 * h);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) vb[j] = q.sb[wn + 32 * j + r] >> (8 * h);
+  };
+#define LBQ_MX_STEP(F, SEL, VA, VB)                                                                             \
+  do {                                                                                                          \
+    _Pragma("unroll") for (int i = 0; i < MB; ++i) _Pragma("unroll") for (int j = 0; j < NB; ++j) acc[i][j] =   \
+        __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.b[j], F.a[i], acc[i][j], 4, 4, SEL,                   \
+                                                        static_cast<int>(VB[j]), SEL, static_cast<int>(VA[i])); \
+  } while (0)
+
+  Step f0, f1;
+  auto landed = [&]() {
+    // this wave's copies of the stage after the current one have landed; after
+    // the barrier every wave's, and every wave is done with the stage before
+    wait_vm_lds<(RING - 3) * Tl::kLoads>();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  // stage in cur, its first step's operands in f0; free takes the copies
+  auto stage = [&](const Stage<Tl> &cur, const Stage<Tl> &next, Stage<Tl> &free) {
+    landed();
+    issue(free);
+    read(f1, cur, 1);
+    LBQ_MX_STEP(f0, 0, va, vb);
+    uint32_t wa[MB], wb[NB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i) wa[i] = va[i];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) wb[j] = vb[j];
+    read(f0, next, 0);
+    read_scales(next);
+    LBQ_MX_STEP(f1, 2, wa, wb);
+    // the order of a stage's instructions: LDS reads (this stage's second step's,
+    // then the next stage's first) and the copies one by one between products,
+    // so that neither holds up the matrix cores (8192 x 4096 x 14336: 261 ->
+    // 243 us against the compiler's own order)
+    constexpr int kP = MB * NB, kR = MB + NB;
+#pragma unroll
+    for (int i = 0; i < kP; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < kR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (i >= kR) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      v8i_t fa[2], fb[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        fa[t] = operand(*reinterpret_cast<const uint4 *>(pa[t] + 64 * static_cast<size_t>(kg) + 32 * s));
-        fb[t] = operand(*reinterpret_cast<const uint4 *>(pb[t] + 64 * static_cast<size_t>(kg) + 32 * s));
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          acc[i][j] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], 4, 4, 0, va[i],
-                                                                              0, vb[j])
-                             : __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fa[i], fb[j], acc[i][j], 4, 4, 2, va[i],
-                                                                              2, vb[j]);
+    for (int i = 0; i < kP; ++i) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      if (i < kR) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+      if (i >= kR) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
+    }
+  };
+  issue(q0);
+  issue(q1);
+  if constexpr (RING == 4) issue(q2);
+  wait_vm_lds<(RING - 2) * Tl::kLoads>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read(f0, q0, 0);
+  read_scales(q0);
+  // whole rounds of the ring, then what is left of one (no exits inside the
+  // loop: the accumulators keep their registers)
+  const int rest = G % RING;
+  for (int n = G / RING; n > 0; --n) {
+    if constexpr (RING == 4) {
+      stage(q0, q1, q3);
+      stage(q1, q2, q0);
+      stage(q2, q3, q1);
+      stage(q3, q0, q2);
+    } else {
+      stage(q0, q1, q2);
+      stage(q1, q2, q0);
+      stage(q2, q0, q1);
     }
   }
-  using T = typename Elem<DT>::type;
-  T *y = static_cast<T *>(g.y);
+  if (rest > 0) {
+    if constexpr (RING == 4) stage(q0, q1, q3);
+    else stage(q0, q1, q2);
+  }
+  if (rest > 1) {
+    if constexpr (RING == 4) stage(q1, q2, q0);
+    else stage(q1, q2, q0);
+  }
+  if constexpr (RING == 4)
+    if (rest > 2) stage(q2, q3, q1);
+#undef LBQ_MX_STEP
+  wait_vm_lds<0>();   // no copy into LDS outlives the workgroup
+  // the last products' results are complete before anything moves them (sixteen
+  // passes of four cycles)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15");
+  __builtin_amdgcn_sched_barrier(0);
+  const bool vecs = g.N % 8 == 0;
+  // slices write partial results one behind the other
+  void *y = g.y;
+  if constexpr (DT == kF32) y = static_cast<float *>(y) + static_cast<size_t>(blockIdx.y) * g.M * g.N;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int i = 0; i < MB; ++i) {
+    const int row = wm + 32 * i + r;
+    const size_t at = static_cast<size_t>(i0) + row;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const int row = wm + 32 * i + 8 * (k / 4) + 4 * h + k % 4, n = wn + 32 * j + r;
-        if (row < n_rows && n < g.N) y[static_cast<size_t>(i0 + row) * g.N + n] = from_f32<DT>(acc[i][j][k]);
-      }
+    for (int j = 0; j < NB; ++j) {
+      const int n0 = col0 + wn + 32 * j;
+      if (vecs) store_block<DT, true>(y, at, row < n_rows, n0, g.N, h, acc[i][j]);
+      else store_block<DT, false>(y, at, row < n_rows, n0, g.N, h, acc[i][j]);
+    }
+  }
+}
+
+// Sum of S partial results in slice order, rounded once.
+__global__ void __launch_bounds__(256) mx_sum_kernel(const float *__restrict__ part, int S, long n, int dtype,
+                                                     void *__restrict__ y) {
+  for (long i = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; i < n; i += 256l * gridDim.x) {
+    float v = part[i];
+    for (int k = 1; k < S; ++k) v += part[k * n + i];
+    if (dtype == kF16) static_cast<uint16_t *>(y)[i] = from_f32<kF16>(v);
+    else if (dtype == kBF16) static_cast<uint16_t *>(y)[i] = from_f32<kBF16>(v);
+    else static_cast<float *>(y)[i] = v;
+  }
+}
+
+template <int MB, int NB, int GM, int GN, int RING>
+hipError_t launch_tiles(GemmArgs g, int dtype, int slices, hipStream_t s) {
+  using Tl = Tile<MB, NB, GM, GN>;
+  // grouped: every expert may end in a ragged tile
+  const long tm = (static_cast<long>(g.M) + Tl::kM - 1) / Tl::kM + (g.E > 0 ? std::min(g.E, g.M) : 0);
+  const long tn = (static_cast<long>(g.N) + Tl::kN - 1) / Tl::kN;
+  if (tm * tn >= (1l << 31)) return hipErrorInvalidValue;
+  g.tiles_m = static_cast<int>(tm);
+  g.tiles_n = static_cast<int>(tn);
+  const dim3 grid(static_cast<unsigned>(tm * tn), static_cast<unsigned>(slices)), block(Tl::kThreads);
+#define LBQ_MX_GO(DT)                                                                                       \
+  if (g.E > 0) hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, RING, DT, true>), grid, block, 0, s, g);        \
+  else hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, RING, DT, false>), grid, block, 0, s, g)
+  if (dtype == kF16) {
+    LBQ_MX_GO(kF16);
+  } else if (dtype == kBF16) {
+    LBQ_MX_GO(kBF16);
+  } else {
+    LBQ_MX_GO(kF32);
+  }
+#undef LBQ_MX_GO
+  return hipGetLastError();
+}
+
+// Which tile, and how many slices of K. A workgroup per compute unit takes, per
+// 4096 of K, about 41 us on 256 x 256, 13.6 on 128 x 128 and 8.7 on 64 x 128
+// (4096^3 and 512 x 4096^2); the smallest sum of rounds wins. Fewer tiles of
+// the smallest kind than half the compute units: K in slices of at least 1024.
+struct Plan {
+  int bm, bn, slices;
+};
+Plan plan_tiles(const MxGemm &p) {
+  auto tiles = [&](int bm, int bn) {
+    // grouped: half of the experts' last tiles are taken to be ragged
+    const long tm = p.E > 0 ? std::max<long>(static_cast<long>(p.M) / bm + p.E / 2, std::min(p.E, p.M))
+                            : (static_cast<long>(p.M) + bm - 1) / bm;
+    return tm * ((static_cast<long>(p.N) + bn - 1) / bn);
+  };
+  auto rounds = [&](int bm, int bn) { return static_cast<double>((tiles(bm, bn) + 255) / 256); };
+  const double big = 41 * rounds(256, 256), mid = 13.6 * rounds(128, 128), small = 8.7 * rounds(64, 128);
+  if (big <= mid && big <= small) return {256, 256, 1};
+  if (mid <= small) return {128, 128, 1};
+  Plan r{64, 128, 1};
+  if (p.E == 0) {
+    const long n = tiles(64, 128);
+    while (r.slices < 8 && n * r.slices * 2 <= 256 && p.K / (r.slices * 2) >= 1024) r.slices *= 2;
+  }
+  return r;
 }
 
 }  // namespace
 
+size_t mx_gemm_scratch_bytes(const MxGemm &p) {
+  const Plan r = plan_tiles(p);
+  return r.slices > 1 ? static_cast<size_t>(r.slices) * p.M * p.N * 4 : 0;
+}
+
 hipError_t launch_mx_gemm(const MxGemm &p, hipStream_t s) {
+  const Plan r = plan_tiles(p);
   GemmArgs g{};
   g.a_codes = static_cast<const uint8_t *>(p.a_codes);
   g.a_scales = static_cast<const uint32_t *>(p.a_scales);
   g.b_codes = static_cast<const uint8_t *>(p.b_codes);
   g.b_scales = static_cast<const uint32_t *>(p.b_scales);
-  g.y = p.y;
+  g.y = r.slices > 1 ? p.scratch : p.y;
   g.a_rows = p.a_rows;
   g.b_rows = p.E > 0 ? p.E * p.N : p.N;
   g.M = p.M;
@@ -173,23 +417,16 @@ hipError_t launch_mx_gemm(const MxGemm &p, hipStream_t s) {
   g.perm = p.perm;
   g.E = p.E;
   g.top_k = p.top_k;
-  // grouped: every expert may end in a ragged tile
-  const long tiles = (static_cast<long>(p.M) + kTile - 1) / kTile + (p.E > 0 ? std::min(p.E, p.M) : 0);
-  const dim3 grid((p.N + kTile - 1) / kTile, static_cast<unsigned>(tiles));
-#define LBQ_MX_GO(DT)                                                                             \
-  if (p.E > 0) hipLaunchKernelGGL((mx_gemm_kernel<DT, true>), grid, dim3(kThreads), 0, s, g);     \
-  else hipLaunchKernelGGL((mx_gemm_kernel<DT, false>), grid, dim3(kThreads), 0, s, g)
-  if (p.dtype == kF16) {
-    LBQ_MX_GO(kF16);
-  } else if (p.dtype == kBF16) {
-    LBQ_MX_GO(kBF16);
-  } else {
-    LBQ_MX_GO(kF32);
-  }
-#undef LBQ_MX_GO
+  const int dtype = r.slices > 1 ? kF32 : p.dtype;
+  hipError_t e;
+  if (r.bm == 256) e = launch_tiles<4, 4, 2, 2, 4>(g, dtype, r.slices, s);
+  else if (r.bm == 128) e = launch_tiles<2, 2, 2, 2, 3>(g, dtype, r.slices, s);
+  else e = launch_tiles<1, 2, 2, 2, 4>(g, dtype, r.slices, s);
+  if (e != hipSuccess || r.slices == 1) return e;
+  const long n = static_cast<long>(p.M) * p.N;
+  hipLaunchKernelGGL(mx_sum_kernel, dim3(static_cast<unsigned>(std::min<long>((n + 255) / 256, 2048))), dim3(256), 0, s,
+                     static_cast<const float *>(p.scratch), r.slices, n, p.dtype, p.y);
   return hipGetLastError();
 }
-
-size_t mx_gemm_scratch_bytes(const MxGemm &) { return 0; }
 
 }  // namespace lbq

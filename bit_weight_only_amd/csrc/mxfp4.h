@@ -62,6 +62,53 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
 }
 
+// The scale byte of a block whose largest magnitude has the bit pattern m (sign
+// off; patterns of one type order like their magnitudes, infinities and NaN
+// last). bf16 and fp32 values below the normal range have exponent field 0 and
+// get byte 0, like every block whose exponent clamps at -127.
+template <int DT>
+__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
+  int e;   // fp32's exponent field of the magnitude
+  bool finite;
+  if constexpr (DT == kF16) {
+    finite = m < 0x7C00u;
+    e = static_cast<int>(__float_as_uint(f16_bits_to_f32(m)) >> 23);
+  } else if constexpr (DT == kBF16) {
+    finite = m < 0x7F80u;
+    e = static_cast<int>(m >> 7);
+  } else {
+    finite = m < 0x7F800000u;
+    e = static_cast<int>(m >> 23);
+  }
+  return finite ? static_cast<uint32_t>(max(e - 2, 0)) : 255u;
+}
+
+// Codes of eight values divided by the power of two s: 16-bit pairs in four
+// words, or fp32. The conversion instruction divides, rounds once to nearest
+// even and saturates.
+template <int DT>
+__device__ __forceinline__ uint32_t codes8(const uint32_t w[4], float s) {
+  uint32_t o = 0;
+  if constexpr (DT == kF16) {
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, w[0]), s, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, w[1]), s, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, w[2]), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, w[3]), s, 3);
+  } else {
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, w[0]), s, 0);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, w[1]), s, 1);
+    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, w[2]), s, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, w[3]), s, 3);
+  }
+}
+__device__ __forceinline__ uint32_t codes8_f32(const float v[8], float s) {
+  uint32_t o = 0;
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[0], v[1], s, 0);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[2], v[3], s, 1);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[4], v[5], s, 2);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[6], v[7], s, 3);
+}
+
 // The value of one e2m1 code: magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6, sign in bit 3.
 __device__ __forceinline__ float e2m1_value(uint32_t c) {
   // exponent and mantissa dropped into fp32's fields make the value times

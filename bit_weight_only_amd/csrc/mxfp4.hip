@@ -25,12 +25,9 @@ using namespace mxfp4;
 
 constexpr int kThreads = 256;
 
-// Magnitude bits of eight values as 32-bit patterns that order like the
-// magnitudes, infinities and NaN last; and the fp32 exponent field of one.
+// Eight consecutive values of a row as they come from memory.
 template <int DT>
-struct In;
-template <>
-struct In<kF16> {
+struct In {
   uint4 v;
   static __device__ __forceinline__ In load(const void *p, size_t unit) {
     return In{static_cast<const uint4 *>(p)[unit]};
@@ -42,31 +39,9 @@ struct In<kF16> {
     for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7FFFu, (w[i] >> 16) & 0x7FFFu));
     return m;
   }
-  static __device__ __forceinline__ bool finite(uint32_t m) { return m < 0x7C00u; }
-  static __device__ __forceinline__ uint32_t exponent(uint32_t m) { return __float_as_uint(f16_bits_to_f32(m)) >> 23; }
   __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t o = 0;
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.x), s, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.y), s, 1);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.z), s, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(o, __builtin_bit_cast(half2_t, v.w), s, 3);
-  }
-};
-template <>
-struct In<kBF16> {
-  uint4 v;
-  static __device__ __forceinline__ In load(const void *p, size_t unit) {
-    return In{static_cast<const uint4 *>(p)[unit]};
-  }
-  __device__ __forceinline__ uint32_t mag() const { return In<kF16>{v}.mag(); }
-  static __device__ __forceinline__ bool finite(uint32_t m) { return m < 0x7F80u; }
-  static __device__ __forceinline__ uint32_t exponent(uint32_t m) { return m >> 7; }
-  __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t o = 0;
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.x), s, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.y), s, 1);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.z), s, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(o, __builtin_bit_cast(bf16x2_t, v.w), s, 3);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    return codes8<DT>(w, s);
   }
 };
 template <>
@@ -82,24 +57,11 @@ struct In<kF32> {
       m = max(m, max(__float_as_uint(a[i]) & 0x7FFFFFFFu, __float_as_uint(b[i]) & 0x7FFFFFFFu));
     return m;
   }
-  static __device__ __forceinline__ bool finite(uint32_t m) { return m < 0x7F800000u; }
-  static __device__ __forceinline__ uint32_t exponent(uint32_t m) { return m >> 23; }
   __device__ __forceinline__ uint32_t codes(float s) const {
-    uint32_t o = 0;
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, a[0], a[1], s, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, a[2], a[3], s, 1);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, b[0], b[1], s, 2);
-    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, b[2], b[3], s, 3);
+    const float v[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    return codes8_f32(v, s);
   }
 };
-
-// The scale byte of a block whose largest magnitude pattern is m. Values below
-// fp32's normal range have exponent field 0 and get byte 0 like every block
-// whose exponent clamps at -127.
-template <int DT>
-__device__ __forceinline__ uint32_t scale_byte(uint32_t m) {
-  return In<DT>::finite(m) ? static_cast<uint32_t>(max(static_cast<int>(In<DT>::exponent(m)) - 2, 0)) : 255u;
-}
 
 // ------------------------------------------------------------------ along rows
 
@@ -166,11 +128,7 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_t_kernel(const void *__r
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t o = 0;
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i], v[8 * i + 1], s, 0);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i + 2], v[8 * i + 3], s, 1);
-    o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i + 4], v[8 * i + 5], s, 2);
-    w[i] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, v[8 * i + 6], v[8 * i + 7], s, 3);
+    w[i] = codes8_f32(v + 8 * i, s);
     if (byte == 255u) w[i] = 0;
   }
   if (c0 + c < cols)

@@ -168,7 +168,8 @@ def test_matmul(L, dev, m, n, k, dtype):
 
 
 @pytest.mark.parametrize("m,n,k", [(700, 1100, 2176), (1030, 260, 4096), (5, 9000, 1024), (40, 70, 17408),
-                                   (600, 600, 8192)])
+                                   (600, 600, 8192), (100, 200, 4096), (130, 500, 14336), (77, 131, 17408),
+                                   (64, 640, 4096), (65, 8, 2176)])
 def test_matmul_larger(L, dev, m, n, k):
     import torch
 
@@ -201,7 +202,9 @@ def test_matmul_nan_blocks_and_wide_scales(L, dev, m, n, k):
 
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("m,n,k", [(1, 40, 128), (1, 4096, 4096), (3, 100, 1152), (4, 1000, 512), (5, 333, 2048),
-                                   (16, 512, 1024), (31, 200, 640), (65, 130, 384), (150, 700, 1536)])
+                                   (16, 512, 1024), (31, 200, 640), (65, 130, 384), (150, 700, 1536), (2, 9000, 256),
+                                   (16, 77, 17408), (9, 1100, 14336), (32, 2500, 8192), (20, 30, 4224),
+                                   (1, 17000, 2048)])
 def test_linear(L, dev, m, n, k, dtype):
     say(f"mx linear {m}x{n}x{k} {dtype}")
     x, x64 = _x(m, k, dtype, item=200 + m)
