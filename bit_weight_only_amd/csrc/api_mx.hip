@@ -42,18 +42,6 @@ lbq_status check_matmul(const lbq_mx *a, const lbq_mx *b) {
   return a->cols == b->cols ? LBQ_OK : LBQ_ERR_SHAPE;
 }
 
-// quantized activations of M rows, then the product's scratch
-struct LinearLayout {
-  size_t scales, scratch, total;
-};
-LinearLayout linear_layout(int M, int K, const MxGemm &g) {
-  LinearLayout l;
-  l.scales = round_up(code_bytes(M, K), kAlign);
-  l.scratch = l.scales + round_up(scale_bytes(M, K), kAlign);
-  l.total = l.scratch + mx_gemm_scratch_bytes(g);
-  return l;
-}
-
 MxGemm dense(int M, const lbq_mx *b, void *y, int32_t dtype) {
   MxGemm g{};
   g.b_codes = b->codes;
@@ -80,6 +68,22 @@ int stream_rows(const MxGemm &g) {
 // workgroups less than a launch: up to eight tokens (4096 -> 4096: 6.3 against
 // 7.1 us; 16 tokens 8.0 against 7.3), and few rows per expert.
 bool stream_quantizes(const MxGemm &g) { return stream_rows(g) > 0 && (g.E > 0 ? stream_rows(g) <= 16 : g.M <= 8); }
+
+size_t scratch_bytes(const MxGemm &g) { return stream_rows(g) > 0 ? 0 : mx_gemm_scratch_bytes(g); }
+
+// The quantized activations of M rows (none where the product takes x itself),
+// then the product's scratch.
+struct LinearLayout {
+  size_t scales = 0, scratch = 0, total = 0;
+};
+LinearLayout linear_layout(int M, int K, const MxGemm &g) {
+  LinearLayout l;
+  if (stream_quantizes(g)) return l;
+  l.scales = round_up(code_bytes(M, K), kAlign);
+  l.scratch = l.scales + round_up(scale_bytes(M, K), kAlign);
+  l.total = l.scratch + scratch_bytes(g);
+  return l;
+}
 
 hipError_t launch_product(const MxGemm &g, hipStream_t s) {
   const int rows = stream_rows(g);
@@ -178,7 +182,7 @@ lbq_status lbq_mx_matmul_workspace(const lbq_mx *a, const lbq_mx *b, size_t *byt
   if (!bytes) return LBQ_ERR_NULL;
   const lbq_status st = check_matmul(a, b);
   if (st != LBQ_OK) return st;
-  *bytes = mx_gemm_scratch_bytes(dense(a->rows, b, nullptr, LBQ_F32));
+  *bytes = scratch_bytes(dense(a->rows, b, nullptr, LBQ_F32));
   return LBQ_OK;
 }
 
@@ -189,7 +193,7 @@ lbq_status lbq_mx_matmul(const lbq_mx *a, const lbq_mx *b, void *y, int32_t dtyp
   if (!value_type(dtype)) return LBQ_ERR_FORMAT;
   if (a->rows == 0 || b->rows == 0) return LBQ_OK;
   MxGemm g = dense(a->rows, b, y, dtype);
-  const size_t need = mx_gemm_scratch_bytes(g);
+  const size_t need = scratch_bytes(g);
   if (!y || (need > 0 && !ws)) return LBQ_ERR_NULL;
   if (!aligned(y, 16) || !aligned(ws, 16)) return LBQ_ERR_ALIGN;
   if (ws_bytes < need) return LBQ_ERR_WORKSPACE;
@@ -215,10 +219,10 @@ lbq_status lbq_mx_linear_forward(const lbq_mx *w, const void *x, int32_t M, void
   if (!mx_shape(M, w->cols)) return LBQ_ERR_SHAPE;
   if (!half_type(dtype)) return LBQ_ERR_FORMAT;
   if (M == 0 || w->rows == 0) return LBQ_OK;
-  if (!x || !y || !ws) return LBQ_ERR_NULL;
-  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(ws, 16)) return LBQ_ERR_ALIGN;
   MxGemm g = dense(M, w, y, dtype);
   const LinearLayout l = linear_layout(M, w->cols, g);
+  if (!x || !y || (l.total > 0 && !ws)) return LBQ_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(ws, 16)) return LBQ_ERR_ALIGN;
   if (ws_bytes < l.total) return LBQ_ERR_WORKSPACE;
   return quantize_and_multiply(g, x, ws, l, static_cast<hipStream_t>(stream));
 }
@@ -239,7 +243,7 @@ lbq_status lbq_mx_grouped_forward(const lbq_mx *w, int32_t E, const void *x, int
   if (top_k < 1 || (!perm && M != T)) return LBQ_ERR_SHAPE;
   if (!half_type(dtype)) return LBQ_ERR_FORMAT;
   if (M == 0 || T == 0 || w->rows == 0) return LBQ_OK;
-  if (!x || !offsets || !y || !ws) return LBQ_ERR_NULL;
+  if (!x || !offsets || !y) return LBQ_ERR_NULL;
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(ws, 16) || !aligned(offsets, 4) || !aligned(perm, 4))
     return LBQ_ERR_ALIGN;
   MxGemm g = grouped(w, E, M, T);
@@ -249,6 +253,7 @@ lbq_status lbq_mx_grouped_forward(const lbq_mx *w, int32_t E, const void *x, int
   g.perm = perm;
   g.top_k = top_k;
   const LinearLayout l = linear_layout(M, w->cols, g);
+  if (l.total > 0 && !ws) return LBQ_ERR_NULL;
   if (ws_bytes < l.total) return LBQ_ERR_WORKSPACE;
   return quantize_and_multiply(g, x, ws, l, static_cast<hipStream_t>(stream));
 }

@@ -8,6 +8,7 @@ built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -444,94 +445,113 @@ def moe_from_host(packed: dict, bits, signs_hidden, signs_ffn, hidden: int, ffn:
 # ------------------------------------------------------------------ MXFP4 tensors, expert dispatch
 #
 # These take torch tensors as they are used in a program, so they check them:
-# one device, contiguous, the right type and shape (LbqError otherwise, nothing
-# launched). They run on the tensors' device whatever the current one is, on
-# the given stream or that device's current one; what they allocate belongs to
-# that stream.
+# one GPU, contiguous, the right type and shape (LbqError otherwise, nothing
+# launched). They run on the tensors' GPU whatever the current one is, on the
+# given stream or that GPU's current one; what they allocate belongs to that
+# stream. A call's own cost counts at one token (its kernels take 5 us), so the
+# usual path keeps to a few attribute reads, one or two allocations and one
+# foreign call.
 
 F16, BF16, F32 = 0, 1, 2
-_DTYPES: dict = {}
+_torch = None
+_dtypes: dict = {}
+
+
+def _ready():
+    """The library and torch, loaded on first use."""
+    global _torch
+    L = lib()
+    if _torch is None:
+        import torch
+
+        _dtypes.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
+        _torch = torch
+    return L
 
 
 def _dtype(t, where: str) -> int:
-    if not _DTYPES:
-        import torch
-
-        _DTYPES.update({torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32})
-    code = _DTYPES.get(t)
+    code = _dtypes.get(t)
     if code is None:
         raise LbqError(-8, f"{where}: {t}")
     return code
 
 
-def _need(where: str, device, dtype, shape, *tensors):
-    """Every tensor is contiguous, on device, of this dtype and (where given) shape."""
-    for t in tensors:
-        if t.device != device or not t.is_cuda:
-            raise LbqError(-8, f"{where}: tensors on {t.device} and {device}")
-        if t.dtype != dtype:
-            raise LbqError(-8, f"{where}: {t.dtype} instead of {dtype}")
-        if not t.is_contiguous() or (shape is not None and tuple(t.shape) != shape):
-            raise LbqError(-2, f"{where}: shape {tuple(t.shape)}, strides {t.stride()}")
+def _need(where: str, gpu: int, dtype, shape, t):
+    """t is contiguous, on that GPU, of this dtype and (where given) shape."""
+    if gpu < 0 or t.get_device() != gpu:
+        raise LbqError(-8, f"{where}: a tensor on {t.device}, another on {'no GPU' if gpu < 0 else gpu}")
+    if t.dtype is not dtype:
+        raise LbqError(-8, f"{where}: {t.dtype} instead of {dtype}")
+    if not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise LbqError(-2, f"{where}: shape {tuple(t.shape)}, strides {t.stride()}")
 
 
-class _On:
-    """The device and stream of a call: entered around its allocations and its launch."""
-
-    def __init__(self, device, stream):
-        self.device, self.stream, self.guards = device, stream, None
-
-    def __enter__(self):
-        import torch
-
-        if self.stream is not None:
-            if self.stream.device != self.device:
-                raise LbqError(-8, f"stream on {self.stream.device}, tensors on {self.device}")
-            self.guards = [torch.cuda.stream(self.stream)]   # also makes its device the current one
-        elif torch.cuda.current_device() != self.device.index:
-            self.guards = [torch.cuda.device(self.device)]
-        if self.guards:
-            self.guards[0].__enter__()
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.guards:
-            self.guards[0].__exit__(*exc)
+def _rows(where: str, t) -> int:
+    """The GPU of t, a contiguous matrix in a value type."""
+    if t.dim() != 2:
+        raise LbqError(-2, f"{where}: a matrix is needed, got {tuple(t.shape)}")
+    gpu = t.get_device()
+    _need(where, gpu, t.dtype, None, t)
+    return gpu
 
 
-def _workspace(ws, need: int, device, where: str):
-    import torch
+def _on(gpu: int, stream, go):
+    """go(raw stream) with that GPU current and its allocations on that stream."""
+    cuda = _torch._C
+    if stream is None:
+        if cuda._cuda_getDevice() == gpu:
+            return go(cuda._cuda_getCurrentRawStream(gpu))
+        with _torch.cuda.device(gpu):
+            return go(cuda._cuda_getCurrentRawStream(gpu))
+    if stream.device.index != gpu:
+        raise LbqError(-8, f"stream on {stream.device}, tensors on GPU {gpu}")
+    with _torch.cuda.stream(stream):
+        return go(stream.cuda_stream)
 
+
+@functools.lru_cache(maxsize=4096)
+def _query(name: str, args: tuple) -> int:
+    """A *_workspace query; sizes alone decide it. Tensors are given as (rows, cols)."""
+    need = ctypes.c_size_t()
+    p = ctypes.c_void_p(16)   # aligned stand-in: queries look at sizes only
+    views = [Mx(a[0], a[1], p, p) if isinstance(a, tuple) else a for a in args]
+    f = getattr(lib(), name)
+    _check(f(*[ctypes.byref(v) if isinstance(v, Mx) else v for v in views], ctypes.byref(need)), name)
+    return need.value
+
+
+def _workspace(ws, need: int, like, gpu: int, where: str):
+    """(pointer, bytes, owner) of a workspace: the caller's, or one of need bytes."""
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
-    if ws.device != device or not ws.is_contiguous():
+        if need == 0:
+            return None, 0, None
+        ws = like.new_empty(need, dtype=_torch.uint8)
+        return ws.data_ptr(), need, ws
+    if ws.get_device() != gpu or not ws.is_contiguous():
         raise LbqError(-5, where)
-    return ws
-
-
-def _bytes_of(t) -> int:
-    return t.numel() * t.element_size()
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
 class MxTensor:
     """An MXFP4 tensor (see include/lbq.h): codes uint8 [rows][cols/2] and scales uint8 [cols/128][rows][4]."""
 
-    __slots__ = ("rows", "cols", "codes", "scales", "_t")
+    __slots__ = ("rows", "cols", "codes", "scales", "gpu", "struct", "ref")
 
     def __init__(self, codes, scales):
-        import torch
+        _ready()
+        if codes.dim() != 2 or codes.shape[1] % 64 or codes.shape[1] == 0:
+            raise LbqError(-2, "MxTensor: codes are [rows][cols/2], cols a positive multiple of 128")
+        rows, half = codes.shape
+        gpu = codes.get_device()
+        _need("MxTensor", gpu, _torch.uint8, None, codes)
+        _need("MxTensor", gpu, _torch.uint8, (half // 64, rows, 4), scales)
+        self._set(codes, scales, rows, 2 * half, gpu)
 
-        if codes.dim() != 2:
-            raise LbqError(-2, "MxTensor: codes are [rows][cols/2]")
-        self.rows, self.cols = codes.shape[0], 2 * codes.shape[1]
-        _need("MxTensor", codes.device, torch.uint8, None, codes)
-        _need("MxTensor", codes.device, torch.uint8, (self.cols // 128, self.rows, 4), scales)
-        self.codes, self.scales = codes, scales
-        self._t = Mx(self.rows, self.cols, codes.data_ptr(), scales.data_ptr())
-
-    @property
-    def struct(self) -> Mx:
-        return self._t
+    def _set(self, codes, scales, rows, cols, gpu):
+        self.rows, self.cols, self.codes, self.scales, self.gpu = rows, cols, codes, scales, gpu
+        self.struct = Mx(rows, cols, codes.data_ptr(), scales.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+        return self
 
     @property
     def device(self):
@@ -540,226 +560,232 @@ class MxTensor:
 
 def mx_quantize(x, transpose: bool = False, stream=None) -> MxTensor:
     """lbq_mx_quantize (transpose: lbq_mx_quantize_t) of x [rows][cols] in float16, bfloat16 or float32."""
-    import torch
-
-    if x.dim() != 2:
-        raise LbqError(-2, "mx_quantize: x is [rows][cols]")
-    _need("mx_quantize", x.device, x.dtype, None, x)
+    L = _ready()
+    gpu = _rows("mx_quantize", x)
     dt = _dtype(x.dtype, "mx_quantize")
     rows, cols = x.shape
     tr, tc = (cols, -(-rows // 128) * 128) if transpose else (rows, cols)
     if tc % 128 or tc == 0:
         raise LbqError(-2, "mx_quantize: blocks run along a multiple of 128 values")
-    with _On(x.device, stream) as s:
-        codes = torch.empty((tr, tc // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((tc // 128, tr, 4), dtype=torch.uint8, device=x.device)
-        f = lib().lbq_mx_quantize_t if transpose else lib().lbq_mx_quantize
+
+    def go(s):
+        codes = x.new_empty((tr, tc // 2), dtype=_torch.uint8)
+        scales = x.new_empty((tc // 128, tr, 4), dtype=_torch.uint8)
+        f = L.lbq_mx_quantize_t if transpose else L.lbq_mx_quantize
         st = f(x.data_ptr(), dt, rows, cols, codes.data_ptr(), scales.data_ptr(), s)
-    _check(st, "lbq_mx_quantize_t" if transpose else "lbq_mx_quantize")
-    return MxTensor(codes, scales)
+        if st:
+            raise LbqError(st, "lbq_mx_quantize_t" if transpose else "lbq_mx_quantize")
+        return MxTensor.__new__(MxTensor)._set(codes, scales, tr, tc, gpu)
+    return _on(gpu, stream, go)
 
 
 def mx_dequantize(t: MxTensor, dtype, out=None, stream=None):
     """lbq_mx_dequantize: the values of t as a [rows][cols] tensor of dtype."""
-    import torch
-
+    L = _ready()
     dt = _dtype(dtype, "mx_dequantize")
-    with _On(t.device, stream) as s:
-        if out is None:
-            out = torch.empty((t.rows, t.cols), dtype=dtype, device=t.device)
-        else:
-            _need("mx_dequantize", t.device, dtype, (t.rows, t.cols), out)
-        st = lib().lbq_mx_dequantize(ctypes.byref(t.struct), out.data_ptr(), dt, s)
-    _check(st, "lbq_mx_dequantize")
-    return out
+    if out is not None:
+        _need("mx_dequantize", t.gpu, dtype, (t.rows, t.cols), out)
+
+    def go(s):
+        y = t.codes.new_empty((t.rows, t.cols), dtype=dtype) if out is None else out
+        st = L.lbq_mx_dequantize(t.ref, y.data_ptr(), dt, s)
+        if st:
+            raise LbqError(st, "lbq_mx_dequantize")
+        return y
+    return _on(t.gpu, stream, go)
 
 
 def mx_matmul(a: MxTensor, b: MxTensor, dtype=None, y=None, ws=None, stream=None):
     """lbq_mx_matmul: y [a.rows][b.rows] = A B^T in dtype (float32 if neither it nor y is given)."""
-    import torch
-
-    L, need = lib(), ctypes.c_size_t()
-    _check(L.lbq_mx_matmul_workspace(ctypes.byref(a.struct), ctypes.byref(b.struct), ctypes.byref(need)),
-           "lbq_mx_matmul_workspace")
-    if b.device != a.device:
+    L = _ready()
+    if a.gpu != b.gpu:
         raise LbqError(-8, f"mx_matmul: tensors on {a.device} and {b.device}")
-    dtype = dtype if dtype is not None else (torch.float32 if y is None else y.dtype)
+    if dtype is None:
+        dtype = _torch.float32 if y is None else y.dtype
     dt = _dtype(dtype, "mx_matmul")
-    with _On(a.device, stream) as s:
-        if y is None:
-            y = torch.empty((a.rows, b.rows), dtype=dtype, device=a.device)
-        else:
-            _need("mx_matmul", a.device, dtype, (a.rows, b.rows), y)
-        ws = _workspace(ws, need.value, a.device, "mx_matmul")
-        st = L.lbq_mx_matmul(ctypes.byref(a.struct), ctypes.byref(b.struct), y.data_ptr(), dt, ws.data_ptr(),
-                             _bytes_of(ws), s)
-    _check(st, "lbq_mx_matmul")
-    return y
+    if y is not None:
+        _need("mx_matmul", a.gpu, dtype, (a.rows, b.rows), y)
+    need = _query("lbq_mx_matmul_workspace", ((a.rows, a.cols), (b.rows, b.cols)))
+
+    def go(s):
+        out = a.codes.new_empty((a.rows, b.rows), dtype=dtype) if y is None else y
+        p, size, keep = _workspace(ws, need, a.codes, a.gpu, "mx_matmul")
+        st = L.lbq_mx_matmul(a.ref, b.ref, out.data_ptr(), dt, p, size, s)
+        if st:
+            raise LbqError(st, "lbq_mx_matmul")
+        return out
+    return _on(a.gpu, stream, go)
 
 
 def mx_linear_forward(w: MxTensor, x, y=None, ws=None, stream=None):
     """lbq_mx_linear_forward: y [M][w.rows] = Q(x) W^T, x [M][w.cols] in float16 or bfloat16, y in x's type."""
-    import torch
-
+    L = _ready()
+    dtype = x.dtype
+    dt = _dtype(dtype, "mx_linear_forward")
+    _need("mx_linear_forward", w.gpu, dtype, None, x)
     if x.dim() != 2 or x.shape[1] != w.cols:
         raise LbqError(-2, "mx_linear_forward: x is [M][w.cols]")
     M = x.shape[0]
-    dt = _dtype(x.dtype, "mx_linear_forward")
-    _need("mx_linear_forward", w.device, x.dtype, None, x)
-    L, need = lib(), ctypes.c_size_t()
-    _check(L.lbq_mx_linear_workspace(ctypes.byref(w.struct), M, ctypes.byref(need)), "lbq_mx_linear_workspace")
-    with _On(w.device, stream) as s:
-        if y is None:
-            y = torch.empty((M, w.rows), dtype=x.dtype, device=w.device)
-        else:
-            _need("mx_linear_forward", w.device, x.dtype, (M, w.rows), y)
-        ws = _workspace(ws, need.value, w.device, "mx_linear_forward")
-        st = L.lbq_mx_linear_forward(ctypes.byref(w.struct), x.data_ptr(), M, y.data_ptr(), dt, ws.data_ptr(),
-                                     _bytes_of(ws), s)
-    _check(st, "lbq_mx_linear_forward")
-    return y
+    if y is not None:
+        _need("mx_linear_forward", w.gpu, dtype, (M, w.rows), y)
+    need = _query("lbq_mx_linear_workspace", ((w.rows, w.cols), M))
+
+    def go(s):
+        out = x.new_empty((M, w.rows)) if y is None else y
+        p, size, keep = _workspace(ws, need, x, w.gpu, "mx_linear_forward")
+        st = L.lbq_mx_linear_forward(w.ref, x.data_ptr(), M, out.data_ptr(), dt, p, size, s)
+        if st:
+            raise LbqError(st, "lbq_mx_linear_forward")
+        return out
+    return _on(w.gpu, stream, go)
 
 
 def mx_grouped_forward(w: MxTensor, E: int, x, offsets, perm=None, top_k: int = 1, y=None, ws=None, stream=None):
     """lbq_mx_grouped_forward: w holds E experts of w.rows / E rows; y [T][w.rows / E], T the length of perm
     (of x without perm). Rows of y from offsets[E] on are left as they were (uninitialised if y is not given)."""
-    import torch
-
+    L = _ready()
+    where, gpu, dtype = "mx_grouped_forward", w.gpu, x.dtype
+    dt = _dtype(dtype, where)
+    _need(where, gpu, dtype, None, x)
     if x.dim() != 2 or x.shape[1] != w.cols:
         raise LbqError(-2, "mx_grouped_forward: x is [M][w.cols]")
     if E < 1 or w.rows % E:
         raise LbqError(-2, "mx_grouped_forward: w holds E experts of equal rows")
     M, N = x.shape[0], w.rows // E
-    T = M if perm is None else perm.numel()
-    dt = _dtype(x.dtype, "mx_grouped_forward")
-    _need("mx_grouped_forward", w.device, x.dtype, None, x)
-    _need("mx_grouped_forward", w.device, torch.int32, (E + 1,), offsets)
+    _need(where, gpu, _torch.int32, (E + 1,), offsets)
+    T = M
     if perm is not None:
-        _need("mx_grouped_forward", w.device, torch.int32, None, perm)
-    L, need = lib(), ctypes.c_size_t()
-    _check(L.lbq_mx_grouped_workspace(ctypes.byref(w.struct), E, M, T, ctypes.byref(need)),
-           "lbq_mx_grouped_workspace")
-    with _On(w.device, stream) as s:
-        if y is None:
-            y = torch.empty((T, N), dtype=x.dtype, device=w.device)
-        else:
-            _need("mx_grouped_forward", w.device, x.dtype, (T, N), y)
-        ws = _workspace(ws, need.value, w.device, "mx_grouped_forward")
-        st = L.lbq_mx_grouped_forward(ctypes.byref(w.struct), E, x.data_ptr(), M, offsets.data_ptr(),
-                                      None if perm is None else perm.data_ptr(), top_k, T, y.data_ptr(), dt,
-                                      ws.data_ptr(), _bytes_of(ws), s)
-    _check(st, "lbq_mx_grouped_forward")
-    return y
+        _need(where, gpu, _torch.int32, None, perm)
+        T = perm.numel()
+    if y is not None:
+        _need(where, gpu, dtype, (T, N), y)
+    need = _query("lbq_mx_grouped_workspace", ((w.rows, w.cols), E, M, T))
+
+    def go(s):
+        out = x.new_empty((T, N)) if y is None else y
+        p, size, keep = _workspace(ws, need, x, gpu, where)
+        st = L.lbq_mx_grouped_forward(w.ref, E, x.data_ptr(), M, offsets.data_ptr(),
+                                      None if perm is None else perm.data_ptr(), top_k, T, out.data_ptr(), dt, p, size,
+                                      s)
+        if st:
+            raise LbqError(st, "lbq_mx_grouped_forward")
+        return out
+    return _on(gpu, stream, go)
 
 
 def moe_sort(ids, E: int, stream=None):
     """lbq_moe_sort of ids int32 [M][top_k]: (counts [E], offsets [E+1], perm [M*top_k], pos [M][top_k])."""
-    import torch
-
+    L = _ready()
+    gpu = ids.get_device()
+    _need("moe_sort", gpu, _torch.int32, None, ids)
     if ids.dim() != 2:
         raise LbqError(-2, "moe_sort: ids are [M][top_k]")
-    _need("moe_sort", ids.device, torch.int32, None, ids)
     M, k = ids.shape
-    L, need = lib(), ctypes.c_size_t()
-    _check(L.lbq_moe_sort_workspace(M, E, k, ctypes.byref(need)), "lbq_moe_sort_workspace")
-    with _On(ids.device, stream) as s:
-        n = M * k
-        sizes = [n, n, E, E + 1, need.value // 4]
-        pos, perm, counts, offsets, ws = torch.empty(sum(sizes), dtype=torch.int32, device=ids.device).split(sizes)
+    need = _query("lbq_moe_sort_workspace", (M, E, k))
+    n = M * k
+
+    def go(s):
+        pos = ids.new_empty((M, k))
+        perm, counts, offsets, ws = ids.new_empty(n + 2 * E + 1 + need // 4).split((n, E, E + 1, need // 4))
         st = L.lbq_moe_sort(ids.data_ptr(), M, E, k, counts.data_ptr(), offsets.data_ptr(), perm.data_ptr(),
-                            pos.data_ptr(), ws.data_ptr(), need.value, s)
-    _check(st, "lbq_moe_sort")
-    return counts, offsets, perm, pos.view(M, k)
+                            pos.data_ptr(), ws.data_ptr(), need, s)
+        if st:
+            raise LbqError(st, "lbq_moe_sort")
+        return counts, offsets, perm, pos
+    return _on(gpu, stream, go)
 
 
-def _places(where: str, pos, device, *weights):
-    import torch
-
+def _places(where: str, gpu: int, pos):
+    _need(where, gpu, _torch.int32, None, pos)
     if pos.dim() != 2:
         raise LbqError(-2, f"{where}: pos is [M][top_k]")
-    _need(where, device, torch.int32, None, pos)
-    if weights:
-        _need(where, device, torch.float32, tuple(pos.shape), *weights)
     return pos.shape
-
-
-def _rows(where: str, x, rows=None):
-    if x.dim() != 2 or (rows is not None and x.shape[0] != rows):
-        raise LbqError(-2, f"{where}: rows {tuple(x.shape)}")
-    _need(where, x.device, x.dtype, None, x)
-    return _dtype(x.dtype, where)
 
 
 def moe_gather(x, pos, out=None, stream=None):
     """lbq_moe_gather: out[pos[t][j]] = x[t]. out [T][H] is [M * top_k][H] if not given; rows that no place
     names are left as they were (uninitialised if out is not given)."""
-    import torch
+    L = _ready()
+    gpu = _rows("moe_gather", x)
+    dt = _dtype(x.dtype, "moe_gather")
+    M, k = _places("moe_gather", gpu, pos)
+    H = x.shape[1]
+    if x.shape[0] != M:
+        raise LbqError(-2, f"moe_gather: {x.shape[0]} rows, places of {M}")
+    if out is not None:
+        _need("moe_gather", gpu, x.dtype, (out.shape[0], H), out)
 
-    M, k = _places("moe_gather", pos, x.device)
-    dt, H = _rows("moe_gather", x, M), x.shape[-1]
-    with _On(x.device, stream) as s:
-        if out is None:
-            out = torch.empty((M * k, H), dtype=x.dtype, device=x.device)
-        else:
-            _need("moe_gather", x.device, x.dtype, (out.shape[0], H), out)
-        st = lib().lbq_moe_gather(x.data_ptr(), dt, M, H, pos.data_ptr(), k, out.shape[0], out.data_ptr(), s)
-    _check(st, "lbq_moe_gather")
-    return out
+    def go(s):
+        o = x.new_empty((M * k, H)) if out is None else out
+        st = L.lbq_moe_gather(x.data_ptr(), dt, M, H, pos.data_ptr(), k, o.shape[0], o.data_ptr(), s)
+        if st:
+            raise LbqError(st, "lbq_moe_gather")
+        return o
+    return _on(gpu, stream, go)
 
 
 def moe_gather_backward(d_out, pos, dx=None, stream=None):
     """lbq_moe_gather_backward: dx[t] = sum_j d_out[pos[t][j]]."""
-    import torch
-
-    M, k = _places("moe_gather_backward", pos, d_out.device)
-    dt = _rows("moe_gather_backward", d_out)
+    L = _ready()
+    gpu = _rows("moe_gather_backward", d_out)
+    dt = _dtype(d_out.dtype, "moe_gather_backward")
+    M, k = _places("moe_gather_backward", gpu, pos)
     T, H = d_out.shape
-    with _On(d_out.device, stream) as s:
-        if dx is None:
-            dx = torch.empty((M, H), dtype=d_out.dtype, device=d_out.device)
-        else:
-            _need("moe_gather_backward", d_out.device, d_out.dtype, (M, H), dx)
-        st = lib().lbq_moe_gather_backward(d_out.data_ptr(), dt, T, H, pos.data_ptr(), M, k, dx.data_ptr(), s)
-    _check(st, "lbq_moe_gather_backward")
-    return dx
+    if dx is not None:
+        _need("moe_gather_backward", gpu, d_out.dtype, (M, H), dx)
+
+    def go(s):
+        o = d_out.new_empty((M, H)) if dx is None else dx
+        st = L.lbq_moe_gather_backward(d_out.data_ptr(), dt, T, H, pos.data_ptr(), M, k, o.data_ptr(), s)
+        if st:
+            raise LbqError(st, "lbq_moe_gather_backward")
+        return o
+    return _on(gpu, stream, go)
 
 
 def moe_combine(o, pos, weights, y=None, stream=None):
     """lbq_moe_combine: y[t] = sum_j weights[t][j] o[pos[t][j]] (weights float32 [M][top_k])."""
-    import torch
-
-    M, k = _places("moe_combine", pos, o.device, weights)
-    dt = _rows("moe_combine", o)
+    L = _ready()
+    gpu = _rows("moe_combine", o)
+    dt = _dtype(o.dtype, "moe_combine")
+    M, k = _places("moe_combine", gpu, pos)
+    _need("moe_combine", gpu, _torch.float32, (M, k), weights)
     T, H = o.shape
-    with _On(o.device, stream) as s:
-        if y is None:
-            y = torch.empty((M, H), dtype=o.dtype, device=o.device)
-        else:
-            _need("moe_combine", o.device, o.dtype, (M, H), y)
-        st = lib().lbq_moe_combine(o.data_ptr(), dt, T, H, pos.data_ptr(), weights.data_ptr(), M, k, y.data_ptr(), s)
-    _check(st, "lbq_moe_combine")
-    return y
+    if y is not None:
+        _need("moe_combine", gpu, o.dtype, (M, H), y)
+
+    def go(s):
+        out = o.new_empty((M, H)) if y is None else y
+        st = L.lbq_moe_combine(o.data_ptr(), dt, T, H, pos.data_ptr(), weights.data_ptr(), M, k, out.data_ptr(), s)
+        if st:
+            raise LbqError(st, "lbq_moe_combine")
+        return out
+    return _on(gpu, stream, go)
 
 
 def moe_combine_backward(dy, o, pos, weights, d_o=None, d_weights=None, stream=None):
     """lbq_moe_combine_backward: (d_o [T][H], d_weights float32 [M][top_k]). Rows of d_o that no place names are
     left as they were (uninitialised if d_o is not given)."""
-    import torch
-
-    M, k = _places("moe_combine_backward", pos, o.device, weights)
-    dt = _rows("moe_combine_backward", o)
+    L = _ready()
+    where = "moe_combine_backward"
+    gpu = _rows(where, o)
+    dt = _dtype(o.dtype, where)
+    M, k = _places(where, gpu, pos)
+    _need(where, gpu, _torch.float32, (M, k), weights)
     T, H = o.shape
-    _need("moe_combine_backward", o.device, o.dtype, (M, H), dy)
-    with _On(o.device, stream) as s:
-        if d_o is None:
-            d_o = torch.empty_like(o)
-        else:
-            _need("moe_combine_backward", o.device, o.dtype, (T, H), d_o)
-        if d_weights is None:
-            d_weights = torch.empty((M, k), dtype=torch.float32, device=o.device)
-        else:
-            _need("moe_combine_backward", o.device, torch.float32, (M, k), d_weights)
-        st = lib().lbq_moe_combine_backward(dy.data_ptr(), o.data_ptr(), dt, T, H, pos.data_ptr(), weights.data_ptr(),
-                                            M, k, d_o.data_ptr(), d_weights.data_ptr(), s)
-    _check(st, "lbq_moe_combine_backward")
-    return d_o, d_weights
+    _need(where, gpu, o.dtype, (M, H), dy)
+    if d_o is not None:
+        _need(where, gpu, o.dtype, (T, H), d_o)
+    if d_weights is not None:
+        _need(where, gpu, _torch.float32, (M, k), d_weights)
+
+    def go(s):
+        go_, gw = o.new_empty((T, H)) if d_o is None else d_o, d_weights
+        if gw is None:
+            gw = weights.new_empty((M, k))
+        st = L.lbq_moe_combine_backward(dy.data_ptr(), o.data_ptr(), dt, T, H, pos.data_ptr(), weights.data_ptr(), M,
+                                        k, go_.data_ptr(), gw.data_ptr(), s)
+        if st:
+            raise LbqError(st, "lbq_moe_combine_backward")
+        return go_, gw
+    return _on(gpu, stream, go)

@@ -459,7 +459,8 @@ lbq_status lbq_mx_matmul_workspace(const lbq_mx *a, const lbq_mx *b, size_t *byt
 lbq_status lbq_mx_matmul(const lbq_mx *a, const lbq_mx *b, void *y, int32_t dtype, void *ws, size_t ws_bytes,
                          void *stream);
 
-/* Workspace bytes of lbq_mx_linear_forward for M tokens (host query). */
+/* Workspace bytes of lbq_mx_linear_forward for M tokens (host query; 0 where the
+ * product quantizes x on the way: ws may then be NULL). */
 lbq_status lbq_mx_linear_workspace(const lbq_mx *w, int32_t M, size_t *bytes);
 
 /* y [M][w.rows] (dtype) = Q(x) W^T: x [M][w.cols] (dtype LBQ_F16 or LBQ_BF16)

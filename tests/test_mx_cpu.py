@@ -66,23 +66,24 @@ def test_product_refusals(L):
     assert lib.lbq_mx_matmul(a, b, P, 5, P, 1 << 40, None) == FORMAT
     assert lib.lbq_mx_matmul(_mx(L, 0, 256, None, None), b, None, 0, None, 0, None) == OK
 
-    assert lib.lbq_mx_linear_workspace(b, 3, ctypes.byref(n)) == OK and n.value >= 3 * (128 + 8)
+    assert lib.lbq_mx_linear_workspace(b, 200, ctypes.byref(n)) == OK and n.value >= 200 * (128 + 8)
     assert lib.lbq_mx_linear_workspace(b, -1, ctypes.byref(n)) == SHAPE
-    assert lib.lbq_mx_linear_forward(b, P, 3, P, 0, P, n.value - 1, None) == WORKSPACE
-    assert lib.lbq_mx_linear_forward(b, P, 3, P, 2, P, n.value, None) == FORMAT      # fp32 activations
-    assert lib.lbq_mx_linear_forward(b, None, 3, P, 0, P, n.value, None) == NULL
-    assert lib.lbq_mx_linear_forward(b, P, 3, P, 0, None, n.value, None) == NULL
-    assert lib.lbq_mx_linear_forward(b, P, 3, P, 0, P + 8, n.value, None) == ALIGN
+    assert lib.lbq_mx_linear_forward(b, P, 200, P, 0, P, n.value - 1, None) == WORKSPACE
+    assert lib.lbq_mx_linear_forward(b, P, 200, P, 2, P, n.value, None) == FORMAT      # fp32 activations
+    assert lib.lbq_mx_linear_forward(b, None, 200, P, 0, P, n.value, None) == NULL
+    assert lib.lbq_mx_linear_forward(b, P, 200, P, 0, None, n.value, None) == NULL
+    assert lib.lbq_mx_linear_forward(b, P, 200, P, 0, P + 8, n.value, None) == ALIGN
     assert lib.lbq_mx_linear_forward(b, None, 0, None, 0, None, 0, None) == OK
 
     def grouped(w=b, E=3, M=4, T=8, x=P, off=P, perm=P, k=2, y=P, dt=0, ws=P, nb=1 << 40):
         return lib.lbq_mx_grouped_forward(w, E, x, M, off, perm, k, T, y, dt, ws, nb, None)
-    assert lib.lbq_mx_grouped_workspace(b, 3, 4, 8, ctypes.byref(n)) == OK
+    assert lib.lbq_mx_grouped_workspace(b, 3, 200, 400, ctypes.byref(n)) == OK and n.value >= 200 * (128 + 8)
+    assert grouped(M=200, T=400, nb=n.value - 1) == WORKSPACE and grouped(M=200, T=400, ws=None) == NULL
     assert grouped(E=4) == SHAPE and grouped(E=0) == SHAPE and grouped(k=0) == SHAPE
     assert grouped(w=_mx(L, 2050, 128), E=1025) == SHAPE
     assert grouped(perm=None) == SHAPE                             # without perm x has T rows
     assert grouped(dt=2) == FORMAT and grouped(off=None) == NULL and grouped(y=P + 2) == ALIGN
-    assert grouped(off=P + 2) == ALIGN and grouped(nb=n.value - 1) == WORKSPACE
+    assert grouped(off=P + 2) == ALIGN and grouped(perm=P + 2) == ALIGN
     assert grouped(M=0, x=None, off=None, y=None, ws=None, T=0) == OK
 
 
