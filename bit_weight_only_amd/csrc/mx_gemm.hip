@@ -39,21 +39,23 @@ struct GemmArgs {
 // weight rows. The weight is the instruction's first operand, so a lane's four
 // consecutive result registers are four neighbouring outputs of one token.
 //
-// Stages of one 128-group of K (64 bytes a row, and a scale word a row) go
-// global -> LDS by asynchronous copies into a ring of RING buffers. In stage s
-// the copies of stages s + 2 .. s + RING - 1 are in flight and the operands of
-// the next 64-long step are read from LDS while one step is multiplied, across
-// the stage's border too: stage s starts when s + 1 has landed. One barrier per
-// stage. Vector v (16 bytes) of row r lies in slot v ^ ((r >> 2) & 3) of the
-// row: the sixteen rows that a quarter of an operand read touches fall in
-// sixteen distinct 16-byte bank groups.
+// Stages of one 128-group of K (64 bytes and a scale word a row) go global -> LDS
+// by asynchronous copies into a ring of RING buffers. In stage s the copies of
+// stages s + 2 .. s + RING - 1 are in flight and the operands of the next
+// 64-long step are read from LDS while one step is multiplied, across the stage's
+// border too: stage s starts when s + 1 has landed. One barrier per stage. Vector
+// v (16 bytes) of row r lies in slot v ^ ((r >> 2) & 3) of the row: the sixteen
+// rows that a quarter of an operand read touches fall in sixteen distinct 16-byte
+// bank groups. Stages of two groups (128 bytes a row) leave fewer workgroups per
+// compute unit and measured slower (256 experts, 2048 tokens: 193 -> 210 us).
 template <int MB, int NB, int GM, int GN>
 struct Tile {
-  static constexpr int kThreads = 64 * GM * GN;
+  static constexpr int kThreads = 64 * GM * GN, kVecs = 4;   // 16-byte vectors of a row's stage
   static constexpr int kM = 32 * MB * GM, kN = 32 * NB * GN;
-  static constexpr int kCopiesA = kM * 4 / kThreads, kCopiesB = kN * 4 / kThreads;
-  static_assert(kCopiesA * kThreads == kM * 4 && kCopiesB * kThreads == kN * 4, "whole copies");
-  // scale words: where a tile has fewer rows than threads, waves copy the same words
+  static constexpr int kCopiesA = kM * kVecs / kThreads, kCopiesB = kN * kVecs / kThreads;
+  static_assert(kCopiesA * kThreads == kM * kVecs && kCopiesB * kThreads == kN * kVecs, "whole copies");
+  // scale words: where a tile has fewer rows than threads, the waves without rows
+  // copy one word (so that every wave has the same number of copies in flight)
   static constexpr int kScalesA = kM < kThreads ? 1 : kM / kThreads, kScalesB = kN < kThreads ? 1 : kN / kThreads;
   static_assert(kM % 64 == 0 && kN % 64 == 0, "a wave copies 64 scale words");
   static constexpr int kLoads = kCopiesA + kCopiesB + kScalesA + kScalesB;   // per wave and stage
@@ -63,17 +65,13 @@ struct Tile {
 // from copies in flight into another.
 template <class Tl>
 struct Stage {
-  uint4 a[Tl::kM * 4], b[Tl::kN * 4];
-  uint32_t sa[Tl::kM], sb[Tl::kN];
+  uint4 a[Tl::kM * Tl::kVecs], b[Tl::kN * Tl::kVecs];
+  uint32_t sa[Tl::kM], sb[Tl::kN], idle[64];
 };
 
-// Workgroup number -> (row tile, column tile). Workgroups go to the eight XCDs
-// in turn, each with an L2 of its own: XCD i gets the i-th eighth of the tile
-// sequence, which walks `group` row tiles down each column before the next.
-__device__ __forceinline__ void place_tile(int pid, int tm, int tn, int group, int &m, int &n) {
-  const int total = tm * tn, q = total / 8, rem = total % 8;
-  const int xcd = pid & 7;
-  const int id = xcd * q + min(xcd, rem) + (pid >> 3);
+// Tile number -> (row tile, column tile): `group` row tiles down each column
+// before the next.
+__device__ __forceinline__ void place_tile(int id, int tm, int tn, int group, int &m, int &n) {
   const int width = group * tn, g = id / width, first = g * group;
   const int rows = min(tm - first, group), in = id - g * width;
   m = first + in % rows;
@@ -127,26 +125,32 @@ __device__ __forceinline__ void store_block(void *y, size_t row, bool ok, int n0
 template <int MB, int NB, int GM, int GN, int RING, int DT, bool GROUPED>
 __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
   using Tl = Tile<MB, NB, GM, GN>;
+  using Buffer = Stage<Tl>;
   constexpr int TH = Tl::kThreads, CA = Tl::kCopiesA, CB = Tl::kCopiesB;
   static_assert(RING == 3 || RING == 4, "ring");
-  __shared__ __attribute__((aligned(16))) Stage<Tl> q0, q1, q2, q3;
+  __shared__ __attribute__((aligned(16))) Buffer q0, q1, q2, q3;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
-  int tile_m, tile_n;
-  place_tile(blockIdx.x, g.tiles_m, g.tiles_n, 4, tile_m, tile_n);
-  int i0 = tile_m * Tl::kM, n_rows = g.M - i0, e = 0;
+  int tile_m, tile_n, i0, n_rows, e = 0;
   if constexpr (GROUPED) {
-    const GroupTile t = find_tile(g.offsets, g.E, g.M, Tl::kM, tile_m);
-    if (t.n == 0) return;
+    const GroupTiles tiles(g.offsets, g.E, g.M, Tl::kM);
+    const int tm = tiles.total(), id = xcd_order(blockIdx.x, tm * g.tiles_n);
+    if (id < 0) return;
+    place_tile(id, tm, g.tiles_n, 4, tile_m, tile_n);
+    const GroupTile t = tiles.find(tile_m);
     i0 = t.i0;
     n_rows = t.n;
     e = t.e;
+  } else {
+    place_tile(xcd_order(blockIdx.x, g.tiles_m * g.tiles_n), g.tiles_m, g.tiles_n, 4, tile_m, tile_n);
+    i0 = tile_m * Tl::kM;
+    n_rows = g.M - i0;
   }
   const int col0 = tile_n * Tl::kN;
-  // K slice blockIdx.y: groups [first, first + G)
+  // K slice blockIdx.y: S stages from stage `first` on
   const int all = g.K / kGroup, first = static_cast<int>(static_cast<long>(all) * blockIdx.y / gridDim.y);
-  const int G = static_cast<int>(static_cast<long>(all) * (blockIdx.y + 1) / gridDim.y) - first;
+  const int S = static_cast<int>(static_cast<long>(all) * (blockIdx.y + 1) / gridDim.y) - first;
   // activation row of list row i0 + i (rows past the end repeat the last one;
   // their results are not stored)
   auto act_row = [&](int i) {
@@ -156,35 +160,38 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
     return static_cast<size_t>(min(max(ia, 0), g.a_rows - 1));
   };
   auto weight_row = [&](int n) { return static_cast<size_t>(e) * g.N + min(col0 + n, g.N - 1); };
-  const int vec = (tid & 3) ^ ((tid >> 4) & 3);
+  constexpr int kVecs = Tl::kVecs;
+  const int vec = (tid % kVecs) ^ ((tid >> 4) % kVecs);
   const uint8_t *pa[CA], *pb[CB];
 #pragma unroll
-  for (int it = 0; it < CA; ++it) 
-    pa[it] = g.a_codes + act_row(it * (TH / 4) + (tid >> 2)) * (g.K / 2) + 64 * first + 16 * vec;
+  for (int it = 0; it < CA; ++it)
+    pa[it] = g.a_codes + act_row((it * TH + tid) / kVecs) * (g.K / 2) + 64 * first + 16 * vec;
 #pragma unroll
-  for (int it = 0; it < CB; ++it) 
-    pb[it] = g.b_codes + weight_row(it * (TH / 4) + (tid >> 2)) * (g.K / 2) + 64 * first + 16 * vec;
+  for (int it = 0; it < CB; ++it)
+    pb[it] = g.b_codes + weight_row((it * TH + tid) / kVecs) * (g.K / 2) + 64 * first + 16 * vec;
   const uint32_t *psa[Tl::kScalesA], *psb[Tl::kScalesB];
 #pragma unroll
-  for (int it = 0; it < Tl::kScalesA; ++it) 
-    psa[it] = g.a_scales + static_cast<size_t>(first) * g.a_rows + act_row((it * TH + tid) % Tl::kM);
+  for (int it = 0; it < Tl::kScalesA; ++it)
+    psa[it] = g.a_scales + static_cast<size_t>(first) * g.a_rows + act_row(it * TH + tid < Tl::kM ? it * TH + tid : 0);
 #pragma unroll
-  for (int it = 0; it < Tl::kScalesB; ++it) 
-    psb[it] = g.b_scales + static_cast<size_t>(first) * g.b_rows + weight_row((it * TH + tid) % Tl::kN);
+  for (int it = 0; it < Tl::kScalesB; ++it)
+    psb[it] = g.b_scales + static_cast<size_t>(first) * g.b_rows + weight_row(it * TH + tid < Tl::kN ? it * TH + tid : 0);
 
   // copies of the next stage in line; past the last one it repeats, so that
   // every stage has the same number of copies in flight (never multiplied)
   int ahead = 0;
-  auto issue = [&](Stage<Tl> &q) {
+  auto issue = [&](Buffer &q) {
 #pragma unroll
     for (int it = 0; it < CA; ++it) copy16_to_lds(pa[it], q.a + it * TH + wave * 64);
 #pragma unroll
     for (int it = 0; it < CB; ++it) copy16_to_lds(pb[it], q.b + it * TH + wave * 64);
 #pragma unroll
-    for (int it = 0; it < Tl::kScalesA; ++it) copy4_to_lds(psa[it], q.sa + (it * TH + wave * 64) % Tl::kM);
+    for (int it = 0; it < Tl::kScalesA; ++it)
+      copy4_to_lds(psa[it], it * TH + wave * 64 < Tl::kM ? q.sa + it * TH + wave * 64 : q.idle);
 #pragma unroll
-    for (int it = 0; it < Tl::kScalesB; ++it) copy4_to_lds(psb[it], q.sb + (it * TH + wave * 64) % Tl::kN);
-    const bool more = ++ahead < G;
+    for (int it = 0; it < Tl::kScalesB; ++it)
+      copy4_to_lds(psb[it], it * TH + wave * 64 < Tl::kN ? q.sb + it * TH + wave * 64 : q.idle);
+    const bool more = ++ahead < S;
     const int by = more ? 64 : 0;
     const size_t da = more ? g.a_rows : 0, db = more ? g.b_rows : 0;
 #pragma unroll
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
   };
 
   const int wm = (wave / GN) * 32 * MB, wn = (wave % GN) * 32 * NB;
-  const int key = (r >> 2) & 3;
+  const int key = (r >> 2) % kVecs;
   v16f_t acc[MB][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
@@ -210,56 +217,55 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
   struct Step {
     v8i_t a[MB], b[NB];
   };
-  uint32_t va[MB], vb[NB];   // scale words: bytes 0 and 2 are this lane's blocks of the two steps
-  auto read = [&](Step &f, const Stage<Tl> &q, int s) {
+  struct Scales {   // words of one group: bytes 0 and 2 are this lane's blocks of its two steps
+    uint32_t a[MB], b[NB];
+  };
+  auto read = [&](Step &f, const Buffer &q, int s) {
     const int at = (2 * s + h) ^ key;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) f.b[j] = operand(q.b[(wn + 32 * j + r) * 4 + at]);
+    for (int j = 0; j < NB; ++j) f.b[j] = operand(q.b[(wn + 32 * j + r) * kVecs + at]);
 #pragma unroll
-    for (int i = 0; i < MB; ++i) f.a[i] = operand(q.a[(wm + 32 * i + r) * 4 + at]);
+    for (int i = 0; i < MB; ++i) f.a[i] = operand(q.a[(wm + 32 * i + r) * kVecs + at]);
   };
-  auto read_scales = [&](const Stage<Tl> &q) {
+  auto read_scales = [&](Scales &v, const Buffer &q) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) va[i] = q.sa[wm + 32 * i + r] >> (8 * h);
+    for (int i = 0; i < MB; ++i) v.a[i] = q.sa[wm + 32 * i + r] >> (8 * h);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) vb[j] = q.sb[wn + 32 * j + r] >> (8 * h);
+    for (int j = 0; j < NB; ++j) v.b[j] = q.sb[wn + 32 * j + r] >> (8 * h);
   };
-#define LBQ_MX_STEP(F, SEL, VA, VB)                                                                             \
+#define LBQ_MX_STEP(F, SEL, V)                                                                                  \
   do {                                                                                                          \
     _Pragma("unroll") for (int i = 0; i < MB; ++i) _Pragma("unroll") for (int j = 0; j < NB; ++j) acc[i][j] =   \
         __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(F.b[j], F.a[i], acc[i][j], 4, 4, SEL,                   \
-                                                        static_cast<int>(VB[j]), SEL, static_cast<int>(VA[i])); \
+                                                        static_cast<int>(V.b[j]), SEL, static_cast<int>(V.a[i])); \
   } while (0)
 
   Step f0, f1;
-  auto landed = [&]() {
-    // this wave's copies of the stage after the current one have landed; after
-    // the barrier every wave's, and every wave is done with the stage before
-    wait_vm_lds<(RING - 3) * Tl::kLoads>();
+  Scales v0, v1;
+  // After a wait for its own copies: every wave's have landed, and every wave is
+  // done with its reads so far.
+  auto meet = [&]() {
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
-  // stage in cur, its first step's operands in f0; free takes the copies
-  auto stage = [&](const Stage<Tl> &cur, const Stage<Tl> &next, Stage<Tl> &free) {
-    landed();
+  // Stage in cur, its first step's operands in f0, its first scales in v0; free
+  // takes the copies. The order of the instructions: LDS reads (a step's, while
+  // the step before it is multiplied), then copies, one by one between products,
+  // so that neither holds up the matrix cores (8192 x 4096 x 14336: 261 -> 243 us
+  // against the compiler's own order).
+  auto stage = [&](const Buffer &cur, const Buffer &next, Buffer &free) {
+    wait_vm_lds<(RING - 3) * Tl::kLoads>();   // the stage after this one
+    meet();
     issue(free);
     read(f1, cur, 1);
-    LBQ_MX_STEP(f0, 0, va, vb);
-    uint32_t wa[MB], wb[NB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) wa[i] = va[i];
-#pragma unroll
-    for (int j = 0; j < NB; ++j) wb[j] = vb[j];
+    LBQ_MX_STEP(f0, 0, v0);
+    v1 = v0;
     read(f0, next, 0);
-    read_scales(next);
-    LBQ_MX_STEP(f1, 2, wa, wb);
-    // the order of a stage's instructions: LDS reads (this stage's second step's,
-    // then the next stage's first) and the copies one by one between products,
-    // so that neither holds up the matrix cores (8192 x 4096 x 14336: 261 ->
-    // 243 us against the compiler's own order)
+    read_scales(v0, next);
+    LBQ_MX_STEP(f1, 2, v1);
     constexpr int kP = MB * NB, kR = MB + NB;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
@@ -278,14 +284,13 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
   issue(q1);
   if constexpr (RING == 4) issue(q2);
   wait_vm_lds<(RING - 2) * Tl::kLoads>();
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
+  meet();
   read(f0, q0, 0);
-  read_scales(q0);
+  read_scales(v0, q0);
   // whole rounds of the ring, then what is left of one (no exits inside the
   // loop: the accumulators keep their registers)
-  const int rest = G % RING;
-  for (int n = G / RING; n > 0; --n) {
+  const int rest = S % RING;
+  for (int n = S / RING; n > 0; --n) {
     if constexpr (RING == 4) {
       stage(q0, q1, q3);
       stage(q1, q2, q0);
@@ -367,29 +372,36 @@ hipError_t launch_tiles(GemmArgs g, int dtype, int slices, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which tile, and how many slices of K. A workgroup per compute unit takes, per
-// 4096 of K, about 41 us on 256 x 256, 13.6 on 128 x 128 and 8.7 on 64 x 128
-// (4096^3 and 512 x 4096^2); the smallest sum of rounds wins. Fewer tiles of
-// the smallest kind than half the compute units: K in slices of at least 1024.
+// Which tile, and how many slices of K.
+//
+// Dense: a workgroup per compute unit takes, per 4096 of K, about 41 us on 256 x
+// 256, 13.6 on 128 x 128 and 8.7 on 64 x 128 (4096^3 and 512 x 4096^2); the
+// smallest sum of rounds wins. Fewer tiles of the smallest kind than half the
+// compute units: K in slices of at least 1024.
+//
+// Grouped, by the average expert's rows: 64 x 256 to 96 rows, where the experts'
+// weights are what has to move (256 experts of 2048 x 2048, 64 rows: 181 us;
+// 128 x 128 193, 256 x 256 226), 128 x 128 below 512 (8 experts of 4096 x 4096,
+// 128 rows: 31 us; 36 and 37), else 256 x 256 (28672 x 4096, 2048 rows: 1.39 ms;
+// 128 x 128 1.71).
 struct Plan {
   int bm, bn, slices;
 };
 Plan plan_tiles(const MxGemm &p) {
+  if (p.E > 0) {
+    const int avg = p.M / p.E;
+    if (avg <= 96) return {64, p.N <= 128 ? 128 : 256, 1};
+    return avg < 512 ? Plan{128, 128, 1} : Plan{256, 256, 1};
+  }
   auto tiles = [&](int bm, int bn) {
-    // grouped: half of the experts' last tiles are taken to be ragged
-    const long tm = p.E > 0 ? std::max<long>(static_cast<long>(p.M) / bm + p.E / 2, std::min(p.E, p.M))
-                            : (static_cast<long>(p.M) + bm - 1) / bm;
-    return tm * ((static_cast<long>(p.N) + bn - 1) / bn);
+    return ((static_cast<long>(p.M) + bm - 1) / bm) * ((static_cast<long>(p.N) + bn - 1) / bn);
   };
   auto rounds = [&](int bm, int bn) { return static_cast<double>((tiles(bm, bn) + 255) / 256); };
   const double big = 41 * rounds(256, 256), mid = 13.6 * rounds(128, 128), small = 8.7 * rounds(64, 128);
   if (big <= mid && big <= small) return {256, 256, 1};
   if (mid <= small) return {128, 128, 1};
   Plan r{64, 128, 1};
-  if (p.E == 0) {
-    const long n = tiles(64, 128);
-    while (r.slices < 8 && n * r.slices * 2 <= 256 && p.K / (r.slices * 2) >= 1024) r.slices *= 2;
-  }
+  while (r.slices < 8 && tiles(64, 128) * r.slices * 2 <= 256 && p.K / (r.slices * 2) >= 1024) r.slices *= 2;
   return r;
 }
 
@@ -421,6 +433,7 @@ hipError_t launch_mx_gemm(const MxGemm &p, hipStream_t s) {
   hipError_t e;
   if (r.bm == 256) e = launch_tiles<4, 4, 2, 2, 4>(g, dtype, r.slices, s);
   else if (r.bm == 128) e = launch_tiles<2, 2, 2, 2, 3>(g, dtype, r.slices, s);
+  else if (r.bn == 256) e = launch_tiles<2, 2, 1, 4, 3>(g, dtype, r.slices, s);
   else e = launch_tiles<1, 2, 2, 2, 4>(g, dtype, r.slices, s);
   if (e != hipSuccess || r.slices == 1) return e;
   const long n = static_cast<long>(p.M) * p.N;

@@ -63,18 +63,26 @@ constexpr int kLongLds = 146 * 1024;
 constexpr int long_lds_bytes(int K) { return 16 * (K / 2 + 16) + 16 * (K / 32); }
 
 template <int MT, int GPW, int NT>
-__global__ void __launch_bounds__(kThreads) mx_stream_kernel(MxGemm g, int T16) {
+__global__ void __launch_bounds__(kThreads) mx_stream_kernel(MxGemm g, int T16, int walkers) {
   __shared__ __attribute__((aligned(16))) float4_t part[kWaves][NT * MT * 64];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);   // uniform: addresses by group in scalar registers
   const int r = lane & 15, q = lane >> 4;
-  int i0 = blockIdx.y * (16 * MT), n_rows = min(g.M - i0, 16 * MT), e = 0;
+  // `walkers` workgroups share a token tile and take its batches of rows in turn
+  int i0, n_rows, e = 0, walker;
   if (g.E > 0) {
-    const GroupTile t = find_tile(g.offsets, g.E, g.M, 16 * MT, blockIdx.y);
-    if (t.n == 0) return;
+    const GroupTiles tiles(g.offsets, g.E, g.M, 16 * MT);
+    const int id = xcd_order(blockIdx.x, tiles.total() * walkers);
+    if (id < 0) return;
+    const GroupTile t = tiles.find(id / walkers);
+    walker = id % walkers;
     i0 = t.i0;
     n_rows = t.n;
     e = t.e;
+  } else {
+    i0 = blockIdx.x / walkers * (16 * MT);
+    walker = blockIdx.x % walkers;
+    n_rows = min(g.M - i0, 16 * MT);
   }
   const int G = g.K / kGroup, g0 = wave * GPW;
   const uint32_t row_bytes = g.K / 2;
@@ -99,7 +107,7 @@ __global__ void __launch_bounds__(kThreads) mx_stream_kernel(MxGemm g, int T16) 
       }
     }
   };
-  int tb = blockIdx.x;
+  int tb = walker;
   // the first weights travel while the tokens are quantized
   load_weights(tb);
 
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kThreads) mx_stream_kernel(MxGemm g, int T16) 
 #pragma unroll
       for (int m = 0; m < MT; ++m) part[wave][(t * MT + m) * 64 + lane] = acc[t][m];
     const int cur = tb;
-    tb += gridDim.x;
+    tb += walkers;
     const bool more = static_cast<long>(tb) * NT < T16;
     if (more) load_weights(tb);   // in flight during the sums below
     barrier_lds();
@@ -233,12 +241,11 @@ hipError_t launch(const MxGemm &g, int tiles, hipStream_t s) {
   constexpr int kMany = GPW * MT >= 8 ? 1 : GPW * MT >= 4 ? 2 : 4;
   const int T16 = (g.N + 15) / 16;
   if (g.E > 0 && T16 >= 4 * kMany) {
-    const int nb = (T16 + kMany - 1) / kMany;
-    hipLaunchKernelGGL((mx_stream_kernel<MT, GPW, kMany>), dim3(std::min(nb, std::max(1, 1024 / tiles)), tiles),
-                       dim3(kThreads), 0, s, g, T16);
+    const int walkers = std::min((T16 + kMany - 1) / kMany, std::max(1, 1024 / tiles));
+    hipLaunchKernelGGL((mx_stream_kernel<MT, GPW, kMany>), dim3(tiles * walkers), dim3(kThreads), 0, s, g, T16, walkers);
   } else {
-    hipLaunchKernelGGL((mx_stream_kernel<MT, GPW, 1>), dim3(std::min(T16, std::max(1, 256 / tiles)), tiles),
-                       dim3(kThreads), 0, s, g, T16);
+    const int walkers = std::min(T16, std::max(1, 256 / tiles));
+    hipLaunchKernelGGL((mx_stream_kernel<MT, GPW, 1>), dim3(tiles * walkers), dim3(kThreads), 0, s, g, T16, walkers);
   }
   return hipGetLastError();
 }
@@ -256,7 +263,7 @@ bool mx_stream_supported(int rows, int K) {
 hipError_t launch_mx_stream(const MxGemm &g, int rows, hipStream_t s) {
   const int mt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4, gpw = groups_per_wave(g.K);
   const long n = (static_cast<long>(g.M) + 16 * mt - 1) / (16 * mt) + (g.E > 0 ? std::min(g.E, g.M) : 0);
-  if (!mx_stream_supported(rows, g.K) || n > 65535) return hipErrorInvalidValue;
+  if (!mx_stream_supported(rows, g.K) || n > (1 << 24)) return hipErrorInvalidValue;
   const int tiles = static_cast<int>(n);
   if (mt == 1) {
     if (gpw <= 2) return launch<1, 2>(g, tiles, s);

@@ -10,49 +10,63 @@ namespace mxfp4 {
 
 typedef int v8i_t __attribute__((ext_vector_type(8)));
 
-// Row tile `slot` of the expert-sorted list: its expert, first row and rows
-// (0 rows past the last tile). Every lane of the wave gets the same answer.
-// offsets is taken as it comes: ranges are clamped to [0, T].
+// Row tiles of bm rows of an expert-sorted list; every expert may end in a
+// ragged one. Each wave counts for itself: lane l holds the ranges of experts
+// l per .. (l + 1) per - 1 (all loads at once) and the running sum of their
+// tiles. offsets is taken as it comes: ranges are clamped to [0, T].
 struct GroupTile {
-  int e, i0, n;
+  int e, i0, n;   // expert, first list row, rows
 };
-__device__ __forceinline__ GroupTile find_tile(const int32_t *offsets, int E, int T, int bm, int slot) {
-  const int lane = threadIdx.x & 63;
-  const int per = (E + 63) / 64, e0 = lane * per;
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = e0 + i;
-    if (e >= E) break;
-    const int lo = min(max(offsets[e], 0), T), hi = min(max(offsets[e + 1], lo), T);
-    mine += (hi - lo + bm - 1) / bm;
-  }
-  int incl = mine;
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
-  const uint64_t past = __ballot(slot < incl);
-  GroupTile t{0, 0, 0};
-  if (past == 0) return t;
-  const int src = __builtin_ctzll(past);
-  int k = slot - (incl - mine);   // the lane's own tile number, if src
-  if (lane == src) {
-    for (int i = 0; i < per; ++i) {
-      const int e = e0 + i;
-      if (e >= E) break;
-      const int lo = min(max(offsets[e], 0), T), hi = min(max(offsets[e + 1], lo), T);
-      const int tiles = (hi - lo + bm - 1) / bm;
-      if (k < tiles) {
-        t = GroupTile{e, lo + k * bm, min(hi - lo - k * bm, bm)};
-        break;
+struct GroupTiles {
+  static constexpr int kMost = 16;   // experts per lane, for up to 1024
+  int at[kMost + 1];                 // where the lane's experts begin, and the last ends
+  int per, bm, mine, incl;
+  __device__ __forceinline__ GroupTiles(const int32_t *offsets, int E, int T, int bm_) : per((E + 63) / 64), bm(bm_) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i <= kMost; ++i)
+      if (i <= per) at[i] = offsets[min(lane * per + i, E)];
+    mine = 0;
+#pragma unroll
+    for (int i = 0; i <= kMost; ++i)
+      if (i <= per) {
+        at[i] = min(max(at[i], i > 0 ? at[i - 1] : 0), T);
+        if (i > 0) mine += (at[i] - at[i - 1] + bm - 1) / bm;
       }
-      k -= tiles;
+    incl = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(incl, d);
+      if (lane >= d) incl += o;
     }
   }
-  t.e = __shfl(t.e, src);
-  t.i0 = __shfl(t.i0, src);
-  t.n = __shfl(t.n, src);
-  return t;
+  __device__ __forceinline__ int total() const { return __builtin_amdgcn_readlane(incl, 63); }
+  // tile number slot < total(), the same for every lane
+  __device__ __forceinline__ GroupTile find(int slot) const {
+    const int src = __builtin_ctzll(__ballot(slot < incl));
+    int k = slot - (incl - mine), e = 0, i0 = 0, n = 0;   // of use in lane src
+#pragma unroll
+    for (int i = 0; i < kMost; ++i)
+      if (i < per) {
+        const int rows = at[i + 1] - at[i], tiles = (rows + bm - 1) / bm;
+        if (k >= 0 && k < tiles) {
+          e = src * per + i;
+          i0 = at[i] + k * bm;
+          n = min(rows - k * bm, bm);
+        }
+        k -= tiles;
+      }
+    return GroupTile{__builtin_amdgcn_readlane(e, src), __builtin_amdgcn_readlane(i0, src),
+                     __builtin_amdgcn_readlane(n, src)};
+  }
+};
+
+// Workgroups go to the eight XCDs in turn, each with an L2 of its own: XCD i
+// takes the i-th eighth of `total` pieces of work in order, so that neighbours
+// share an L2. The piece of workgroup pid, -1 for none.
+__device__ __forceinline__ int xcd_order(int pid, int total) {
+  const int xcd = pid & 7, at = pid >> 3, q = total / 8, rem = total % 8;
+  return at < q + (xcd < rem ? 1 : 0) ? xcd * q + min(xcd, rem) + at : -1;
 }
 
 __device__ __forceinline__ v8i_t operand(uint4 v) {

@@ -95,49 +95,92 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const void *__res
 // ------------------------------------------------------------------ along columns
 
 // The transposed tensor: blocks of 32 rows of x. A workgroup takes 128 rows by
-// 64 columns of x through LDS; a thread then owns one column's block of 32.
-// Rows past the end count as zeros.
-constexpr int kTileCols = 64;
-
-template <int DT>
+// 256 bytes of columns (128 columns in 16 bits, 64 in fp32) through LDS, rows of
+// 64 words. Wave b then owns rows 32 b .. 32 b + 31 and lane l the column, or
+// pair of columns, of word l: a read of one row by the wave is 64 neighbouring
+// words. Codes leave through LDS too, so that the four 16-byte blocks of a
+// column go out side by side. Rows and columns past the end count as zeros.
+//
+// Bound: HBM (2 + 17/32 bytes per 16-bit value). VEC: every row starts on a
+// 16-byte boundary.
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) mx_quantize_t_kernel(const void *__restrict__ x, uint4 *__restrict__ codes,
                                                                  uint32_t *__restrict__ scales, int rows, int cols,
                                                                  int row_groups) {
   using T = typename Elem<DT>::type;
-  __shared__ T tile[128][kTileCols + (DT == kF32 ? 1 : 2)];
-  const int c0 = blockIdx.x * kTileCols;
-  const int g = blockIdx.y;
+  constexpr int kPer = DT == kF32 ? 1 : 2;        // columns per word
+  constexpr int kCols = 64 * kPer, kVec = 4 * kPer;   // of a tile; of 16 bytes
+  __shared__ __attribute__((aligned(16))) uint32_t tile[128][64];
+  __shared__ __attribute__((aligned(4))) uint8_t bytes[kCols][4];
+  const int c0 = blockIdx.x * kCols, g = blockIdx.y;
   const T *src = static_cast<const T *>(x);
-  for (int i = threadIdx.x; i < 128 * kTileCols; i += kThreads) {
-    const int r = i / kTileCols, c = i % kTileCols;
-    const long row = static_cast<long>(g) * 128 + r;
-    tile[r][c] = row < rows && c0 + c < cols ? src[row * cols + c0 + c] : T(0);
+#pragma unroll
+  for (int it = 0; it < 8; ++it) {
+    const int i = it * kThreads + threadIdx.x, r = i >> 4, c = c0 + (i & 15) * kVec;
+    const int row = min(g * 128 + r, rows - 1);
+    const bool there = g * 128 + r < rows;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if constexpr (VEC) {
+      if (there && c < cols) v = *reinterpret_cast<const uint4 *>(src + static_cast<size_t>(row) * cols + c);
+    } else {
+      uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int e = 0; e < kVec; ++e)
+        if (there && c + e < cols) {
+          const T t = src[static_cast<size_t>(row) * cols + c + e];
+          if constexpr (DT == kF32) w[e] = __float_as_uint(t);
+          else w[e / 2] |= static_cast<uint32_t>(t) << (16 * (e % 2));
+        }
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    *reinterpret_cast<uint4 *>(&tile[r][4 * (i & 15)]) = v;
   }
   __syncthreads();
-  const int c = threadIdx.x & 63, b = threadIdx.x >> 6;   // one wave per block of 32 rows
-  __shared__ uint8_t bytes[4][kTileCols];
-  uint32_t m = 0;
-  float v[32];
+  const int l = threadIdx.x & 63, b = threadIdx.x >> 6;
+  uint32_t w[32];
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = to_f32<DT>(tile[32 * b + i][c]);
-    m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-  }
-  const uint32_t byte = scale_byte<kF32>(m);
-  const float s = scale_value(byte);
-  uint32_t w[4];
+  for (int i = 0; i < 32; ++i) w[i] = tile[32 * b + i][l];
+  __syncthreads();   // the tile's words are read: its memory takes the codes
+  uint4 *out = reinterpret_cast<uint4 *>(&tile[0][0]);   // [kCols][4]
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = codes8_f32(v + 8 * i, s);
-    if (byte == 255u) w[i] = 0;
+  for (int p = 0; p < kPer; ++p) {
+    uint32_t m = 0, byte;
+    uint32_t o[4];
+    if constexpr (DT == kF32) {
+      float v[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        v[i] = __uint_as_float(w[i]);
+        m = max(m, w[i] & 0x7FFFFFFFu);
+      }
+      byte = scale_byte<DT>(m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = codes8_f32(v + 8 * i, scale_value(byte));
+    } else {
+      // this column's 16-bit values, two rows to a word
+      uint32_t v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        v[i] = __builtin_amdgcn_perm(w[2 * i + 1], w[2 * i], p == 0 ? 0x05040100u : 0x07060302u);
+        m = max(m, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
+      }
+      byte = scale_byte<DT>(m);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = codes8<DT>(v + 4 * i, scale_value(byte));
+    }
+    const int c = kPer * l + p;
+    out[c * 4 + b] = byte == 255u ? make_uint4(0, 0, 0, 0) : make_uint4(o[0], o[1], o[2], o[3]);
+    bytes[c][b] = static_cast<uint8_t>(byte);
   }
-  if (c0 + c < cols)
-    codes[(static_cast<long>(c0 + c) * row_groups + g) * 4 + b] = make_uint4(w[0], w[1], w[2], w[3]);
-  bytes[b][c] = static_cast<uint8_t>(byte);
   __syncthreads();
-  if (b == 0 && c0 + c < cols)
-    scales[static_cast<long>(g) * cols + c0 + c] = bytes[0][c] | (bytes[1][c] << 8) | (bytes[2][c] << 16) |
-                                                   (static_cast<uint32_t>(bytes[3][c]) << 24);
+#pragma unroll
+  for (int it = 0; it < kCols * 4 / kThreads; ++it) {
+    const int i = it * kThreads + threadIdx.x, c = c0 + (i >> 2);
+    if (c < cols) codes[(static_cast<size_t>(c) * row_groups + g) * 4 + (i & 3)] = out[i];
+  }
+  const int c = threadIdx.x;
+  if (c < kCols && c0 + c < cols)
+    scales[static_cast<size_t>(g) * cols + c0 + c] = *reinterpret_cast<const uint32_t *>(bytes[c]);
 }
 
 // ------------------------------------------------------------------ values
@@ -184,15 +227,22 @@ hipError_t launch_mx_quantize(const void *x, int dtype, int rows, int cols, void
 hipError_t launch_mx_quantize_t(const void *x, int dtype, int rows, int cols, void *codes, void *scales,
                                 hipStream_t s) {
   const int rg = static_cast<int>((static_cast<long>(rows) + 127) / 128);
-  const dim3 grid((cols + kTileCols - 1) / kTileCols, rg);
+  const int per = dtype == kF32 ? 64 : 128;
+  const dim3 grid((cols + per - 1) / per, rg);
+  const bool vec = cols % (dtype == kF32 ? 4 : 8) == 0;
   uint4 *c = static_cast<uint4 *>(codes);
   uint32_t *e = static_cast<uint32_t *>(scales);
-  if (dtype == kF16)
-    hipLaunchKernelGGL(mx_quantize_t_kernel<kF16>, grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg);
-  else if (dtype == kBF16)
-    hipLaunchKernelGGL(mx_quantize_t_kernel<kBF16>, grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg);
-  else
-    hipLaunchKernelGGL(mx_quantize_t_kernel<kF32>, grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg);
+#define LBQ_MX_GO(DT)                                                                                               \
+  if (vec) hipLaunchKernelGGL((mx_quantize_t_kernel<DT, true>), grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg); \
+  else hipLaunchKernelGGL((mx_quantize_t_kernel<DT, false>), grid, dim3(kThreads), 0, s, x, c, e, rows, cols, rg)
+  if (dtype == kF16) {
+    LBQ_MX_GO(kF16);
+  } else if (dtype == kBF16) {
+    LBQ_MX_GO(kBF16);
+  } else {
+    LBQ_MX_GO(kF32);
+  }
+#undef LBQ_MX_GO
   return hipGetLastError();
 }
 
