@@ -21,8 +21,11 @@ inline lbq_status hip_status(hipError_t e) { return e == hipSuccess ? LBQ_OK : L
 inline bool value_type(int32_t dtype) { return dtype >= LBQ_F16 && dtype <= LBQ_F32; }
 inline bool half_type(int32_t dtype) { return dtype == LBQ_F16 || dtype == LBQ_BF16; }
 
+// (row numbers and their roundings up to whole tiles stay 32-bit)
+constexpr int64_t kMaxRows = 1 << 30;
+
 bool mx_shape(int64_t rows, int64_t cols) {
-  return rows >= 0 && cols > 0 && cols % 128 == 0 && rows * (cols / 128) < (1ll << 31);
+  return rows >= 0 && rows <= kMaxRows && cols > 0 && cols % 128 == 0 && rows * (cols / 128) < (1ll << 31);
 }
 size_t code_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * (cols / 2); }
 size_t scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * (cols / 32); }
@@ -108,7 +111,7 @@ lbq_status quantize_and_multiply(MxGemm g, const void *x, void *ws, const Linear
 lbq_status check_grouped(const lbq_mx *w, int32_t E, int32_t M, int32_t T) {
   const lbq_status st = check_mx(w);
   if (st != LBQ_OK) return st;
-  if (E < 1 || E > kMoeMaxExperts || w->rows % E != 0 || M < 0 || T < 0) return LBQ_ERR_SHAPE;
+  if (E < 1 || E > kMoeMaxExperts || w->rows % E != 0 || T < 0 || T > kMaxRows) return LBQ_ERR_SHAPE;
   if (!mx_shape(M, w->cols)) return LBQ_ERR_SHAPE;
   return LBQ_OK;
 }
@@ -129,7 +132,7 @@ lbq_status check_picks(int32_t M, int32_t top_k) {
 lbq_status check_rows(int32_t dtype, int32_t M, int32_t top_k, int32_t T, int32_t H) {
   const lbq_status st = check_picks(M, top_k);
   if (st != LBQ_OK) return st;
-  if (T < 0 || H < 1) return LBQ_ERR_SHAPE;
+  if (T < 0 || H < 1 || H > kMaxRows) return LBQ_ERR_SHAPE;
   return value_type(dtype) ? LBQ_OK : LBQ_ERR_FORMAT;
 }
 

@@ -168,14 +168,21 @@ struct Row {
     }
     return r;
   }
+  // PAST: past the caches
+  template <bool PAST = false>
   __device__ __forceinline__ void store(void *p, size_t at) const {
     if constexpr (V == 1) {
       static_cast<T *>(p)[at] = v[0];
     } else {
+      typedef uint32_t vec_t __attribute__((ext_vector_type(4)));
       constexpr int kVecs = V * sizeof(T) / 16;
-      const uint4 *q = reinterpret_cast<const uint4 *>(v);
+      const vec_t *q = reinterpret_cast<const vec_t *>(v);
+      vec_t *o = reinterpret_cast<vec_t *>(static_cast<T *>(p) + at);
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) reinterpret_cast<uint4 *>(static_cast<T *>(p) + at)[i] = q[i];
+      for (int i = 0; i < kVecs; ++i) {
+        if constexpr (PAST) __builtin_nontemporal_store(q[i], o + i);
+        else o[i] = q[i];
+      }
     }
   }
 };
@@ -183,7 +190,10 @@ struct Row {
 constexpr int kRowThreads = 256;
 
 // out[pos[t][j]] = x[t]: each token row is read once and written top_k times.
-template <int DT, int V>
+// PAST: a list larger than the memory-side cache goes past it. 131072 rows of
+// 4 KB: the gather itself takes 117 instead of 87 us, what reads such a list
+// next 113 instead of 150 (it need not wait for the cache to be written back).
+template <int DT, int V, bool PAST>
 __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const void *__restrict__ x, int M, int H, int T,
                                                                  const int32_t *__restrict__ pos, int top_k,
                                                                  void *__restrict__ out) {
@@ -192,7 +202,7 @@ __global__ void __launch_bounds__(kRowThreads) moe_gather_kernel(const void *__r
     const auto r = Row<DT, V>::load(x, static_cast<size_t>(t) * H + c);
     for (int j = 0; j < top_k; ++j) {
       const int p = pos[static_cast<size_t>(t) * top_k + j];
-      if (p >= 0 && p < T) r.store(out, static_cast<size_t>(p) * H + c);
+      if (p >= 0 && p < T) r.template store<PAST>(out, static_cast<size_t>(p) * H + c);
     }
   }
 }
@@ -301,6 +311,11 @@ __global__ void __launch_bounds__(kRowThreads) moe_combine_backward_kernel(
   }
 }
 
+template <int DT, int V>
+constexpr auto gather_past = moe_gather_kernel<DT, V, true>;
+template <int DT, int V>
+constexpr auto gather_kept = moe_gather_kernel<DT, V, false>;
+
 unsigned chunks(int H, int v) { return static_cast<unsigned>(std::min((H + kRowThreads * v - 1) / (kRowThreads * v), 64)); }
 
 }  // namespace
@@ -336,7 +351,10 @@ hipError_t launch_moe_sort(const int32_t *ids, int n, int E, int32_t *counts, in
 
 hipError_t launch_moe_gather(const void *x, int dtype, int M, int H, int T, const int32_t *pos, int top_k, void *out,
                              hipStream_t s) {
-  LBQ_ROWS(moe_gather_kernel, true, x, M, H, T, pos, top_k, out);
+  constexpr size_t kMemorySideCache = size_t{256} << 20;
+  const size_t bytes = static_cast<size_t>(M) * top_k * H * (dtype == kF32 ? 4 : 2);
+  if (bytes > kMemorySideCache) LBQ_ROWS(gather_past, true, x, M, H, T, pos, top_k, out);
+  else LBQ_ROWS(gather_kept, true, x, M, H, T, pos, top_k, out);
   return hipGetLastError();
 }
 

@@ -314,11 +314,6 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
     if (rest > 2) stage(q2, q3, q1);
 #undef LBQ_MX_STEP
   wait_vm_lds<0>();   // no copy into LDS outlives the workgroup
-  // the last products' results are complete before anything moves them (sixteen
-  // passes of four cycles)
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("s_nop 15\n\ts_nop 15\n\ts_nop 15\n\ts_nop 15");
-  __builtin_amdgcn_sched_barrier(0);
   const bool vecs = g.N % 8 == 0;
   // slices write partial results one behind the other
   void *y = g.y;

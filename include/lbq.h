@@ -409,9 +409,12 @@ lbq_status lbq_stream_read(const void *buf, size_t bytes, int32_t grid, int32_t 
  *           and 2i + 1 in its high nibble.
  *   scales: uint8 [C/128][R][4]; byte b of word (g, r) belongs to values
  *           128 g + 32 b .. 128 g + 32 b + 31 of row r.
- * R * (C/128) stays below 2^31 (LBQ_ERR_SHAPE otherwise). These calls take no
- * rotation signs: lbq_rotate the activations, and the weights before they are
- * quantized, where a rotated basis is wanted.
+ * R is at most 2^30 and R * (C/128) below 2^31 (LBQ_ERR_SHAPE otherwise).
+ * These calls take no rotation signs: lbq_rotate the activations, and the
+ * weights before they are quantized, where a rotated basis is wanted. Outputs
+ * overlap no input. They have no gradient of their own: a layer's backward pass
+ * is two more products, of tensors quantized along what each sums over
+ * (lbq_mx_quantize_t), the rounding taken as the identity.
  */
 
 /* Value types of the buffers that are not in a packed format. */
@@ -440,7 +443,8 @@ lbq_status lbq_mx_quantize(const void *x, int32_t dtype, int32_t rows, int32_t c
 /* The same for x^T: x [rows][cols] (any rows >= 0 and cols > 0) into the MXFP4
  * tensor of cols rows and Rp = rows rounded up to a multiple of 128 columns,
  * the columns past rows zero. What a product needs whose sum runs over x's
- * rows (the weight's gradient sums over tokens, the input's over outputs). */
+ * rows (the weight's gradient sums over tokens, the input's over outputs).
+ * rows is at most 128 * 65535. */
 lbq_status lbq_mx_quantize_t(const void *x, int32_t dtype, int32_t rows, int32_t cols, void *codes, void *scales,
                              void *stream);
 
@@ -489,7 +493,7 @@ lbq_status lbq_mx_grouped_forward(const lbq_mx *w, int32_t E, const void *x, int
  *
  * A pick is assignment a = t * top_k + j: slot j of token t goes to expert
  * ids[t][j]. Limits as lbq_moe_route's: E <= 1024, top_k <= 32, M * top_k <=
- * 2^20 (LBQ_ERR_SHAPE). Row buffers hold H values of dtype each (any H > 0). */
+ * 2^20 (LBQ_ERR_SHAPE). Row buffers hold H values of dtype each, 1 <= H <= 2^30. */
 
 /* Workspace bytes of lbq_moe_sort (host query). */
 lbq_status lbq_moe_sort_workspace(int32_t M, int32_t E, int32_t top_k, size_t *bytes);

@@ -196,3 +196,19 @@ def test_dropped_values_do_not_count(L, dev):
     L.moe_gather(s["xd"], s["pd"], out=short)
     L.moe_gather(s["xd"], s["pd"], out=full)
     assert torch.equal(short, full[:T])
+
+
+def test_gather_larger_than_the_memory_side_cache(L, dev):
+    """A list of over 256 MB is stored past the caches; smaller ones are not: the same rows."""
+    import torch
+
+    m, k, H = 17000, 4, 2048
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn(m, H, device="cuda", generator=g).to(torch.bfloat16)
+    ids = torch.randint(-1, 40, (m, k), device="cuda", generator=g, dtype=torch.int32)
+    counts, offsets, perm, pos = L.moe_sort(ids, 40)
+    n = int(offsets[-1])
+    out = torch.full((m * k, H), 2.5, dtype=torch.bfloat16, device="cuda")
+    assert out.numel() * 2 > 256 << 20
+    L.moe_gather(x, pos, out=out)
+    assert torch.equal(out[:n], x[(perm[:n] // k).long()]) and (out[n:] == 2.5).all()

@@ -25,7 +25,7 @@ def test_bytes(L):
     lib, a, b = L.lib(), ctypes.c_size_t(), ctypes.c_size_t()
     assert lib.lbq_mx_bytes(10, 256, ctypes.byref(a), ctypes.byref(b)) == OK and (a.value, b.value) == (1280, 80)
     assert lib.lbq_mx_bytes(0, 128, ctypes.byref(a), ctypes.byref(b)) == OK and (a.value, b.value) == (0, 0)
-    for rows, cols in ((-1, 128), (1, 0), (1, 64), (1, 130), (2 ** 31 - 1, 256)):
+    for rows, cols in ((-1, 128), (1, 0), (1, 64), (1, 130), (2 ** 31 - 1, 128), (2 ** 30 + 1, 128), (2 ** 30, 256)):
         assert lib.lbq_mx_bytes(rows, cols, ctypes.byref(a), ctypes.byref(b)) == SHAPE
     assert lib.lbq_mx_bytes(1, 128, None, ctypes.byref(b)) == NULL
 
@@ -82,6 +82,7 @@ def test_product_refusals(L):
     assert grouped(E=4) == SHAPE and grouped(E=0) == SHAPE and grouped(k=0) == SHAPE
     assert grouped(w=_mx(L, 2050, 128), E=1025) == SHAPE
     assert grouped(perm=None) == SHAPE                             # without perm x has T rows
+    assert grouped(T=2 ** 30 + 1) == SHAPE and grouped(M=-1) == SHAPE
     assert grouped(dt=2) == FORMAT and grouped(off=None) == NULL and grouped(y=P + 2) == ALIGN
     assert grouped(off=P + 2) == ALIGN and grouped(perm=P + 2) == ALIGN
     assert grouped(M=0, x=None, off=None, y=None, ws=None, T=0) == OK
@@ -111,7 +112,7 @@ def test_dispatch_refusals(L):
     def combine_b(x=P, dt=0, M=4, H=8, pos=P, k=2, T=8, out=P, w=P, dw=P):
         return lib.lbq_moe_combine_backward(P, x, dt, T, H, pos, w, M, k, out, dw, None)
     for f in (gather, gather_b, combine, combine_b):
-        assert f(dt=3) == FORMAT and f(H=0) == SHAPE and f(k=33) == SHAPE and f(M=-1) == SHAPE and f(T=-1) == SHAPE
+        assert f(dt=3) == FORMAT and f(H=0) == SHAPE and f(H=2 ** 30 + 1) == SHAPE and f(k=33) == SHAPE and f(M=-1) == SHAPE and f(T=-1) == SHAPE
         assert f(x=None) == NULL and f(pos=None) == NULL and f(out=None) == NULL
         assert f(x=P + 4) == ALIGN and f(out=P + 4) == ALIGN and f(pos=P + 2) == ALIGN
         assert f(M=0, x=None, pos=None, out=None) == OK
