@@ -68,10 +68,16 @@ int stream_rows(const MxGemm &g) {
   return 0;
 }
 
-// The streaming kernel quantizes the activations itself where that costs its
-// workgroups less than a launch: up to eight tokens (4096 -> 4096: 6.3 against
-// 7.1 us; 16 tokens 8.0 against 7.3), and few rows per expert.
-bool stream_quantizes(const MxGemm &g) { return stream_rows(g) > 0 && (g.E > 0 || g.M <= 8); }
+// The streaming kernel quantizes the activations itself where every workgroup
+// doing so costs about as much as a launch, or less. Per call, itself against
+// with a launch before it, in a graph (one by one): 8 tokens 4096 -> 4096 6.3
+// against 7.1 us; 16 tokens 4096 -> 4096 7.8 against 7.3 (8.0 against 10.8); 32
+// tokens 2048 -> 4096 7.1 against 6.7 (7.0 against 10.7); 32 tokens 4096 -> 4096
+// 11.6 against 8.7. Grouped: always (few rows per expert).
+bool stream_quantizes(const MxGemm &g) {
+  if (stream_rows(g) == 0) return false;
+  return g.E > 0 || g.M <= 8 || (g.M <= 32 && static_cast<long>(g.M) * g.K <= 1 << 16);
+}
 
 size_t scratch_bytes(const MxGemm &g) { return stream_rows(g) > 0 ? 0 : mx_gemm_scratch_bytes(g); }
 
