@@ -21,11 +21,13 @@ inline lbq_status hip_status(hipError_t e) { return e == hipSuccess ? LBQ_OK : L
 inline bool value_type(int32_t dtype) { return dtype >= LBQ_F16 && dtype <= LBQ_F32; }
 inline bool half_type(int32_t dtype) { return dtype == LBQ_F16 || dtype == LBQ_BF16; }
 
-// (row numbers and their roundings up to whole tiles stay 32-bit)
-constexpr int64_t kMaxRows = 1 << 30;
+// (row numbers and their roundings up to whole tiles stay 32-bit, and so do the
+// offsets within 256 rows)
+constexpr int64_t kMaxRows = 1 << 30, kMaxCols = 1 << 24;
 
 bool mx_shape(int64_t rows, int64_t cols) {
-  return rows >= 0 && rows <= kMaxRows && cols > 0 && cols % 128 == 0 && rows * (cols / 128) < (1ll << 31);
+  return rows >= 0 && rows <= kMaxRows && cols > 0 && cols <= kMaxCols && cols % 128 == 0 &&
+         rows * (cols / 128) < (1ll << 31);
 }
 size_t code_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * (cols / 2); }
 size_t scale_bytes(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * (cols / 32); }
@@ -60,7 +62,7 @@ MxGemm dense(int M, const lbq_mx *b, void *y, int32_t dtype) {
 
 // Rows of a tile on the streaming kernel, 0: the tile kernel. Grouped: where 16
 // rows hold the average expert's and half as many again (256 experts of 2048 x
-// 2048, 4 rows: 96 us, the tile kernel 105; 16 rows in tiles of 32: 148, 125).
+// 2048, 4 rows: 105 us, the tile kernel 115; 8 rows: 115, 119; 12 rows: 141, 125).
 int stream_rows(const MxGemm &g) {
   const long rows = g.E > 0 ? (3l * g.M + 2 * g.E - 1) / (2 * g.E) : g.M;
   for (int t = 16; t <= (g.E > 0 ? 16 : 64); t *= 2)
@@ -119,6 +121,8 @@ lbq_status check_grouped(const lbq_mx *w, int32_t E, int32_t M, int32_t T) {
   if (st != LBQ_OK) return st;
   if (E < 1 || E > kMoeMaxExperts || w->rows % E != 0 || T < 0 || T > kMaxRows) return LBQ_ERR_SHAPE;
   if (!mx_shape(M, w->cols)) return LBQ_ERR_SHAPE;
+  // the quantized rows, taken in any order, at 32-bit offsets
+  if (code_bytes(M, w->cols) >= 1ull << 32) return LBQ_ERR_SHAPE;
   return LBQ_OK;
 }
 

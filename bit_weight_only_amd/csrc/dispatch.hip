@@ -35,8 +35,8 @@ __device__ __forceinline__ int expert_of(const int32_t *ids, int a, int end, int
 }
 
 // Counts of one workgroup's chunk (integer sums: the order does not matter).
-__global__ void __launch_bounds__(kSortThreads) moe_hist_kernel(const int32_t *__restrict__ ids, int n, int E, int chunk,
-                                                                int32_t *__restrict__ hist) {
+__global__ void __launch_bounds__(kSortThreads) moe_hist_kernel(const int32_t *__restrict__ ids, int n, int E,
+                                                                int chunk, int32_t *__restrict__ hist) {
   __shared__ int32_t cnt[kMoeMaxExperts];
   for (int i = threadIdx.x; i < E; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
@@ -55,11 +55,12 @@ __global__ void __launch_bounds__(kSortThreads) moe_hist_kernel(const int32_t *_
 // waves' from the LDS counts, its own wave's earlier ones from the running
 // count, and among the 64 by a ballot over the bits of the expert number).
 // hist is null where one workgroup holds every pick.
-__global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const int32_t *__restrict__ ids, int n, int E, int chunk,
-                                                                 const int32_t *__restrict__ hist,
+__global__ void __launch_bounds__(kSortThreads) moe_place_kernel(const int32_t *__restrict__ ids, int n, int E,
+                                                                 int chunk, const int32_t *__restrict__ hist,
                                                                  int32_t *__restrict__ counts,
                                                                  int32_t *__restrict__ offsets,
-                                                                 int32_t *__restrict__ perm, int32_t *__restrict__ pos) {
+                                                                 int32_t *__restrict__ perm,
+                                                                 int32_t *__restrict__ pos) {
   __shared__ int32_t s_cnt[kSortWaves * kMoeMaxExperts];   // per (wave, expert): count, then the running place
   __shared__ int32_t s_wave[kSortWaves];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -316,7 +317,9 @@ constexpr auto gather_past = moe_gather_kernel<DT, V, true>;
 template <int DT, int V>
 constexpr auto gather_kept = moe_gather_kernel<DT, V, false>;
 
-unsigned chunks(int H, int v) { return static_cast<unsigned>(std::min((H + kRowThreads * v - 1) / (kRowThreads * v), 64)); }
+unsigned chunks(int H, int v) {
+  return static_cast<unsigned>(std::min((H + kRowThreads * v - 1) / (kRowThreads * v), 64));
+}
 
 }  // namespace
 
@@ -337,16 +340,16 @@ hipError_t launch_moe_sort(const int32_t *ids, int n, int E, int32_t *counts, in
 }
 
 // eight values a lane where every row starts on a 16-byte boundary
-#define LBQ_ROWS(KERNEL, GRIDY, ...)                                                                                  \
-  do {                                                                                                                \
-    const bool vec = H % 8 == 0;                                                                                      \
-    const dim3 grid(static_cast<unsigned>(M), GRIDY ? chunks(H, vec ? 8 : 1) : 1);                                    \
-    if (dtype == kF16 && vec) hipLaunchKernelGGL((KERNEL<kF16, 8>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);      \
-    else if (dtype == kF16) hipLaunchKernelGGL((KERNEL<kF16, 1>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);        \
-    else if (dtype == kBF16 && vec) hipLaunchKernelGGL((KERNEL<kBF16, 8>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__); \
-    else if (dtype == kBF16) hipLaunchKernelGGL((KERNEL<kBF16, 1>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);      \
-    else if (vec) hipLaunchKernelGGL((KERNEL<kF32, 8>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);                  \
-    else hipLaunchKernelGGL((KERNEL<kF32, 1>), grid, dim3(kRowThreads), 0, s, __VA_ARGS__);                           \
+#define LBQ_ROWS(KERNEL, GRIDY, ...)                                                                        \
+  do {                                                                                                      \
+    const bool vec = H % 8 == 0;                                                                            \
+    const dim3 grid(static_cast<unsigned>(M), GRIDY ? chunks(H, vec ? 8 : 1) : 1), block(kRowThreads);      \
+    if (dtype == kF16 && vec) hipLaunchKernelGGL((KERNEL<kF16, 8>), grid, block, 0, s, __VA_ARGS__);        \
+    else if (dtype == kF16) hipLaunchKernelGGL((KERNEL<kF16, 1>), grid, block, 0, s, __VA_ARGS__);          \
+    else if (dtype == kBF16 && vec) hipLaunchKernelGGL((KERNEL<kBF16, 8>), grid, block, 0, s, __VA_ARGS__); \
+    else if (dtype == kBF16) hipLaunchKernelGGL((KERNEL<kBF16, 1>), grid, block, 0, s, __VA_ARGS__);        \
+    else if (vec) hipLaunchKernelGGL((KERNEL<kF32, 8>), grid, block, 0, s, __VA_ARGS__);                    \
+    else hipLaunchKernelGGL((KERNEL<kF32, 1>), grid, block, 0, s, __VA_ARGS__);                             \
   } while (0)
 
 hipError_t launch_moe_gather(const void *x, int dtype, int M, int H, int T, const int32_t *pos, int top_k, void *out,

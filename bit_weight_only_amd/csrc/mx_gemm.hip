@@ -39,26 +39,28 @@ struct GemmArgs {
 // weight rows. The weight is the instruction's first operand, so a lane's four
 // consecutive result registers are four neighbouring outputs of one token.
 //
-// Stages of one 128-group of K (64 bytes and a scale word a row) go global -> LDS
-// by asynchronous copies into a ring of RING buffers. In stage s the copies of
-// stages s + 2 .. s + RING - 1 are in flight and the operands of the next
-// 64-long step are read from LDS while one step is multiplied, across the stage's
-// border too: stage s starts when s + 1 has landed. One barrier per stage. Vector
-// v (16 bytes) of row r lies in slot v ^ ((r >> 2) & 3) of the row: the sixteen
-// rows that a quarter of an operand read touches fall in sixteen distinct 16-byte
-// bank groups. Stages of two groups (128 bytes a row) leave fewer workgroups per
-// compute unit and measured slower (256 experts, 2048 tokens: 193 -> 210 us).
+// Stages of two 128-groups of K (128 bytes and two scale words a row) go global
+// -> LDS by asynchronous copies into two buffers in turn. A copy of 64 lanes
+// takes eight rows of 128 bytes: whole cache lines, for which the copies reach
+// 50 to 56 bytes per cycle and compute unit; of 64-byte pieces only 28 to 30, too
+// few for the matrix cores (256 x 256 tiles take 34 KB per 1024 cycles of
+// products). The operands of the next 64-long step are read from LDS while one
+// step is multiplied, across the stage's border too, with one barrier per stage:
+// before a stage's last step all its operands are in registers and the next
+// stage has landed, so the barrier frees this stage's buffer for the copies after
+// next and opens the next one's. Vector v (16 bytes) of row r lies in slot
+// v ^ ((r >> 1) & 7) of the row: the sixteen rows that a quarter of an operand
+// read touches fall in sixteen distinct 16-byte bank groups.
 template <int MB, int NB, int GM, int GN>
 struct Tile {
-  static constexpr int kThreads = 64 * GM * GN, kVecs = 4;   // 16-byte vectors of a row's stage
+  static constexpr int kThreads = 64 * GM * GN, kVecs = 8;   // 16-byte vectors of a row's stage
   static constexpr int kM = 32 * MB * GM, kN = 32 * NB * GN;
   static constexpr int kCopiesA = kM * kVecs / kThreads, kCopiesB = kN * kVecs / kThreads;
   static_assert(kCopiesA * kThreads == kM * kVecs && kCopiesB * kThreads == kN * kVecs, "whole copies");
   // scale words: where a tile has fewer rows than threads, the waves without rows
-  // copy one word (so that every wave has the same number of copies in flight)
+  // copy one word (cheaper than a branch around the copy)
   static constexpr int kScalesA = kM < kThreads ? 1 : kM / kThreads, kScalesB = kN < kThreads ? 1 : kN / kThreads;
   static_assert(kM % 64 == 0 && kN % 64 == 0, "a wave copies 64 scale words");
-  static constexpr int kLoads = kCopiesA + kCopiesB + kScalesA + kScalesB;   // per wave and stage
 };
 
 // One stage's buffer, an object of its own: the compiler tells reads of one
@@ -66,7 +68,7 @@ struct Tile {
 template <class Tl>
 struct Stage {
   uint4 a[Tl::kM * Tl::kVecs], b[Tl::kN * Tl::kVecs];
-  uint32_t sa[Tl::kM], sb[Tl::kN], idle[64];
+  uint32_t sa[2][Tl::kM], sb[2][Tl::kN], idle[64];   // idle: for copies without a row
 };
 
 // Tile number -> (row tile, column tile): `group` row tiles down each column
@@ -103,7 +105,8 @@ __device__ __forceinline__ void store_block(void *y, size_t row, bool ok, int n0
         b[i] = sw[1];
       }
       const int n = n0 + 16 * q + 8 * h;
-      if (ok && n < N) *reinterpret_cast<uint4 *>(static_cast<T *>(y) + row * N + n) = make_uint4(a[0], a[1], b[0], b[1]);
+      if (ok && n < N)
+        *reinterpret_cast<uint4 *>(static_cast<T *>(y) + row * N + n) = make_uint4(a[0], a[1], b[0], b[1]);
     }
   } else if constexpr (VEC) {
 #pragma unroll
@@ -122,13 +125,12 @@ __device__ __forceinline__ void store_block(void *y, size_t row, bool ok, int n0
   }
 }
 
-template <int MB, int NB, int GM, int GN, int RING, int DT, bool GROUPED>
+template <int MB, int NB, int GM, int GN, int DT, bool GROUPED>
 __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
   using Tl = Tile<MB, NB, GM, GN>;
   using Buffer = Stage<Tl>;
   constexpr int TH = Tl::kThreads, CA = Tl::kCopiesA, CB = Tl::kCopiesB;
-  static_assert(RING == 3 || RING == 4, "ring");
-  __shared__ __attribute__((aligned(16))) Buffer q0, q1, q2, q3;
+  __shared__ __attribute__((aligned(16))) Buffer q0, q1;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 31, h = lane >> 5;
@@ -148,64 +150,75 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
     n_rows = g.M - i0;
   }
   const int col0 = tile_n * Tl::kN;
-  // K slice blockIdx.y: S stages from stage `first` on
-  const int all = g.K / kGroup, first = static_cast<int>(static_cast<long>(all) * blockIdx.y / gridDim.y);
-  const int S = static_cast<int>(static_cast<long>(all) * (blockIdx.y + 1) / gridDim.y) - first;
-  // activation row of list row i0 + i (rows past the end repeat the last one;
-  // their results are not stored)
+  // K slice blockIdx.y: S stages from stage `first` on. An odd number of groups
+  // leaves the last stage of the last slice half full.
+  const int all = g.K / kGroup, pairs = (all + 1) / 2;
+  const int first = static_cast<int>(static_cast<long>(pairs) * blockIdx.y / gridDim.y);
+  const int S = static_cast<int>(static_cast<long>(pairs) * (blockIdx.y + 1) / gridDim.y) - first;
+  const bool half_last = 2 * (first + S) > all;
+  // Activation row of list row i0 + i and weight row col0 + n, from the row the
+  // tile's base pointers stand at (rows past the end repeat the last one; their
+  // results are not stored). Offsets from there are 32-bit: a tile's rows, or
+  // with perm all of A's.
+  const int a_base = GROUPED ? 0 : i0;
   auto act_row = [&](int i) {
     int ia = i0 + min(i, n_rows - 1);
     if constexpr (GROUPED)
       if (g.perm) ia = g.perm[ia] / g.top_k;
-    return static_cast<size_t>(min(max(ia, 0), g.a_rows - 1));
+    return static_cast<uint32_t>(min(max(ia, 0), g.a_rows - 1) - a_base);
   };
-  auto weight_row = [&](int n) { return static_cast<size_t>(e) * g.N + min(col0 + n, g.N - 1); };
+  auto weight_row = [&](int n) { return static_cast<uint32_t>(min(n, g.N - 1 - col0)); };
+  const size_t b_base = static_cast<size_t>(e) * g.N + col0;
   constexpr int kVecs = Tl::kVecs;
+  const uint32_t row_bytes = g.K / 2;
   const int vec = (tid % kVecs) ^ ((tid >> 4) % kVecs);
-  const uint8_t *pa[CA], *pb[CB];
+  uint32_t oa[CA], ob[CB], osa[Tl::kScalesA], osb[Tl::kScalesB];
 #pragma unroll
-  for (int it = 0; it < CA; ++it)
-    pa[it] = g.a_codes + act_row((it * TH + tid) / kVecs) * (g.K / 2) + 64 * first + 16 * vec;
+  for (int it = 0; it < CA; ++it) oa[it] = act_row((it * TH + tid) / kVecs) * row_bytes + 16 * vec;
 #pragma unroll
-  for (int it = 0; it < CB; ++it)
-    pb[it] = g.b_codes + weight_row((it * TH + tid) / kVecs) * (g.K / 2) + 64 * first + 16 * vec;
-  const uint32_t *psa[Tl::kScalesA], *psb[Tl::kScalesB];
+  for (int it = 0; it < CB; ++it) ob[it] = weight_row((it * TH + tid) / kVecs) * row_bytes + 16 * vec;
 #pragma unroll
-  for (int it = 0; it < Tl::kScalesA; ++it)
-    psa[it] = g.a_scales + static_cast<size_t>(first) * g.a_rows + act_row(it * TH + tid < Tl::kM ? it * TH + tid : 0);
+  for (int it = 0; it < Tl::kScalesA; ++it) osa[it] = act_row(it * TH + tid < Tl::kM ? it * TH + tid : 0);
 #pragma unroll
-  for (int it = 0; it < Tl::kScalesB; ++it)
-    psb[it] = g.b_scales + static_cast<size_t>(first) * g.b_rows + weight_row(it * TH + tid < Tl::kN ? it * TH + tid : 0);
+  for (int it = 0; it < Tl::kScalesB; ++it) osb[it] = weight_row(it * TH + tid < Tl::kN ? it * TH + tid : 0);
+  // where the next stage in line begins
+  const uint8_t *pa = g.a_codes + static_cast<size_t>(a_base) * row_bytes + 128 * static_cast<size_t>(first);
+  const uint8_t *pb = g.b_codes + b_base * row_bytes + 128 * static_cast<size_t>(first);
+  const uint32_t *psa = g.a_scales + a_base + static_cast<size_t>(2 * first) * g.a_rows;
+  const uint32_t *psb = g.b_scales + b_base + static_cast<size_t>(2 * first) * g.b_rows;
 
-  // copies of the next stage in line; past the last one it repeats, so that
-  // every stage has the same number of copies in flight (never multiplied)
+  // Copies of the next stage in line; past the last one it repeats (never
+  // multiplied). A half-full stage repeats its first half. No branches: a stage's
+  // products and copies stay one block for the scheduler.
   int ahead = 0;
   auto issue = [&](Buffer &q) {
+    const bool half = half_last && ahead >= S - 1;
+    const uint32_t back = half && vec >= 4 ? 64 : 0;
+    const size_t second_a = half ? 0 : g.a_rows, second_b = half ? 0 : g.b_rows;
 #pragma unroll
-    for (int it = 0; it < CA; ++it) copy16_to_lds(pa[it], q.a + it * TH + wave * 64);
+    for (int it = 0; it < CA; ++it) copy16_to_lds(pa + (oa[it] - back), q.a + it * TH + wave * 64);
 #pragma unroll
-    for (int it = 0; it < CB; ++it) copy16_to_lds(pb[it], q.b + it * TH + wave * 64);
+    for (int it = 0; it < CB; ++it) copy16_to_lds(pb + (ob[it] - back), q.b + it * TH + wave * 64);
 #pragma unroll
-    for (int it = 0; it < Tl::kScalesA; ++it)
-      copy4_to_lds(psa[it], it * TH + wave * 64 < Tl::kM ? q.sa + it * TH + wave * 64 : q.idle);
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-    for (int it = 0; it < Tl::kScalesB; ++it)
-      copy4_to_lds(psb[it], it * TH + wave * 64 < Tl::kN ? q.sb + it * TH + wave * 64 : q.idle);
+      for (int it = 0; it < Tl::kScalesA; ++it)
+        copy4_to_lds(psa + (u ? second_a : 0) + osa[it],
+                     it * TH + wave * 64 < Tl::kM ? q.sa[u] + it * TH + wave * 64 : q.idle);
+#pragma unroll
+      for (int it = 0; it < Tl::kScalesB; ++it)
+        copy4_to_lds(psb + (u ? second_b : 0) + osb[it],
+                     it * TH + wave * 64 < Tl::kN ? q.sb[u] + it * TH + wave * 64 : q.idle);
+    }
     const bool more = ++ahead < S;
-    const int by = more ? 64 : 0;
-    const size_t da = more ? g.a_rows : 0, db = more ? g.b_rows : 0;
-#pragma unroll
-    for (int it = 0; it < CA; ++it) pa[it] += by;
-#pragma unroll
-    for (int it = 0; it < CB; ++it) pb[it] += by;
-#pragma unroll
-    for (int it = 0; it < Tl::kScalesA; ++it) psa[it] += da;
-#pragma unroll
-    for (int it = 0; it < Tl::kScalesB; ++it) psb[it] += db;
+    pa += more ? 128 : 0;
+    pb += more ? 128 : 0;
+    psa += more ? 2 * static_cast<size_t>(g.a_rows) : 0;
+    psb += more ? 2 * static_cast<size_t>(g.b_rows) : 0;
   };
 
   const int wm = (wave / GN) * 32 * MB, wn = (wave % GN) * 32 * NB;
-  const int key = (r >> 2) % kVecs;
+  const int key = (r >> 1) % kVecs;
   v16f_t acc[MB][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
@@ -227,11 +240,11 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
 #pragma unroll
     for (int i = 0; i < MB; ++i) f.a[i] = operand(q.a[(wm + 32 * i + r) * kVecs + at]);
   };
-  auto read_scales = [&](Scales &v, const Buffer &q) {
+  auto read_scales = [&](Scales &v, const Buffer &q, int u) {
 #pragma unroll
-    for (int i = 0; i < MB; ++i) v.a[i] = q.sa[wm + 32 * i + r] >> (8 * h);
+    for (int i = 0; i < MB; ++i) v.a[i] = q.sa[u][wm + 32 * i + r] >> (8 * h);
 #pragma unroll
-    for (int j = 0; j < NB; ++j) v.b[j] = q.sb[wn + 32 * j + r] >> (8 * h);
+    for (int j = 0; j < NB; ++j) v.b[j] = q.sb[u][wn + 32 * j + r] >> (8 * h);
   };
 #define LBQ_MX_STEP(F, SEL, V)                                                                                  \
   do {                                                                                                          \
@@ -242,76 +255,67 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
 
   Step f0, f1;
   Scales v0, v1;
-  // After a wait for its own copies: every wave's have landed, and every wave is
-  // done with its reads so far.
+  // Every copy and LDS read of this wave is done; past the barrier every wave's.
   auto meet = [&]() {
+    wait_vm_lds<0>();
     __builtin_amdgcn_sched_barrier(0);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
   };
-  // Stage in cur, its first step's operands in f0, its first scales in v0; free
-  // takes the copies. The order of the instructions: LDS reads (a step's, while
-  // the step before it is multiplied), then copies, one by one between products,
-  // so that neither holds up the matrix cores (8192 x 4096 x 14336: 261 -> 243 us
-  // against the compiler's own order).
-  auto stage = [&](const Buffer &cur, const Buffer &next, Buffer &free) {
-    wait_vm_lds<(RING - 3) * Tl::kLoads>();   // the stage after this one
-    meet();
-    issue(free);
+  // Stage in cur, its first step's operands in f0, its first scales in v0, the
+  // next stage on its way into next. Between the products go, one by one, the LDS
+  // reads of the step after (and in the last step the copies), so that neither
+  // holds up the matrix cores.
+  constexpr int kP = MB * NB, kR = MB + NB;
+  auto stage = [&](Buffer &cur, const Buffer &next) {
     read(f1, cur, 1);
     LBQ_MX_STEP(f0, 0, v0);
-    v1 = v0;
+    read(f0, cur, 2);
+    read_scales(v1, cur, 1);
+    LBQ_MX_STEP(f1, 2, v0);
+    read(f1, cur, 3);
+    LBQ_MX_STEP(f0, 0, v1);
+#pragma unroll
+    for (int u = 0; u < 3; ++u)
+#pragma unroll
+      for (int i = 0; i < kP; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (i < kR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if (u == 1 && i < kR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);   // the scales
+      }
+    meet();
+    issue(cur);
     read(f0, next, 0);
-    read_scales(v0, next);
+    read_scales(v0, next, 0);
     LBQ_MX_STEP(f1, 2, v1);
-    constexpr int kP = MB * NB, kR = MB + NB;
 #pragma unroll
     for (int i = 0; i < kP; ++i) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      if (i < kR) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (i >= kR) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < kP; ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x010, 2, 0);
       if (i < kR) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-      if (i >= kR) __builtin_amdgcn_sched_group_barrier(0x010, 1, 0);
     }
   };
   issue(q0);
-  issue(q1);
-  if constexpr (RING == 4) issue(q2);
-  wait_vm_lds<(RING - 2) * Tl::kLoads>();
   meet();
+  issue(q1);
   read(f0, q0, 0);
-  read_scales(v0, q0);
-  // whole rounds of the ring, then what is left of one (no exits inside the
-  // loop: the accumulators keep their registers)
-  const int rest = S % RING;
-  for (int n = S / RING; n > 0; --n) {
-    if constexpr (RING == 4) {
-      stage(q0, q1, q3);
-      stage(q1, q2, q0);
-      stage(q2, q3, q1);
-      stage(q3, q0, q2);
-    } else {
-      stage(q0, q1, q2);
-      stage(q1, q2, q0);
-      stage(q2, q0, q1);
-    }
+  read_scales(v0, q0, 0);
+  // whole stages by twos, then what is left (no exits inside the loop: the
+  // accumulators keep their registers)
+  const int full = S - (half_last ? 1 : 0);
+  for (int n = full / 2; n > 0; --n) {
+    stage(q0, q1);
+    stage(q1, q0);
   }
-  if (rest > 0) {
-    if constexpr (RING == 4) stage(q0, q1, q3);
-    else stage(q0, q1, q2);
+  const bool odd = full & 1;
+  if (odd) stage(q0, q1);
+  if (half_last) {
+    read(f1, odd ? q1 : q0, 1);
+    LBQ_MX_STEP(f0, 0, v0);
+    LBQ_MX_STEP(f1, 2, v0);
   }
-  if (rest > 1) {
-    if constexpr (RING == 4) stage(q1, q2, q0);
-    else stage(q1, q2, q0);
-  }
-  if constexpr (RING == 4)
-    if (rest > 2) stage(q2, q3, q1);
 #undef LBQ_MX_STEP
   wait_vm_lds<0>();   // no copy into LDS outlives the workgroup
   const bool vecs = g.N % 8 == 0;
@@ -343,7 +347,7 @@ __global__ void __launch_bounds__(256) mx_sum_kernel(const float *__restrict__ p
   }
 }
 
-template <int MB, int NB, int GM, int GN, int RING>
+template <int MB, int NB, int GM, int GN>
 hipError_t launch_tiles(GemmArgs g, int dtype, int slices, hipStream_t s) {
   using Tl = Tile<MB, NB, GM, GN>;
   // grouped: every expert may end in a ragged tile
@@ -354,8 +358,8 @@ hipError_t launch_tiles(GemmArgs g, int dtype, int slices, hipStream_t s) {
   g.tiles_n = static_cast<int>(tn);
   const dim3 grid(static_cast<unsigned>(tm * tn), static_cast<unsigned>(slices)), block(Tl::kThreads);
 #define LBQ_MX_GO(DT)                                                                                       \
-  if (g.E > 0) hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, RING, DT, true>), grid, block, 0, s, g);        \
-  else hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, RING, DT, false>), grid, block, 0, s, g)
+  if (g.E > 0) hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, DT, true>), grid, block, 0, s, g);        \
+  else hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, DT, false>), grid, block, 0, s, g)
   if (dtype == kF16) {
     LBQ_MX_GO(kF16);
   } else if (dtype == kBF16) {
@@ -367,36 +371,33 @@ hipError_t launch_tiles(GemmArgs g, int dtype, int slices, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Which tile, and how many slices of K.
-//
-// Dense: a workgroup per compute unit takes, per 4096 of K, about 41 us on 256 x
-// 256, 13.6 on 128 x 128 and 8.7 on 64 x 128 (4096^3 and 512 x 4096^2); the
-// smallest sum of rounds wins. Fewer tiles of the smallest kind than half the
-// compute units: K in slices of at least 1024.
-//
-// Grouped, by the average expert's rows: 64 x 256 to 96 rows, where the experts'
-// weights are what has to move (256 experts of 2048 x 2048, 64 rows: 181 us;
-// 128 x 128 193, 256 x 256 226), 128 x 128 below 512 (8 experts of 4096 x 4096,
-// 128 rows: 31 us; 36 and 37), else 256 x 256 (28672 x 4096, 2048 rows: 1.39 ms;
-// 128 x 128 1.71).
+// Which tile, and how many slices of K. Per 4096 of K, T tiles take about, in us:
+// 256 x 256, one workgroup on a compute unit, 41 a round of 256; 128 x 128, two,
+// 6 + 12 T / 256; 64 x 128, three, 6 + 6.6 T / 256 (T at least 256 in both). The
+// least of them is taken. Measured at K = 4096 (64 x 128, 128 x 128, 256 x 256):
+// 512 x 4096 12.7, 16.0, 34.1; 2048 x 4096 34, 28, 36; 400 x 28672 47, 44, 40;
+// 4096 x 4096 59, 48, 43. Grouped, every expert's last tile is taken to be half
+// full: 256 experts of 2048 x 2048, 64 rows each, 175, 191, 235; 8 of 4096 x 4096,
+// 512 rows, 81, 73, 88; 8 of 28672 x 4096, 2048 rows, 2085, 1681, 1355. Dense with
+// fewer tiles of the smallest kind than half the compute units: K in slices of
+// at least 1024.
 struct Plan {
   int bm, bn, slices;
 };
 Plan plan_tiles(const MxGemm &p) {
-  if (p.E > 0) {
-    const int avg = p.M / p.E;
-    if (avg <= 96) return {64, p.N <= 128 ? 128 : 256, 1};
-    return avg < 512 ? Plan{128, 128, 1} : Plan{256, 256, 1};
-  }
   auto tiles = [&](int bm, int bn) {
-    return ((static_cast<long>(p.M) + bm - 1) / bm) * ((static_cast<long>(p.N) + bn - 1) / bn);
+    const long tm = p.E > 0 ? std::max<long>(p.M / bm + p.E / 2, std::min(p.E, p.M))
+                            : (static_cast<long>(p.M) + bm - 1) / bm;
+    return tm * ((static_cast<long>(p.N) + bn - 1) / bn);
   };
-  auto rounds = [&](int bm, int bn) { return static_cast<double>((tiles(bm, bn) + 255) / 256); };
-  const double big = 41 * rounds(256, 256), mid = 13.6 * rounds(128, 128), small = 8.7 * rounds(64, 128);
+  auto per_unit = [&](int bm, int bn) { return std::max(1.0, tiles(bm, bn) / 256.0); };
+  const double big = 41 * static_cast<double>((tiles(256, 256) + 255) / 256);
+  const double mid = 6 + 12 * per_unit(128, 128), small = 6 + 6.6 * per_unit(64, 128);
   if (big <= mid && big <= small) return {256, 256, 1};
   if (mid <= small) return {128, 128, 1};
   Plan r{64, 128, 1};
-  while (r.slices < 8 && tiles(64, 128) * r.slices * 2 <= 256 && p.K / (r.slices * 2) >= 1024) r.slices *= 2;
+  if (p.E == 0)
+    while (r.slices < 8 && tiles(64, 128) * r.slices * 2 <= 256 && p.K / (r.slices * 2) >= 1024) r.slices *= 2;
   return r;
 }
 
@@ -426,10 +427,9 @@ hipError_t launch_mx_gemm(const MxGemm &p, hipStream_t s) {
   g.top_k = p.top_k;
   const int dtype = r.slices > 1 ? kF32 : p.dtype;
   hipError_t e;
-  if (r.bm == 256) e = launch_tiles<4, 4, 2, 2, 4>(g, dtype, r.slices, s);
-  else if (r.bm == 128) e = launch_tiles<2, 2, 2, 2, 3>(g, dtype, r.slices, s);
-  else if (r.bn == 256) e = launch_tiles<2, 2, 1, 4, 3>(g, dtype, r.slices, s);
-  else e = launch_tiles<1, 2, 2, 2, 4>(g, dtype, r.slices, s);
+  if (r.bm == 256) e = launch_tiles<4, 4, 2, 2>(g, dtype, r.slices, s);
+  else if (r.bm == 128) e = launch_tiles<2, 2, 2, 2>(g, dtype, r.slices, s);
+  else e = launch_tiles<1, 2, 2, 2>(g, dtype, r.slices, s);
   if (e != hipSuccess || r.slices == 1) return e;
   const long n = static_cast<long>(p.M) * p.N;
   hipLaunchKernelGGL(mx_sum_kernel, dim3(static_cast<unsigned>(std::min<long>((n + 255) / 256, 2048))), dim3(256), 0, s,

@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(kThreads) mx_stream_kernel(MxGemm g, int T16, 
       } else {
         codes = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(g.a_codes) +
                                                  static_cast<size_t>(ia) * row_bytes + 16 * b);
-        byte = (static_cast<const uint32_t *>(g.a_scales)[static_cast<size_t>(b >> 2) * g.a_rows + ia] >> (8 * (b & 3))) & 0xFFu;
+        const uint32_t *words = static_cast<const uint32_t *>(g.a_scales) + static_cast<size_t>(b >> 2) * g.a_rows;
+        byte = (words[ia] >> (8 * (b & 3))) & 0xFFu;
       }
       *reinterpret_cast<uint4 *>(tok + t * tok_row + 16 * b) = codes;
       tok[tok_scales + t * blocks + b] = static_cast<uint8_t>(byte);
@@ -173,7 +174,8 @@ __global__ void __launch_bounds__(kThreads) mx_stream_kernel(MxGemm g, int T16, 
         } else {
           codes = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(g.a_codes) +
                                                    static_cast<size_t>(ia) * row_bytes + 64 * gi + 16 * q);
-          byte = (static_cast<const uint32_t *>(g.a_scales)[static_cast<size_t>(gi) * g.a_rows + ia] >> (8 * q)) & 0xFFu;
+          const uint32_t *words = static_cast<const uint32_t *>(g.a_scales) + static_cast<size_t>(gi) * g.a_rows;
+          byte = (words[ia] >> (8 * q)) & 0xFFu;
         }
       }
       a[m][i] = codes;
@@ -242,7 +244,8 @@ hipError_t launch(const MxGemm &g, int tiles, hipStream_t s) {
   const int T16 = (g.N + 15) / 16;
   if (g.E > 0 && T16 >= 4 * kMany) {
     const int walkers = std::min((T16 + kMany - 1) / kMany, std::max(1, 1024 / tiles));
-    hipLaunchKernelGGL((mx_stream_kernel<MT, GPW, kMany>), dim3(tiles * walkers), dim3(kThreads), 0, s, g, T16, walkers);
+    hipLaunchKernelGGL((mx_stream_kernel<MT, GPW, kMany>), dim3(tiles * walkers), dim3(kThreads), 0, s, g, T16,
+                       walkers);
   } else {
     const int walkers = std::min(T16, std::max(1, 256 / tiles));
     hipLaunchKernelGGL((mx_stream_kernel<MT, GPW, 1>), dim3(tiles * walkers), dim3(kThreads), 0, s, g, T16, walkers);

@@ -409,7 +409,8 @@ lbq_status lbq_stream_read(const void *buf, size_t bytes, int32_t grid, int32_t 
  *           and 2i + 1 in its high nibble.
  *   scales: uint8 [C/128][R][4]; byte b of word (g, r) belongs to values
  *           128 g + 32 b .. 128 g + 32 b + 31 of row r.
- * R is at most 2^30 and R * (C/128) below 2^31 (LBQ_ERR_SHAPE otherwise).
+ * R is at most 2^30, C at most 2^24 and R * (C/128) below 2^31 (LBQ_ERR_SHAPE
+ * otherwise).
  * These calls take no rotation signs: lbq_rotate the activations, and the
  * weights before they are quantized, where a rotated basis is wanted. Outputs
  * overlap no input. They have no gradient of their own: a layer's backward pass
@@ -484,7 +485,8 @@ lbq_status lbq_mx_grouped_workspace(const lbq_mx *w, int32_t E, int32_t M, int32
  * offsets and perm as lbq_moe_route or lbq_moe_sort write them; rows of y from
  * offsets[E] on are left as they were. offsets are clamped to [0, T] and x's
  * row numbers to [0, M): contents out of range give wrong rows, never an access
- * out of bounds. Limits: E <= 1024. Errors as lbq_mx_matmul. */
+ * out of bounds. Limits: E <= 1024, M * w.cols below 2^33. Errors as
+ * lbq_mx_matmul. */
 lbq_status lbq_mx_grouped_forward(const lbq_mx *w, int32_t E, const void *x, int32_t M, const int32_t *offsets,
                                   const int32_t *perm, int32_t top_k, int32_t T, void *y, int32_t dtype, void *ws,
                                   size_t ws_bytes, void *stream);

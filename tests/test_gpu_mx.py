@@ -169,7 +169,8 @@ def test_matmul(L, dev, m, n, k, dtype):
 
 @pytest.mark.parametrize("m,n,k", [(700, 1100, 2176), (1030, 260, 4096), (5, 9000, 1024), (40, 70, 17408),
                                    (600, 600, 8192), (100, 200, 4096), (130, 500, 14336), (77, 131, 17408),
-                                   (64, 640, 4096), (65, 8, 2176)])
+                                   (64, 640, 4096), (65, 8, 2176), (900, 5000, 128), (2000, 2100, 384),
+                                   (1100, 2300, 640), (2100, 1030, 256), (2400, 3600, 384), (4000, 3900, 384)])
 def test_matmul_larger(L, dev, m, n, k):
     import torch
 
@@ -222,7 +223,8 @@ def _routing(m, E, k, item):
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 @pytest.mark.parametrize("m,E,top_k,n,k", [(1, 4, 1, 40, 128), (3, 256, 8, 64, 256), (32, 16, 4, 130, 512),
                                            (150, 3, 2, 100, 384), (400, 2, 1, 300, 640), (9, 1, 1, 33, 1024),
-                                           (70, 1024, 6, 16, 128), (900, 5, 3, 140, 256)])
+                                           (70, 1024, 6, 16, 128), (900, 5, 3, 140, 256), (700, 6, 3, 500, 384),
+                                           (3000, 4, 2, 1100, 128), (2100, 4, 2, 3500, 384)])
 def test_grouped(L, dev, m, E, top_k, n, k, dtype):
     import torch
 

@@ -25,7 +25,7 @@ def test_bytes(L):
     lib, a, b = L.lib(), ctypes.c_size_t(), ctypes.c_size_t()
     assert lib.lbq_mx_bytes(10, 256, ctypes.byref(a), ctypes.byref(b)) == OK and (a.value, b.value) == (1280, 80)
     assert lib.lbq_mx_bytes(0, 128, ctypes.byref(a), ctypes.byref(b)) == OK and (a.value, b.value) == (0, 0)
-    for rows, cols in ((-1, 128), (1, 0), (1, 64), (1, 130), (2 ** 31 - 1, 128), (2 ** 30 + 1, 128), (2 ** 30, 256)):
+    for rows, cols in ((-1, 128), (1, 0), (1, 64), (1, 130), (2 ** 31 - 1, 128), (2 ** 30 + 1, 128), (2 ** 30, 256), (1, 2 ** 24 + 128)):
         assert lib.lbq_mx_bytes(rows, cols, ctypes.byref(a), ctypes.byref(b)) == SHAPE
     assert lib.lbq_mx_bytes(1, 128, None, ctypes.byref(b)) == NULL
 
@@ -83,6 +83,7 @@ def test_product_refusals(L):
     assert grouped(w=_mx(L, 2050, 128), E=1025) == SHAPE
     assert grouped(perm=None) == SHAPE                             # without perm x has T rows
     assert grouped(T=2 ** 30 + 1) == SHAPE and grouped(M=-1) == SHAPE
+    assert grouped(w=_mx(L, 6, 4096), M=2 ** 21) == SHAPE           # 2^33 values of x
     assert grouped(dt=2) == FORMAT and grouped(off=None) == NULL and grouped(y=P + 2) == ALIGN
     assert grouped(off=P + 2) == ALIGN and grouped(perm=P + 2) == ALIGN
     assert grouped(M=0, x=None, off=None, y=None, ws=None, T=0) == OK
