@@ -15,7 +15,9 @@
 // weight row 4 q + i, token c.
 //
 // Bound: HBM, (17/32) N K bytes; with fewer than a few MB to read, the latency
-// of one load and the launch.
+// of one load and the launch. One token 4096 -> 4096 5.2 us; 16 tokens 4096 ->
+// 28672 15 us, 4.2 TB/s; 32 tokens on 163 of 256 experts of 2048 x 2048 57 us,
+// 6.4 TB/s.
 #include "device.h"
 #include "gemm_common.h"
 #include "kernels.h"

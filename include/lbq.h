@@ -445,7 +445,7 @@ lbq_status lbq_mx_quantize(const void *x, int32_t dtype, int32_t rows, int32_t c
  * tensor of cols rows and Rp = rows rounded up to a multiple of 128 columns,
  * the columns past rows zero. What a product needs whose sum runs over x's
  * rows (the weight's gradient sums over tokens, the input's over outputs).
- * rows is at most 128 * 65535. */
+ * rows is at most 128 * 65535, cols at most 2^30 - 64. */
 lbq_status lbq_mx_quantize_t(const void *x, int32_t dtype, int32_t rows, int32_t cols, void *codes, void *scales,
                              void *stream);
 

@@ -45,6 +45,7 @@ def test_quantize_refusals(L):
         assert f(P, 0, 0, 128, None, None, None) == OK           # nothing to do
     assert lib.lbq_mx_quantize(P, 0, 4, 100, P, P, None) == SHAPE
     assert lib.lbq_mx_quantize_t(P, 0, 2 ** 31 - 1, 4, P, P, None) == SHAPE
+    assert lib.lbq_mx_quantize_t(P, 2, 1, 2 ** 30 - 63, P, P, None) == SHAPE
     assert lib.lbq_mx_dequantize(None, P, 0, None) == NULL
     assert lib.lbq_mx_dequantize(_mx(L, 4, 128), None, 0, None) == NULL
     assert lib.lbq_mx_dequantize(_mx(L, 4, 128), P, 9, None) == FORMAT
