@@ -362,6 +362,46 @@ def test_training_step_of_one_linear(L, dev):
     _check_product(dw, q(R.transposed(dy64)), q(R.transposed(x64)), "float32")
 
 
+def test_gradients_against_differences(L, dev):
+    """Values on the e2m1 grid with a 6 in every block of 32 along both axes: quantizing keeps them, and every
+    sum is a multiple of 1/4 below 2^22, exact in fp32. L = <dy, x W^T> is linear in each value, so its
+    difference over one value's step equals the gradient's value times the step, exactly."""
+    import torch
+
+    m, k, n = 128, 256, 128
+    g = synth.rng(64, 41, synth.ROLE_LOGITS)
+    grid = np.array([-6, -4, -3, -2, -1.5, -1, -0.5, 0, 0.5, 1, 1.5, 2, 3, 4, 6])
+
+    def tensor(rows, cols):
+        v = g.choice(grid, (rows, cols))
+        for i in range(32):
+            v[i::32, i::32] = 6.0
+        return v
+
+    def dev32(v):
+        return torch.from_numpy(v.astype(np.float32)).cuda()
+
+    x, w, dy = tensor(m, k), tensor(n, k), tensor(m, n)
+    dx = L.mx_matmul(L.mx_quantize(dev32(dy)), L.mx_quantize(dev32(w), transpose=True)).double().cpu().numpy()
+    dw = L.mx_matmul(L.mx_quantize(dev32(dy), transpose=True),
+                     L.mx_quantize(dev32(x), transpose=True)).double().cpu().numpy()
+    assert np.array_equal(dx, dy @ w) and np.array_equal(dw, dy.T @ x)
+
+    def loss(a, b):
+        y = L.mx_matmul(L.mx_quantize(dev32(a)), L.mx_quantize(dev32(b)))
+        return float((y.double().cpu().numpy() * dy).sum())
+    at = loss(x, w)
+    for which, v, grad in (("x", x, dx), ("w", w, dw)):
+        for _ in range(8):
+            i, j = int(g.integers(0, v.shape[0])), int(g.integers(0, v.shape[1]))
+            if i % 32 == j % 32:
+                j = (j + 1) % v.shape[1]               # the 6 that holds the block's scale stays
+            step = v.copy()
+            step[i, j] = 1.0 if v[i, j] != 1.0 else -2.0
+            moved = loss(step, w) if which == "x" else loss(x, step)
+            assert moved - at == grad[i, j] * (step[i, j] - v[i, j]), (which, i, j)
+
+
 def test_moe_block_end_to_end(L, dev):
     """A routed block in MXFP4: route, sort, gate|up, SwiGLU, down, combine. Each step is compared on the inputs
     that the GPU's own earlier steps gave, so a rounding that falls the other way does not spread."""
