@@ -92,14 +92,17 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return from_f32<DT>(a) | (static_cast<uint32_t>(from_f32<DT>(b)) << 16);
 }
 
-// One 32 x 32 result block: token row m (the lane's), outputs n0 .. n0 + 31.
-// VEC: N is a multiple of 8, so eight neighbouring outputs (four in fp32) are
-// one aligned 16-byte store. The halves of a token's outputs sit in lanes
-// (m, 0) and (m, 1); a lane swap gives each eight neighbours.
-template <int DT, bool VEC>
-__device__ __forceinline__ void store_block(void *y, size_t row, bool ok, int n0, int N, int h, const v16f_t &acc) {
-  using T = typename Elem<DT>::type;
-  if constexpr (VEC && DT != kF32) {
+// One 32 x 32 result block into LDS: the lane's token is a row at `at`, its
+// outputs as they lie in y. The halves of a token's eight neighbouring 16-bit
+// outputs sit in lanes (m, 0) and (m, 1); a lane swap gives each eight.
+template <int DT>
+__device__ __forceinline__ void place_block(uint8_t *at, int h, const v16f_t &acc) {
+  if constexpr (DT == kF32) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<float4_t *>(at + 4 * (8 * q + 4 * h)) =
+          float4_t{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+  } else {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
       uint32_t a[2], b[2];
@@ -111,23 +114,7 @@ __device__ __forceinline__ void store_block(void *y, size_t row, bool ok, int n0
         a[i] = sw[0];
         b[i] = sw[1];
       }
-      const int n = n0 + 16 * q + 8 * h;
-      if (ok && n < N)
-        *reinterpret_cast<uint4 *>(static_cast<T *>(y) + row * N + n) = make_uint4(a[0], a[1], b[0], b[1]);
-    }
-  } else if constexpr (VEC) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = n0 + 8 * q + 4 * h;
-      if (ok && n < N)
-        *reinterpret_cast<float4_t *>(static_cast<T *>(y) + row * N + n) =
-            float4_t{acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int n = n0 + 8 * (k / 4) + 4 * h + k % 4;
-      if (ok && n < N) static_cast<T *>(y)[row * N + n] = from_f32<DT>(acc[k]);
+      *reinterpret_cast<uint4 *>(at + 2 * (16 * q + 8 * h)) = make_uint4(a[0], a[1], b[0], b[1]);
     }
   }
 }
@@ -324,20 +311,47 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
     LBQ_MX_STEP(f1, 2, v0);
   }
 #undef LBQ_MX_STEP
-  wait_vm_lds<0>();   // no copy into LDS outlives the workgroup
-  const bool vecs = g.N % 8 == 0;
+  meet();   // no copy is under way any more, and no operand is read
   // slices write partial results one behind the other
-  void *y = g.y;
-  if constexpr (DT == kF32) y = static_cast<float *>(y) + static_cast<size_t>(blockIdx.y) * g.M * g.N;
+  using T = typename Elem<DT>::type;
+  T *y = static_cast<T *>(g.y);
+  if constexpr (DT == kF32) y += static_cast<size_t>(blockIdx.y) * g.M * g.N;
+  if (g.N % 8 == 0) {
+    // 32 tokens at a time through LDS, so that neighbouring lanes store
+    // neighbouring outputs: kChunk bytes of a row by kLanes lanes.
+    constexpr int kSize = sizeof(T), kChunk = 64 * NB, kPitch = kChunk + 16, kLanes = kChunk / 16;
+    constexpr int kBlocks = kChunk / (32 * kSize), kPer = 64 / kLanes;
+    static_assert(sizeof(Buffer) >= GM * GN * 32 * kPitch, "a wave's rows");
+    uint8_t *mine = reinterpret_cast<uint8_t *>(&q0) + wave * 32 * kPitch;
+    const int at = lane % kLanes;
 #pragma unroll
-  for (int i = 0; i < MB; ++i) {
-    const int row = wm + 32 * i + r;
-    const size_t at = static_cast<size_t>(i0) + row;
+    for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-      const int n0 = col0 + wn + 32 * j;
-      if (vecs) store_block<DT, true>(y, at, row < n_rows, n0, g.N, h, acc[i][j]);
-      else store_block<DT, false>(y, at, row < n_rows, n0, g.N, h, acc[i][j]);
+      for (int j0 = 0; j0 < NB; j0 += kBlocks) {
+#pragma unroll
+        for (int j = 0; j < kBlocks; ++j) place_block<DT>(mine + r * kPitch + 32 * kSize * j, h, acc[i][j0 + j]);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        const int n = col0 + wn + 32 * j0 + at * (16 / kSize);
+#pragma unroll
+        for (int p = 0; p < 32; p += kPer) {
+          const int row = p + lane / kLanes, token = wm + 32 * i + row;
+          const uint4 v = *reinterpret_cast<const uint4 *>(mine + row * kPitch + 16 * at);
+          if (token < n_rows && n < g.N)
+            *reinterpret_cast<uint4 *>(y + (static_cast<size_t>(i0) + token) * g.N + n) = v;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < MB; ++i) {
+      const int token = wm + 32 * i + r;
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int n = col0 + wn + 32 * j + 8 * (k / 4) + 4 * h + k % 4;
+          if (token < n_rows && n < g.N) y[(static_cast<size_t>(i0) + token) * g.N + n] = from_f32<DT>(acc[i][j][k]);
+        }
     }
   }
 }
