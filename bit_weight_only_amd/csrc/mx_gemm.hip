@@ -9,10 +9,10 @@
 //
 // Bound: with many rows the matrix cores at the clock that the power limit leaves
 // (6.3 PFLOP/s without any loads, on random codes), the copies into LDS beside
-// them, and the results' way out after each tile. 8192 tokens 4096 -> 14336 260
-// us, 3.7 PFLOP/s; 14336 -> 4096 293 us, 3.3; matrix cores 0.38 and 0.42 busy. With
+// them, and the results' way out after each tile. 8192 tokens 4096 -> 14336 279
+// us, 3.4 PFLOP/s; 14336 -> 4096 255 us, 3.8; matrix cores 0.40 and 0.43 busy. With
 // few rows per expert, HBM and the start and end of each tile (256 experts of
-// 2048 x 2048, 64 rows each: 654 MB fetched in 174 us, 3.8 TB/s).
+// 2048 x 2048, 64 rows each: 654 MB fetched in 169 us, 3.9 TB/s).
 #include "device.h"
 #include "gemm_common.h"
 #include "kernels.h"
@@ -318,7 +318,9 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
   if constexpr (DT == kF32) y += static_cast<size_t>(blockIdx.y) * g.M * g.N;
   if (g.N % 8 == 0) {
     // 32 tokens at a time through LDS, so that neighbouring lanes store
-    // neighbouring outputs: kChunk bytes of a row by kLanes lanes.
+    // neighbouring outputs: kChunk bytes of a row by kLanes lanes (8192 tokens 4096
+    // -> 14336 279 us; straight from the registers, 32 bytes of a row by two
+    // lanes, 287; in fp32, 14336 x 4096 over 8192 tokens, 273 and 294).
     constexpr int kSize = sizeof(T), kChunk = 64 * NB, kPitch = kChunk + 16, kLanes = kChunk / 16;
     constexpr int kBlocks = kChunk / (32 * kSize), kPer = 64 / kLanes;
     static_assert(sizeof(Buffer) >= GM * GN * 32 * kPitch, "a wave's rows");
