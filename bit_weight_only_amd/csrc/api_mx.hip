@@ -174,7 +174,9 @@ lbq_status lbq_mx_quantize_t(const void *x, int32_t dtype, int32_t rows, int32_t
   const int64_t padded = (static_cast<int64_t>(rows) + 127) / 128 * 128;
   // the transposed tensor's columns are an int32, its row groups a grid dimension,
   // and so are 64 of its rows, of 256 threads
-  if (padded > INT32_MAX || padded / 128 > 65535 || cols > kMaxRows - 64 || (rows > 0 && !mx_shape(cols, padded))) return LBQ_ERR_SHAPE;
+  if (padded > INT32_MAX || padded / 128 > 65535 || cols > kMaxRows - 64 ||
+      (rows > 0 && !mx_shape(cols, padded)))
+    return LBQ_ERR_SHAPE;
   if (!value_type(dtype)) return LBQ_ERR_FORMAT;
   if (rows == 0) return LBQ_OK;
   if (!x || !codes || !scales) return LBQ_ERR_NULL;
