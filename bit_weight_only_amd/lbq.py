@@ -453,6 +453,7 @@ def moe_from_host(packed: dict, bits, signs_hidden, signs_ffn, hidden: int, ffn:
 # foreign call.
 
 F16, BF16, F32 = 0, 1, 2
+_MOST = 2 ** 31 - 1   # a size of the C ABI; ctypes would cut a larger one off without a word
 _torch = None
 _dtypes: dict = {}
 
@@ -488,8 +489,8 @@ def _need(where: str, gpu: int, dtype, shape, t):
 
 def _rows(where: str, t) -> int:
     """The GPU of t, a contiguous matrix in a value type."""
-    if t.dim() != 2:
-        raise LbqError(-2, f"{where}: a matrix is needed, got {tuple(t.shape)}")
+    if t.dim() != 2 or t.shape[0] > _MOST or t.shape[1] > _MOST:
+        raise LbqError(-2, f"{where}: a matrix of 32-bit sizes is needed, got {tuple(t.shape)}")
     gpu = t.get_device()
     _need(where, gpu, t.dtype, None, t)
     return gpu
@@ -512,6 +513,10 @@ def _on(gpu: int, stream, go):
 @functools.lru_cache(maxsize=4096)
 def _query(name: str, args: tuple) -> int:
     """A *_workspace query; sizes alone decide it. Tensors are given as (rows, cols)."""
+    for a in args:
+        for n in a if isinstance(a, tuple) else (a,):
+            if not -_MOST <= n <= _MOST:
+                raise LbqError(-2, f"{name}: {args}")
     need = ctypes.c_size_t()
     p = ctypes.c_void_p(16)   # aligned stand-in: queries look at sizes only
     views = [Mx(a[0], a[1], p, p) if isinstance(a, tuple) else a for a in args]
@@ -542,6 +547,8 @@ class MxTensor:
         if codes.dim() != 2 or codes.shape[1] % 64 or codes.shape[1] == 0:
             raise LbqError(-2, "MxTensor: codes are [rows][cols/2], cols a positive multiple of 128")
         rows, half = codes.shape
+        if rows > _MOST or 2 * half > _MOST:
+            raise LbqError(-2, f"MxTensor: {rows} x {2 * half}")
         gpu = codes.get_device()
         _need("MxTensor", gpu, _torch.uint8, None, codes)
         _need("MxTensor", gpu, _torch.uint8, (half // 64, rows, 4), scales)
@@ -649,8 +656,8 @@ def mx_grouped_forward(w: MxTensor, E: int, x, offsets, perm=None, top_k: int = 
     _need(where, gpu, dtype, None, x)
     if x.dim() != 2 or x.shape[1] != w.cols:
         raise LbqError(-2, "mx_grouped_forward: x is [M][w.cols]")
-    if E < 1 or w.rows % E:
-        raise LbqError(-2, "mx_grouped_forward: w holds E experts of equal rows")
+    if E < 1 or w.rows % E or top_k > _MOST:
+        raise LbqError(-2, f"mx_grouped_forward: w holds E experts of equal rows; E {E}, top_k {top_k}")
     M, N = x.shape[0], w.rows // E
     _need(where, gpu, _torch.int32, (E + 1,), offsets)
     T = M
@@ -697,8 +704,8 @@ def moe_sort(ids, E: int, stream=None):
 
 def _places(where: str, gpu: int, pos):
     _need(where, gpu, _torch.int32, None, pos)
-    if pos.dim() != 2:
-        raise LbqError(-2, f"{where}: pos is [M][top_k]")
+    if pos.dim() != 2 or pos.shape[0] > _MOST or pos.shape[1] > _MOST:
+        raise LbqError(-2, f"{where}: pos is [M][top_k], got {tuple(pos.shape)}")
     return pos.shape
 
 
@@ -713,6 +720,7 @@ def moe_gather(x, pos, out=None, stream=None):
     if x.shape[0] != M:
         raise LbqError(-2, f"moe_gather: {x.shape[0]} rows, places of {M}")
     if out is not None:
+        _rows("moe_gather", out)
         _need("moe_gather", gpu, x.dtype, (out.shape[0], H), out)
 
     def go(s):

@@ -136,6 +136,64 @@ def test_binding_refusals(L):
         assert e.value.status in (SHAPE, FORMAT)
 
 
+def test_sizes_past_32_bits(L, monkeypatch):
+    """A size that a C int does not hold is refused, not cut off: 2^32 + n would arrive as n (meta tensors that
+    claim to be on a GPU: nothing of them is read)."""
+    import torch
+
+    for name, args in (("lbq_mx_linear_workspace", ((256, 128), 2 ** 32)), ("lbq_moe_sort_workspace", (2 ** 32, 8, 2)),
+                       ("lbq_moe_sort_workspace", (16, 2 ** 32 + 8, 2)), ("lbq_moe_sort_workspace", (16, 8, 2 ** 32 + 2)),
+                       ("lbq_mx_matmul_workspace", ((2 ** 32 + 4, 128), (4, 128))),
+                       ("lbq_mx_grouped_workspace", ((256, 128), 2, 4, 2 ** 32 + 4))):
+        with pytest.raises(L.LbqError) as e:
+            L._query(name, args)
+        assert e.value.status == SHAPE
+
+    launched = []
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: launched.append(name) or 0
+    monkeypatch.setattr(L, "_ready", lambda: Lib())
+    monkeypatch.setattr(L, "_on", lambda gpu, stream, go: go(0))
+    monkeypatch.setattr(L, "_need", lambda *a: None)
+    monkeypatch.setattr(L, "_torch", torch)
+    monkeypatch.setattr(L, "_dtypes", {torch.float16: 0})
+    big, one = 2 ** 32 + 2, 2
+
+    def half(*shape):
+        return torch.empty(shape, dtype=torch.float16, device="meta")
+
+    def ints(*shape):
+        return torch.empty(shape, dtype=torch.int32, device="meta")
+
+    def floats(*shape):
+        return torch.empty(shape, dtype=torch.float32, device="meta")
+    # (sizes that fit go through: the stand-ins reach the call)
+    assert L.moe_combine(half(one, one), ints(one, one), floats(one, one)).shape == (one, one)
+    assert launched == ["lbq_moe_combine"]
+    for call in (lambda: L.mx_quantize(half(big, 128)), lambda: L.mx_quantize(half(big, 1), transpose=True),
+                 lambda: L.mx_quantize(half(1, big), transpose=True),
+                 lambda: L.moe_gather(half(big, 1), ints(big, 1)),
+                 lambda: L.moe_gather(half(one, big), ints(one, 1)),
+                 lambda: L.moe_gather(half(one, 1), ints(one, 1), out=half(big, 1)),
+                 lambda: L.moe_gather_backward(half(big, 1), ints(one, 1)),
+                 lambda: L.moe_gather_backward(half(one, 1), ints(big, 1)),
+                 lambda: L.moe_combine(half(big, 1), ints(one, 1), floats(one, 1)),
+                 lambda: L.moe_combine(half(one, 1), ints(big, 1), floats(big, 1)),
+                 lambda: L.moe_combine_backward(half(one, 1), half(big, 1), ints(one, 1), floats(one, 1)),
+                 lambda: L.MxTensor(torch.empty((big, 64), dtype=torch.uint8, device="meta"),
+                                    torch.empty((1, big, 4), dtype=torch.uint8, device="meta"))):
+        with pytest.raises(L.LbqError) as e:
+            call()
+        assert e.value.status == SHAPE and launched == ["lbq_moe_combine"]
+    w = L.MxTensor.__new__(L.MxTensor)
+    w.rows, w.cols, w.gpu = 256, 128, 0
+    with pytest.raises(L.LbqError) as e:
+        L.mx_grouped_forward(w, 2, half(4, 128), ints(3), ints(8), top_k=2 ** 32 + 2)
+    assert e.value.status == SHAPE
+
+
 def test_reference_quantizer():
     """The tests' quantizer on hand-made blocks: ties to even codes, saturation, the scale of zeros."""
     x = np.zeros((1, 128))
