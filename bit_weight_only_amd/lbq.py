@@ -538,9 +538,11 @@ def _workspace(ws, need: int, like, gpu: int, where: str):
 
 
 class MxTensor:
-    """An MXFP4 tensor (see include/lbq.h): codes uint8 [rows][cols/2] and scales uint8 [cols/128][rows][4]."""
+    """An MXFP4 tensor (see include/lbq.h): codes uint8 [rows][cols/2] and scales uint8 [cols/128][rows][4].
 
-    __slots__ = ("rows", "cols", "codes", "scales", "gpu", "struct", "ref")
+    It keeps both tensors and their addresses: what they hold may change, the tensors may not be replaced."""
+
+    __slots__ = ("rows", "cols", "_codes", "_scales", "gpu", "struct", "ref")
 
     def __init__(self, codes, scales):
         _ready()
@@ -555,14 +557,22 @@ class MxTensor:
         self._set(codes, scales, rows, 2 * half, gpu)
 
     def _set(self, codes, scales, rows, cols, gpu):
-        self.rows, self.cols, self.codes, self.scales, self.gpu = rows, cols, codes, scales, gpu
+        self.rows, self.cols, self._codes, self._scales, self.gpu = rows, cols, codes, scales, gpu
         self.struct = Mx(rows, cols, codes.data_ptr(), scales.data_ptr())
         self.ref = ctypes.byref(self.struct)
         return self
 
     @property
+    def codes(self):
+        return self._codes
+
+    @property
+    def scales(self):
+        return self._scales
+
+    @property
     def device(self):
-        return self.codes.device
+        return self._codes.device
 
 
 def mx_quantize(x, transpose: bool = False, stream=None) -> MxTensor:
@@ -594,7 +604,7 @@ def mx_dequantize(t: MxTensor, dtype, out=None, stream=None):
         _need("mx_dequantize", t.gpu, dtype, (t.rows, t.cols), out)
 
     def go(s):
-        y = t.codes.new_empty((t.rows, t.cols), dtype=dtype) if out is None else out
+        y = t._codes.new_empty((t.rows, t.cols), dtype=dtype) if out is None else out
         st = L.lbq_mx_dequantize(t.ref, y.data_ptr(), dt, s)
         if st:
             raise LbqError(st, "lbq_mx_dequantize")
@@ -615,8 +625,8 @@ def mx_matmul(a: MxTensor, b: MxTensor, dtype=None, y=None, ws=None, stream=None
     need = _query("lbq_mx_matmul_workspace", ((a.rows, a.cols), (b.rows, b.cols)))
 
     def go(s):
-        out = a.codes.new_empty((a.rows, b.rows), dtype=dtype) if y is None else y
-        p, size, keep = _workspace(ws, need, a.codes, a.gpu, "mx_matmul")
+        out = a._codes.new_empty((a.rows, b.rows), dtype=dtype) if y is None else y
+        p, size, keep = _workspace(ws, need, a._codes, a.gpu, "mx_matmul")
         st = L.lbq_mx_matmul(a.ref, b.ref, out.data_ptr(), dt, p, size, s)
         if st:
             raise LbqError(st, "lbq_mx_matmul")

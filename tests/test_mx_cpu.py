@@ -194,6 +194,20 @@ def test_sizes_past_32_bits(L, monkeypatch):
     assert e.value.status == SHAPE
 
 
+def test_tensors_of_a_view_stay(L):
+    """An MxTensor holds the addresses of its tensors, so another tensor cannot be put in their place (the calls
+    would go on reading the old one's memory, which nothing keeps any more)."""
+    import torch
+
+    codes, scales = torch.zeros((4, 64), dtype=torch.uint8), torch.zeros((1, 4, 4), dtype=torch.uint8)
+    t = L.MxTensor.__new__(L.MxTensor)._set(codes, scales, 4, 128, 0)
+    assert t.codes is codes and t.scales is scales and t.device == codes.device
+    for name in ("codes", "scales"):
+        with pytest.raises(AttributeError):
+            setattr(t, name, torch.ones_like(getattr(t, name)))
+    assert t.codes is codes and t.scales is scales
+
+
 def test_reference_quantizer():
     """The tests' quantizer on hand-made blocks: ties to even codes, saturation, the scale of zeros."""
     x = np.zeros((1, 128))
