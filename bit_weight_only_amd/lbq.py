@@ -448,9 +448,11 @@ def moe_from_host(packed: dict, bits, signs_hidden, signs_ffn, hidden: int, ffn:
 # one GPU, contiguous, the right type and shape (LbqError otherwise, nothing
 # launched). They run on the tensors' GPU whatever the current one is, on the
 # given stream or that GPU's current one; what they allocate belongs to that
-# stream. A call's own cost counts at one token (its kernels take 5 us), so the
-# usual path keeps to a few attribute reads, one or two allocations and one
-# foreign call.
+# stream. On a given stream the caller orders the work before and after, but may
+# let go of the tensors as soon as the call returns: their memory is not given
+# out again before the stream is through with them. A call's own cost counts at
+# one token (its kernels take 5 us), so the usual path keeps to a few attribute
+# reads, one or two allocations and one foreign call.
 
 F16, BF16, F32 = 0, 1, 2
 _MOST = 2 ** 31 - 1   # a size of the C ABI; ctypes would cut a larger one off without a word
@@ -496,8 +498,8 @@ def _rows(where: str, t) -> int:
     return gpu
 
 
-def _on(gpu: int, stream, go):
-    """go(raw stream) with that GPU current and its allocations on that stream."""
+def _on(gpu: int, stream, go, *used):
+    """go(raw stream) with that GPU current and its allocations on that stream; used: the caller's tensors."""
     cuda = _torch._C
     if stream is None:
         if cuda._cuda_getDevice() == gpu:
@@ -507,7 +509,12 @@ def _on(gpu: int, stream, go):
     if stream.device.index != gpu:
         raise LbqError(-8, f"stream on {stream.device}, tensors on GPU {gpu}")
     with _torch.cuda.stream(stream):
-        return go(stream.cuda_stream)
+        try:
+            return go(stream.cuda_stream)
+        finally:
+            for t in used:
+                if t is not None:
+                    t.record_stream(stream)
 
 
 @functools.lru_cache(maxsize=4096)
@@ -593,7 +600,7 @@ def mx_quantize(x, transpose: bool = False, stream=None) -> MxTensor:
         if st:
             raise LbqError(st, "lbq_mx_quantize_t" if transpose else "lbq_mx_quantize")
         return MxTensor.__new__(MxTensor)._set(codes, scales, tr, tc, gpu)
-    return _on(gpu, stream, go)
+    return _on(gpu, stream, go, x)
 
 
 def mx_dequantize(t: MxTensor, dtype, out=None, stream=None):
@@ -609,7 +616,7 @@ def mx_dequantize(t: MxTensor, dtype, out=None, stream=None):
         if st:
             raise LbqError(st, "lbq_mx_dequantize")
         return y
-    return _on(t.gpu, stream, go)
+    return _on(t.gpu, stream, go, t._codes, t._scales, out)
 
 
 def mx_matmul(a: MxTensor, b: MxTensor, dtype=None, y=None, ws=None, stream=None):
@@ -631,7 +638,7 @@ def mx_matmul(a: MxTensor, b: MxTensor, dtype=None, y=None, ws=None, stream=None
         if st:
             raise LbqError(st, "lbq_mx_matmul")
         return out
-    return _on(a.gpu, stream, go)
+    return _on(a.gpu, stream, go, a._codes, a._scales, b._codes, b._scales, y, ws)
 
 
 def mx_linear_forward(w: MxTensor, x, y=None, ws=None, stream=None):
@@ -654,7 +661,7 @@ def mx_linear_forward(w: MxTensor, x, y=None, ws=None, stream=None):
         if st:
             raise LbqError(st, "lbq_mx_linear_forward")
         return out
-    return _on(w.gpu, stream, go)
+    return _on(w.gpu, stream, go, w._codes, w._scales, x, y, ws)
 
 
 def mx_grouped_forward(w: MxTensor, E: int, x, offsets, perm=None, top_k: int = 1, y=None, ws=None, stream=None):
@@ -687,7 +694,7 @@ def mx_grouped_forward(w: MxTensor, E: int, x, offsets, perm=None, top_k: int = 
         if st:
             raise LbqError(st, "lbq_mx_grouped_forward")
         return out
-    return _on(gpu, stream, go)
+    return _on(gpu, stream, go, w._codes, w._scales, x, offsets, perm, y, ws)
 
 
 def moe_sort(ids, E: int, stream=None):
@@ -709,7 +716,7 @@ def moe_sort(ids, E: int, stream=None):
         if st:
             raise LbqError(st, "lbq_moe_sort")
         return counts, offsets, perm, pos
-    return _on(gpu, stream, go)
+    return _on(gpu, stream, go, ids)
 
 
 def _places(where: str, gpu: int, pos):
@@ -739,7 +746,7 @@ def moe_gather(x, pos, out=None, stream=None):
         if st:
             raise LbqError(st, "lbq_moe_gather")
         return o
-    return _on(gpu, stream, go)
+    return _on(gpu, stream, go, x, pos, out)
 
 
 def moe_gather_backward(d_out, pos, dx=None, stream=None):
@@ -758,7 +765,7 @@ def moe_gather_backward(d_out, pos, dx=None, stream=None):
         if st:
             raise LbqError(st, "lbq_moe_gather_backward")
         return o
-    return _on(gpu, stream, go)
+    return _on(gpu, stream, go, d_out, pos, dx)
 
 
 def moe_combine(o, pos, weights, y=None, stream=None):
@@ -778,7 +785,7 @@ def moe_combine(o, pos, weights, y=None, stream=None):
         if st:
             raise LbqError(st, "lbq_moe_combine")
         return out
-    return _on(gpu, stream, go)
+    return _on(gpu, stream, go, o, pos, weights, y)
 
 
 def moe_combine_backward(dy, o, pos, weights, d_o=None, d_weights=None, stream=None):
@@ -806,4 +813,4 @@ def moe_combine_backward(dy, o, pos, weights, d_o=None, d_weights=None, stream=N
         if st:
             raise LbqError(st, "lbq_moe_combine_backward")
         return go_, gw
-    return _on(gpu, stream, go)
+    return _on(gpu, stream, go, dy, o, pos, weights, d_o, d_weights)

@@ -341,6 +341,79 @@ def test_on_another_stream(L, dev):
             assert torch.equal(y, want[i])
 
 
+def _stream_calls(L):
+    """name -> (makes the tensors, the call on them); every tensor 2 MB or more, so a block of its own."""
+    import torch
+
+    def codes(r, c):
+        return [torch.randint(0, 256, (r, c // 2), dtype=torch.uint8, device="cuda"),
+                torch.randint(118, 126, (c // 128, r, 4), dtype=torch.uint8, device="cuda")]
+
+    def rows(r, c, dtype=torch.float16):
+        return torch.randn(r, c, device="cuda").to(dtype)
+    m, k, n, E = 1 << 17, 4, 8192, 8        # tokens, picks, rows of the products, experts
+    H = 64
+
+    def ids():
+        return torch.randint(0, E, (m, k), dtype=torch.int32, device="cuda")
+
+    def pos():
+        return torch.randperm(m * k, device="cuda").to(torch.int32).reshape(m, k)
+
+    def grouped():
+        off = torch.arange(E + 1, device="cuda", dtype=torch.int32) * (m * k // E)
+        return codes(E * 1024, 8192) + [rows(n, 8192), off, torch.arange(m * k, device="cuda", dtype=torch.int32) % n]
+    return {
+        "quantize": (lambda: [rows(n, 4096)], lambda x, s: L.mx_quantize(x, stream=s)),
+        "quantize_t": (lambda: [rows(n, 4096)], lambda x, s: L.mx_quantize(x, transpose=True, stream=s)),
+        "dequantize": (lambda: codes(n, 8192),
+                       lambda c, e, s: L.mx_dequantize(L.MxTensor(c, e), torch.float16, stream=s)),
+        "matmul": (lambda: codes(n, 8192) + codes(n, 8192),
+                   lambda a, b, c, d, s: L.mx_matmul(L.MxTensor(a, b), L.MxTensor(c, d), torch.bfloat16, stream=s)),
+        "linear": (lambda: codes(n, 8192) + [rows(256, 8192)],
+                   lambda c, e, x, s: L.mx_linear_forward(L.MxTensor(c, e), x, stream=s)),
+        "grouped": (grouped, lambda c, e, x, o, p, s: L.mx_grouped_forward(L.MxTensor(c, e), E, x, o, p, 1, stream=s)),
+        "sort": (lambda: [ids()], lambda i, s: L.moe_sort(i, E, stream=s)),
+        "gather": (lambda: [rows(m, H), pos()], lambda x, p, s: L.moe_gather(x, p, stream=s)),
+        "gather_backward": (lambda: [rows(m * k, H), pos()], lambda d, p, s: L.moe_gather_backward(d, p, stream=s)),
+        "combine": (lambda: [rows(m * k, H), pos(), torch.rand(m, k, device="cuda")],
+                    lambda o, p, w, s: L.moe_combine(o, p, w, stream=s)),
+        "combine_backward": (lambda: [rows(m, H), rows(m * k, H), pos(), torch.rand(m, k, device="cuda")],
+                             lambda d, o, p, w, s: L.moe_combine_backward(d, o, p, w, stream=s)),
+    }
+
+
+STREAM_CALLS = ["quantize", "quantize_t", "dequantize", "matmul", "linear", "grouped", "sort", "gather",
+                "gather_backward", "combine", "combine_backward"]
+
+
+@pytest.mark.parametrize("name", STREAM_CALLS)
+def test_tensors_let_go_while_another_stream_reads_them(L, dev, name):
+    """The caller drops a call's tensors while the stream has not come to it yet: their memory is not given out
+    again until it has (tensors of the same sizes, made meanwhile, lie elsewhere)."""
+    import torch
+
+    say(f"mx let go {name}")
+    make, call = _stream_calls(L)[name]
+    busy = torch.randn(8192, 8192, device="cuda")
+    s = torch.cuda.Stream()
+    tensors = make()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(24):
+            busy @ busy                              # some 170 ms of work before the call's
+    out = call(*tensors, s)
+    at = {t.data_ptr() for t in tensors if t.numel() * t.element_size() >= 2 << 20}
+    sizes = [(t.shape, t.dtype) for t in tensors]
+    assert at
+    del tensors
+    new = [torch.zeros(shape, dtype=dtype, device="cuda") for shape, dtype in sizes * 2]
+    assert not s.query()
+    assert not at & {t.data_ptr() for t in new}
+    torch.cuda.synchronize()
+    del out, new, busy
+
+
 # ------------------------------------------------------------------ the operators together
 
 def test_training_step_of_one_linear(L, dev):

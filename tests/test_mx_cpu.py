@@ -155,7 +155,7 @@ def test_sizes_past_32_bits(L, monkeypatch):
         def __getattr__(self, name):
             return lambda *a: launched.append(name) or 0
     monkeypatch.setattr(L, "_ready", lambda: Lib())
-    monkeypatch.setattr(L, "_on", lambda gpu, stream, go: go(0))
+    monkeypatch.setattr(L, "_on", lambda gpu, stream, go, *used: go(0))
     monkeypatch.setattr(L, "_need", lambda *a: None)
     monkeypatch.setattr(L, "_torch", torch)
     monkeypatch.setattr(L, "_dtypes", {torch.float16: 0})
