@@ -71,14 +71,25 @@ int stream_rows(const MxGemm &g) {
 }
 
 // The streaming kernel quantizes the activations itself where every workgroup
-// doing so costs about as much as a launch, or less. Per call, itself against
-// with a launch before it, in a graph (one by one): 8 tokens 4096 -> 4096 6.3
-// against 7.1 us; 16 tokens 4096 -> 4096 7.8 against 7.3 (8.0 against 10.8); 32
-// tokens 2048 -> 4096 7.1 against 6.7 (7.0 against 10.7); 32 tokens 4096 -> 4096
-// 11.6 against 8.7. Grouped: always (few rows per expert).
+// doing so costs about as much as a launch, or less; that work is a workgroup's
+// tokens times K, for an expert's rows their average. Itself against with a launch
+// before it, us a call in a graph (one by one):
+//   8 x 4096 -> 4096     6.2 (6.5)     7.0 (9.2)     2^15
+//   16 x 4096 -> 4096    7.9 (8.1)     7.3 (9.2)     2^16
+//   4 x 14336 -> 4096    14.3 (14.1)   14.8 (14.4)   0.9 2^16
+//   8 x 8192 -> 4096     10.8 (10.7)   10.1 (10.1)   2^16; -> 8192 13.6, 13.7
+//   8 x 14336 -> 4096    16.9 (16.7)   16.2 (15.8)   1.8 2^16
+//   8 x 17408 -> 4096    17.7 (17.7)   16.3 (16.3)   2.1 2^16
+//   16 x 8192 -> 4096    14.2 (13.9)   10.9 (10.7)   2^17
+//   256 experts of 2048 x 2048, 8 rows each   141.3   144.7   2^14
+//   16 of 4096 x 4096, 2.5 rows               34.0    35.3    0.6 2^14
+//   16 of 4096 x 4096, 10 rows                39.6    39.0    1.3 2^15
+//   16 of 4096 x 8192, 8 rows                 63.8    60.6    2^16
+//   8 of 4096 x 14336, 4 rows                 83.6    77.6    0.9 2^16
 bool stream_quantizes(const MxGemm &g) {
   if (stream_rows(g) == 0) return false;
-  return g.E > 0 || g.M <= 8 || (g.M <= 32 && static_cast<long>(g.M) * g.K <= 1 << 16);
+  const long work = static_cast<long>(g.M) * g.K;
+  return g.E > 0 ? work < static_cast<long>(g.E) << 15 : g.M <= 32 && work <= 1 << 16;
 }
 
 size_t scratch_bytes(const MxGemm &g) { return stream_rows(g) > 0 ? 0 : mx_gemm_scratch_bytes(g); }

@@ -136,6 +136,24 @@ def test_binding_refusals(L):
         assert e.value.status in (SHAPE, FORMAT)
 
 
+def test_who_quantizes(L):
+    """The workspace tells which product takes x as it is: few tokens on rows that are not too long. A batch whose
+    quantizing every workgroup would repeat at more than a launch's cost has its codes in the workspace."""
+    def linear(M, K, N=4096):
+        return L._query("lbq_mx_linear_workspace", ((N, K), M))
+
+    def grouped(M, K, E, k, N=256):
+        return L._query("lbq_mx_grouped_workspace", ((E * N, K), E, M, M * k))
+    for M, K in ((1, 17408), (3, 14336), (4, 14336), (8, 4096), (8, 8192), (16, 4096), (32, 2048)):
+        assert linear(M, K) == 0
+    for M, K in ((8, 14336), (8, 17408), (5, 17408), (16, 8192), (33, 1024), (32, 4096)):
+        assert linear(M, K) >= M * K * 17 // 32
+    for M, K, E, k in ((32, 2048, 256, 8), (256, 2048, 256, 8), (20, 4096, 16, 2), (1, 14336, 8, 2)):
+        assert grouped(M, K, E, k) == 0
+    for M, K, E, k in ((40, 4096, 16, 4), (32, 8192, 16, 4), (8, 14336, 8, 4)):
+        assert grouped(M, K, E, k) >= M * K * 17 // 32
+
+
 def test_sizes_past_32_bits(L, monkeypatch):
     """A size that a C int does not hold is refused, not cut off: 2^32 + n would arrive as n (meta tensors that
     claim to be on a GPU: nothing of them is read)."""
