@@ -380,15 +380,18 @@ hipError_t launch_tiles(GemmArgs g, int dtype, int slices, hipStream_t s) {
   g.tiles_m = static_cast<int>(tm);
   g.tiles_n = static_cast<int>(tn);
   const dim3 grid(static_cast<unsigned>(tm * tn), static_cast<unsigned>(slices)), block(Tl::kThreads);
-#define LBQ_MX_GO(DT)                                                                                       \
-  if (g.E > 0) hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, DT, true>), grid, block, 0, s, g);        \
-  else hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, DT, false>), grid, block, 0, s, g)
-  if (dtype == kF16) {
-    LBQ_MX_GO(kF16);
+#define LBQ_MX_GO(DT, GROUPED) \
+  hipLaunchKernelGGL((mx_tile_kernel<MB, NB, GM, GN, DT, GROUPED>), grid, block, 0, s, g)
+  if (g.E > 0) {   // in 16 bits
+    if (dtype == kF16) LBQ_MX_GO(kF16, true);
+    else if (dtype == kBF16) LBQ_MX_GO(kBF16, true);
+    else return hipErrorInvalidValue;
+  } else if (dtype == kF16) {
+    LBQ_MX_GO(kF16, false);
   } else if (dtype == kBF16) {
-    LBQ_MX_GO(kBF16);
+    LBQ_MX_GO(kBF16, false);
   } else {
-    LBQ_MX_GO(kF32);
+    LBQ_MX_GO(kF32, false);
   }
 #undef LBQ_MX_GO
   return hipGetLastError();

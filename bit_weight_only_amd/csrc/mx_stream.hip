@@ -242,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) mx_stream_kernel(MxGemm g, int T16, 
 // unit 107).
 template <int MT, int GPW>
 hipError_t launch(const MxGemm &g, int tiles, hipStream_t s) {
-  constexpr int kMany = GPW * MT >= 8 ? 1 : GPW * MT >= 4 ? 2 : 4;
+  constexpr int kMany = MT > 1 || GPW >= 8 ? 1 : GPW >= 4 ? 2 : 4;   // grouped calls come with MT = 1
   const int T16 = (g.N + 15) / 16;
   if (g.E > 0 && T16 >= 4 * kMany) {
     const int walkers = std::min((T16 + kMany - 1) / kMany, std::max(1, 1024 / tiles));
