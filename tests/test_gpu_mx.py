@@ -414,6 +414,37 @@ def test_tensors_let_go_while_another_stream_reads_them(L, dev, name):
     del out, new, busy
 
 
+def test_captured_with_the_stream_given(L, dev):
+    """A capture whose calls name its stream, with tensors dropped inside it and after it."""
+    import torch
+
+    w, _ = _tensor(L, 600, 4096, item=13)
+    x = _x(90, 4096, "bfloat16", item=650)[0]
+    first = x.clone()
+    ids = torch.from_numpy(_routing(90, 5, 2, 13)).cuda()
+
+    def work(x, stream):
+        t = x * 2
+        y = L.mx_linear_forward(w, t, stream=stream)
+        del t
+        pos = L.moe_sort(ids, 5, stream=stream)[3]
+        xs = L.moe_gather(x, pos, stream=stream)
+        return [y, L.moe_combine(xs, pos, torch.ones(90, 2, device="cuda"), stream=stream)]
+    work(x, None)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = work(x, torch.cuda.current_stream())
+    for step in range(3):
+        x.copy_(first * (step + 1))
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(out, work(x, None)):
+            assert torch.equal(a, b), step
+    del w, x, ids
+    assert torch.isfinite(torch.zeros(1 << 20, device="cuda")).all()
+
+
 # ------------------------------------------------------------------ the operators together
 
 def test_training_step_of_one_linear(L, dev):
