@@ -489,13 +489,16 @@ def _need(where: str, gpu: int, dtype, shape, t):
         raise LbqError(-2, f"{where}: shape {tuple(t.shape)}, strides {t.stride()}")
 
 
-def _rows(where: str, t) -> int:
-    """The GPU of t, a contiguous matrix in a value type."""
-    if t.dim() != 2 or t.shape[0] > _MOST or t.shape[1] > _MOST:
-        raise LbqError(-2, f"{where}: a matrix of 32-bit sizes is needed, got {tuple(t.shape)}")
+def _rows(where: str, t):
+    """(GPU, rows, columns) of t, a contiguous matrix in a value type."""
+    if t.dim() != 2:
+        raise LbqError(-2, f"{where}: a matrix is needed, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    if rows > _MOST or cols > _MOST:
+        raise LbqError(-2, f"{where}: {rows} x {cols}")
     gpu = t.get_device()
     _need(where, gpu, t.dtype, None, t)
-    return gpu
+    return gpu, rows, cols
 
 
 def _on(gpu: int, stream, go, *used):
@@ -585,9 +588,8 @@ class MxTensor:
 def mx_quantize(x, transpose: bool = False, stream=None) -> MxTensor:
     """lbq_mx_quantize (transpose: lbq_mx_quantize_t) of x [rows][cols] in float16, bfloat16 or float32."""
     L = _ready()
-    gpu = _rows("mx_quantize", x)
+    gpu, rows, cols = _rows("mx_quantize", x)
     dt = _dtype(x.dtype, "mx_quantize")
-    rows, cols = x.shape
     tr, tc = (cols, -(-rows // 128) * 128) if transpose else (rows, cols)
     if tc % 128 or tc == 0:
         raise LbqError(-2, "mx_quantize: blocks run along a multiple of 128 values")
@@ -721,28 +723,33 @@ def moe_sort(ids, E: int, stream=None):
 
 def _places(where: str, gpu: int, pos):
     _need(where, gpu, _torch.int32, None, pos)
-    if pos.dim() != 2 or pos.shape[0] > _MOST or pos.shape[1] > _MOST:
-        raise LbqError(-2, f"{where}: pos is [M][top_k], got {tuple(pos.shape)}")
-    return pos.shape
+    if pos.dim() != 2:
+        raise LbqError(-2, f"{where}: pos is [M][top_k]")
+    M, k = pos.shape
+    if M > _MOST or k > _MOST:
+        raise LbqError(-2, f"{where}: {M} x {k} places")
+    return M, k
 
 
 def moe_gather(x, pos, out=None, stream=None):
     """lbq_moe_gather: out[pos[t][j]] = x[t]. out [T][H] is [M * top_k][H] if not given; rows that no place
     names are left as they were (uninitialised if out is not given)."""
     L = _ready()
-    gpu = _rows("moe_gather", x)
+    gpu, rows, H = _rows("moe_gather", x)
     dt = _dtype(x.dtype, "moe_gather")
     M, k = _places("moe_gather", gpu, pos)
-    H = x.shape[1]
-    if x.shape[0] != M:
-        raise LbqError(-2, f"moe_gather: {x.shape[0]} rows, places of {M}")
+    if rows != M:
+        raise LbqError(-2, f"moe_gather: {rows} rows, places of {M}")
+    T = M * k
     if out is not None:
-        _rows("moe_gather", out)
-        _need("moe_gather", gpu, x.dtype, (out.shape[0], H), out)
+        T = out.shape[0] if out.dim() == 2 else -1
+        if not 0 <= T <= _MOST:
+            raise LbqError(-2, f"moe_gather: out is [T][H], got {tuple(out.shape)}")
+        _need("moe_gather", gpu, x.dtype, (T, H), out)
 
     def go(s):
-        o = x.new_empty((M * k, H)) if out is None else out
-        st = L.lbq_moe_gather(x.data_ptr(), dt, M, H, pos.data_ptr(), k, o.shape[0], o.data_ptr(), s)
+        o = x.new_empty((T, H)) if out is None else out
+        st = L.lbq_moe_gather(x.data_ptr(), dt, M, H, pos.data_ptr(), k, T, o.data_ptr(), s)
         if st:
             raise LbqError(st, "lbq_moe_gather")
         return o
@@ -752,10 +759,9 @@ def moe_gather(x, pos, out=None, stream=None):
 def moe_gather_backward(d_out, pos, dx=None, stream=None):
     """lbq_moe_gather_backward: dx[t] = sum_j d_out[pos[t][j]]."""
     L = _ready()
-    gpu = _rows("moe_gather_backward", d_out)
+    gpu, T, H = _rows("moe_gather_backward", d_out)
     dt = _dtype(d_out.dtype, "moe_gather_backward")
     M, k = _places("moe_gather_backward", gpu, pos)
-    T, H = d_out.shape
     if dx is not None:
         _need("moe_gather_backward", gpu, d_out.dtype, (M, H), dx)
 
@@ -771,11 +777,10 @@ def moe_gather_backward(d_out, pos, dx=None, stream=None):
 def moe_combine(o, pos, weights, y=None, stream=None):
     """lbq_moe_combine: y[t] = sum_j weights[t][j] o[pos[t][j]] (weights float32 [M][top_k])."""
     L = _ready()
-    gpu = _rows("moe_combine", o)
+    gpu, T, H = _rows("moe_combine", o)
     dt = _dtype(o.dtype, "moe_combine")
     M, k = _places("moe_combine", gpu, pos)
     _need("moe_combine", gpu, _torch.float32, (M, k), weights)
-    T, H = o.shape
     if y is not None:
         _need("moe_combine", gpu, o.dtype, (M, H), y)
 
@@ -793,11 +798,10 @@ def moe_combine_backward(dy, o, pos, weights, d_o=None, d_weights=None, stream=N
     left as they were (uninitialised if d_o is not given)."""
     L = _ready()
     where = "moe_combine_backward"
-    gpu = _rows(where, o)
+    gpu, T, H = _rows(where, o)
     dt = _dtype(o.dtype, where)
     M, k = _places(where, gpu, pos)
     _need(where, gpu, _torch.float32, (M, k), weights)
-    T, H = o.shape
     _need(where, gpu, o.dtype, (M, H), dy)
     if d_o is not None:
         _need(where, gpu, o.dtype, (T, H), d_o)
