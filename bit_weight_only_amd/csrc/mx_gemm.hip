@@ -344,6 +344,8 @@ __global__ void __launch_bounds__(64 * GM *GN, 1) mx_tile_kernel(GemmArgs g) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       }
   } else {
+    // rows of y that start anywhere: value by value from the registers (2048 tokens
+    // 4096 -> 4100 or 4097 in bf16 56 us; 4104, through LDS, 36; 4096 26)
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
       const int token = wm + 32 * i + r;
@@ -404,7 +406,13 @@ hipError_t launch_tiles(GemmArgs g, int dtype, int slices, hipStream_t s) {
 // 512 x 4096 12.7, 16.0, 34.1; 2048 x 4096 34, 28, 36; 400 x 28672 47, 44, 40;
 // 4096 x 4096 59, 48, 43. Grouped, every expert's last tile is taken to be half
 // full: 256 experts of 2048 x 2048, 64 rows each, 175, 191, 235; 8 of 4096 x 4096,
-// 512 rows, 81, 73, 88; 8 of 28672 x 4096, 2048 rows, 2085, 1681, 1355. Dense with
+// 512 rows, 81, 73, 88; 8 of 28672 x 4096, 2048 rows, 2085, 1681, 1355. The starts
+// in these costs do not grow with K, so other K shift the borders a little. Dense,
+// K of 512, 1024, 2048, 8192 and 14336 at 512, 2048 and 4096 x 4096, 400 x 28672
+// and 1000 x 8192: the tile taken is within 5 % of the best of the three. Grouped
+// rows of long K would do better with larger tiles than the rule takes: 256 experts
+// at 64 rows, K = 7168, 538 (64 x 128), 486, 565; 16 of 4096 at 128 rows, K =
+// 14336, 196 (64 x 128), 192, 150; K = 2048 34.7, 36.3, 34.2. Dense with
 // fewer tiles of the smallest kind than half the compute units: K in slices of
 // at least 1024.
 struct Plan {

@@ -452,7 +452,8 @@ def moe_from_host(packed: dict, bits, signs_hidden, signs_ffn, hidden: int, ffn:
 # let go of the tensors as soon as the call returns: their memory is not given
 # out again before the stream is through with them. A call's own cost counts at
 # one token (its kernels take 5 us), so the usual path keeps to a few attribute
-# reads, one or two allocations and one foreign call.
+# reads, one or two allocations and one foreign call. Results carry no
+# gradient, whatever the inputs require: the gradients are calls of their own.
 
 F16, BF16, F32 = 0, 1, 2
 _MOST = 2 ** 31 - 1   # a size of the C ABI; ctypes would cut a larger one off without a word
@@ -586,7 +587,8 @@ class MxTensor:
 
 
 def mx_quantize(x, transpose: bool = False, stream=None) -> MxTensor:
-    """lbq_mx_quantize (transpose: lbq_mx_quantize_t) of x [rows][cols] in float16, bfloat16 or float32."""
+    """lbq_mx_quantize (transpose: lbq_mx_quantize_t, of one row at least) of x [rows][cols] in float16, bfloat16 or
+    float32."""
     L = _ready()
     gpu, rows, cols = _rows("mx_quantize", x)
     dt = _dtype(x.dtype, "mx_quantize")
@@ -622,7 +624,8 @@ def mx_dequantize(t: MxTensor, dtype, out=None, stream=None):
 
 
 def mx_matmul(a: MxTensor, b: MxTensor, dtype=None, y=None, ws=None, stream=None):
-    """lbq_mx_matmul: y [a.rows][b.rows] = A B^T in dtype (float32 if neither it nor y is given)."""
+    """lbq_mx_matmul: y [a.rows][b.rows] = A B^T in dtype (float32 if neither it nor y is given). Autograd does not
+    see it: a layer's gradients are two more of these products."""
     L = _ready()
     if a.gpu != b.gpu:
         raise LbqError(-8, f"mx_matmul: tensors on {a.device} and {b.device}")
@@ -644,7 +647,8 @@ def mx_matmul(a: MxTensor, b: MxTensor, dtype=None, y=None, ws=None, stream=None
 
 
 def mx_linear_forward(w: MxTensor, x, y=None, ws=None, stream=None):
-    """lbq_mx_linear_forward: y [M][w.rows] = Q(x) W^T, x [M][w.cols] in float16 or bfloat16, y in x's type."""
+    """lbq_mx_linear_forward: y [M][w.rows] = Q(x) W^T, x [M][w.cols] in float16 or bfloat16, y in x's type; x is
+    rounded to MXFP4 too. Autograd does not see it."""
     L = _ready()
     dtype = x.dtype
     dt = _dtype(dtype, "mx_linear_forward")
@@ -668,7 +672,8 @@ def mx_linear_forward(w: MxTensor, x, y=None, ws=None, stream=None):
 
 def mx_grouped_forward(w: MxTensor, E: int, x, offsets, perm=None, top_k: int = 1, y=None, ws=None, stream=None):
     """lbq_mx_grouped_forward: w holds E experts of w.rows / E rows; y [T][w.rows / E], T the length of perm
-    (of x without perm). Rows of y from offsets[E] on are left as they were (uninitialised if y is not given)."""
+    (of x without perm). Rows of y from offsets[E] on are left as they were (uninitialised if y is not given).
+    Autograd does not see it."""
     L = _ready()
     where, gpu, dtype = "mx_grouped_forward", w.gpu, x.dtype
     dt = _dtype(dtype, where)
@@ -733,7 +738,8 @@ def _places(where: str, gpu: int, pos):
 
 def moe_gather(x, pos, out=None, stream=None):
     """lbq_moe_gather: out[pos[t][j]] = x[t]. out [T][H] is [M * top_k][H] if not given; rows that no place
-    names are left as they were (uninitialised if out is not given)."""
+    names are left as they were (uninitialised if out is not given). Autograd does not see it; its gradient is
+    moe_gather_backward."""
     L = _ready()
     gpu, rows, H = _rows("moe_gather", x)
     dt = _dtype(x.dtype, "moe_gather")
@@ -775,7 +781,8 @@ def moe_gather_backward(d_out, pos, dx=None, stream=None):
 
 
 def moe_combine(o, pos, weights, y=None, stream=None):
-    """lbq_moe_combine: y[t] = sum_j weights[t][j] o[pos[t][j]] (weights float32 [M][top_k])."""
+    """lbq_moe_combine: y[t] = sum_j weights[t][j] o[pos[t][j]] (weights float32 [M][top_k]). Autograd does not see
+    it; its gradients are moe_combine_backward."""
     L = _ready()
     gpu, T, H = _rows("moe_combine", o)
     dt = _dtype(o.dtype, "moe_combine")

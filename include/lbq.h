@@ -445,12 +445,15 @@ lbq_status lbq_mx_quantize(const void *x, int32_t dtype, int32_t rows, int32_t c
  * tensor of cols rows and Rp = rows rounded up to a multiple of 128 columns,
  * the columns past rows zero. What a product needs whose sum runs over x's
  * rows (the weight's gradient sums over tokens, the input's over outputs).
- * rows is at most 128 * 65535, cols at most 2^30 - 64. */
+ * rows is at most 128 * 65535, cols at most 2^30 - 64. rows = 0 writes nothing:
+ * there is no MXFP4 tensor without columns, so no product takes one. */
 lbq_status lbq_mx_quantize_t(const void *x, int32_t dtype, int32_t rows, int32_t cols, void *codes, void *scales,
                              void *stream);
 
-/* The values of an MXFP4 tensor: x [rows][cols] (dtype), each rounded once
- * (exact in fp32 and bf16; in fp16 wherever the value is in its range). */
+/* The values of an MXFP4 tensor: x [rows][cols] (dtype), each rounded once:
+ * exact in fp32 and bf16, but for magnitudes of 2^128 and more (scale bytes 253
+ * and 254, which quantizing never gives), which become infinities; exact in
+ * fp16 from 2^-23 to below 2^16, rounded below, infinite above. */
 lbq_status lbq_mx_dequantize(const lbq_mx *t, void *x, int32_t dtype, void *stream);
 
 /* Workspace bytes of lbq_mx_matmul (host query). Errors as its argument checks. */
