@@ -680,7 +680,7 @@ def mx_grouped_forward(w: MxTensor, E: int, x, offsets, perm=None, top_k: int = 
     _need(where, gpu, dtype, None, x)
     if x.dim() != 2 or x.shape[1] != w.cols:
         raise LbqError(-2, "mx_grouped_forward: x is [M][w.cols]")
-    if E < 1 or w.rows % E or top_k > _MOST:
+    if E < 1 or w.rows % E or not 1 <= top_k <= _MOST:
         raise LbqError(-2, f"mx_grouped_forward: w holds E experts of equal rows; E {E}, top_k {top_k}")
     M, N = x.shape[0], w.rows // E
     _need(where, gpu, _torch.int32, (E + 1,), offsets)

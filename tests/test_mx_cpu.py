@@ -207,9 +207,10 @@ def test_sizes_past_32_bits(L, monkeypatch):
         assert e.value.status == SHAPE and launched == ["lbq_moe_combine"]
     w = L.MxTensor.__new__(L.MxTensor)
     w.rows, w.cols, w.gpu = 256, 128, 0
-    with pytest.raises(L.LbqError) as e:
-        L.mx_grouped_forward(w, 2, half(4, 128), ints(3), ints(8), top_k=2 ** 32 + 2)
-    assert e.value.status == SHAPE
+    for top_k in (2 ** 32 + 2, -2 ** 32 + 2):
+        with pytest.raises(L.LbqError) as e:
+            L.mx_grouped_forward(w, 2, half(4, 128), ints(3), ints(8), top_k=top_k)
+        assert e.value.status == SHAPE
 
 
 def test_tensors_of_a_view_stay(L):
