@@ -73,7 +73,7 @@ int stream_rows(const MxGemm &g) {
 // The streaming kernel quantizes the activations itself where every workgroup
 // doing so costs about as much as a launch, or less; that work is a workgroup's
 // tokens times K, for an expert's rows their average. Itself against with a launch
-// before it, us a call in a graph (one by one):
+// before it, us a call in a graph (one by one), and the work:
 //   8 x 4096 -> 4096     6.2 (6.5)     7.0 (9.2)     2^15
 //   16 x 4096 -> 4096    7.9 (8.1)     7.3 (9.2)     2^16
 //   4 x 14336 -> 4096    14.3 (14.1)   14.8 (14.4)   0.9 2^16
@@ -81,6 +81,9 @@ int stream_rows(const MxGemm &g) {
 //   8 x 14336 -> 4096    16.9 (16.7)   16.2 (15.8)   1.8 2^16
 //   8 x 17408 -> 4096    17.7 (17.7)   16.3 (16.3)   2.1 2^16
 //   16 x 8192 -> 4096    14.2 (13.9)   10.9 (10.7)   2^17
+//   32 x 2048 -> 4096    7.2 (7.1)     6.7 (9.4)     2^16
+//   33 x 1024 -> 4096    9.2 (8.8)     7.2 (9.4)     2^15
+//   64 x 512 -> 4096     10.5 (10.6)   7.2 (8.9)     2^15
 //   256 experts of 2048 x 2048, 8 rows each   141.3   144.7   2^14
 //   16 of 4096 x 4096, 2.5 rows               34.0    35.3    0.6 2^14
 //   16 of 4096 x 4096, 10 rows                39.6    39.0    1.3 2^15
