@@ -131,9 +131,10 @@ def prepare(case, seed):
     s["base"] = torch.randn(M, N, device="cuda", generator=g).to(dt)      # what the shared projection gave
     if case["runs"]:
         # requests of about equal length, in any order of their adapters
-        of = torch.randint(0, L, (M,), device="cuda", generator=g)
-        of[torch.rand(M, device="cuda", generator=g) < case["none"]] = -1
-        ids = of[torch.arange(M, device="cuda") * max(L, 4) // M]
+        n = max(L, 4)
+        of = torch.randint(0, L, (n,), device="cuda", generator=g)
+        of[torch.rand(n, device="cuda", generator=g) < case["none"]] = -1
+        ids = of[torch.arange(M, device="cuda") * n // M]
     else:
         ids = torch.randint(0, L, (M,), device="cuda", generator=g)
         ids[torch.rand(M, device="cuda", generator=g) < case["none"]] = -1
