@@ -293,15 +293,11 @@ def _exact_select(s):
             if s["group_picks"] == 2:
                 rest = part.scatter(2, part.argmax(2, keepdim=True), -math.inf).amax(2)
                 value = first + torch.where(torch.isinf(rest), 0.0, rest)
-            keep = value.topk(s["top_groups"], 1).values[:, -1:]
-            c = torch.where((value < keep)[..., None], -math.inf, part).reshape(M, -1)
-        picks, live = [], []
-        for _ in range(k):
-            best = c.max(1)
-            picks.append(best.indices)
-            live.append(~torch.isinf(best.values))
-            c = c.scatter(1, best.indices[:, None], -math.inf)
-        picks, live = torch.stack(picks, 1), torch.stack(live, 1)
+            order = value.argsort(1, descending=True, stable=True)
+            lost = torch.zeros_like(value, dtype=torch.bool).scatter(1, order[:, s["top_groups"]:], True)
+            c = torch.where(lost[..., None], -math.inf, part).reshape(M, -1)
+        picks = c.argsort(1, descending=True, stable=True)[:, :k]
+        live = ~torch.isinf(c.gather(1, picks))
     w = p.gather(1, picks) * live
     if s["renormalise"]:
         total = w.sum(1, keepdim=True)
