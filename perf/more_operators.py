@@ -78,11 +78,12 @@ def draw(rng):
             E, top_groups = groups * each, rng.randint(1, groups)
             picks = rng.randint(1, 2)
         else:
-            E, groups, top_groups, picks, each = _log(rng, 1, 1024), 1, 1, 1, 0
+            E, groups, top_groups, picks, each = _log(rng, 2, 1024), 1, 1, 1, 0
         top_k = rng.randint(1, min(16, top_groups * each if groups > 1 else E))
         M = _log(rng, 1, min(131072, (1 << 25) // E))
         return _select(M, E, top_k, rng.choice(["f32", "bf16", "f16"]), score, bias, groups, top_groups, picks,
-                       rng.random() < 0.6, rng.choice([1.0, 2.5]), rng.choice([0.0, 0.05]), train)
+                       top_k > 1 and rng.random() < 0.7, rng.choice([1.0, 2.5]),
+                       rng.choice([0.0, 0.05]) if E >= 16 else 0.0, train)
     K, N = 128 * _log(rng, 1, 112), _log(rng, 8, 28672)
     L, r = _log(rng, 1, 256), _log(rng, 1, 128)
     # the plain form multiplies every token by every adapter
@@ -293,10 +294,10 @@ def _exact_select(s):
             if s["group_picks"] == 2:
                 rest = part.scatter(2, part.argmax(2, keepdim=True), -math.inf).amax(2)
                 value = first + torch.where(torch.isinf(rest), 0.0, rest)
-            order = value.argsort(1, descending=True, stable=True)
+            order = value.argsort(dim=1, descending=True, stable=True)
             lost = torch.zeros_like(value, dtype=torch.bool).scatter(1, order[:, s["top_groups"]:], True)
             c = torch.where(lost[..., None], -math.inf, part).reshape(M, -1)
-        picks = c.argsort(1, descending=True, stable=True)[:, :k]
+        picks = c.argsort(dim=1, descending=True, stable=True)[:, :k]
         live = ~torch.isinf(c.gather(1, picks))
     w = p.gather(1, picks) * live
     if s["renormalise"]:
