@@ -8,4 +8,5 @@ from .lbq import (FMT_PVQ_4x8, FMT_RTN_PLANES, PATH_AUTO, PATH_GEMM, PATH_GEMV, 
                   PackedMoe, linear_forward, moe_forward, moe_from_host, moe_route, pack, pack_moe_host,
                   packed_bytes, rotate, unpack_codes, MxTensor, moe_combine, moe_combine_backward, moe_gather,
                   moe_gather_backward, moe_sort, mx_dequantize, mx_grouped_forward, mx_linear_forward, mx_matmul,
-                  mx_quantize)
+                  mx_quantize, SCORE_SIGMOID, SCORE_SOFTMAX, Adapters, adapters_backward, adapters_forward,
+                  moe_select, moe_select_backward)

@@ -229,4 +229,35 @@ hipError_t launch_moe_combine(const void *o, int dtype, int T, int H, const int3
 hipError_t launch_moe_combine_backward(const void *dy, const void *o, int dtype, int T, int H, const int32_t *pos,
                                        const float *weights, int M, int top_k, void *d_o, float *d_w, hipStream_t s);
 
+// Expert selection (select.hip): lbq_router of include/lbq.h, checked.
+constexpr int kSoftmax = 0, kSigmoid = 1;
+struct MoeSelect {
+  int E, top_k, score, groups, top_groups, group_picks, renormalise;
+  float scale;
+};
+hipError_t launch_moe_select(const MoeSelect &r, const void *logits, int dtype, int M, const float *bias, int32_t *ids,
+                             float *weights, hipStream_t s);
+hipError_t launch_moe_select_backward(const MoeSelect &r, const float *d_w, const void *logits, int dtype, int M,
+                                      const int32_t *ids, void *d_logits, hipStream_t s);
+
+// Low-rank adapters (adapters.hip): a [L][r][K], b [L][N][r] and rows in dtype
+// (16 bits), ids [M]; offsets [L + 1] and perm [M] the tokens sorted by adapter.
+constexpr int kAdapterMaxRank = 128;
+struct AdapterArgs {
+  int L, K, N, r, M, dtype;
+  const void *a, *b;
+  const float *scales;
+  const int32_t *ids, *offsets, *perm;
+  const void *x, *dy, *base;   // base: null for none
+  void *y;                     // the forward's y, the backward's dx
+  float *h;                    // [M][r], the forward's: null where it is not kept
+  float *d_a, *d_b;
+  void *scratch;               // adapters_ws_bytes of it
+};
+size_t adapters_ws_bytes(const AdapterArgs &g, bool backward);
+// whether the forward reads offsets and perm
+bool adapters_forward_by_list(const AdapterArgs &g);
+hipError_t launch_adapters_forward(const AdapterArgs &g, hipStream_t s);
+hipError_t launch_adapters_backward(const AdapterArgs &g, hipStream_t s);
+
 }  // namespace lbq

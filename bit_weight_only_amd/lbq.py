@@ -20,6 +20,7 @@ LIB_PATH = os.environ.get("LBQ_LIBRARY") or os.path.join(_HERE, "liblbq.so")
 FMT_RTN_PLANES = 0
 FMT_PVQ_4x8 = 1
 PATH_AUTO, PATH_GEMV, PATH_GEMM, PATH_GEMM_MX = 0, 1, 2, 3
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 PATH_SPLIT_ROTATION = 0x100   # test flag: the GEMM's rotation in launches of <= 3 tokens
 
 STATUS = {
@@ -36,7 +37,8 @@ EXPORTS = [
     "lbq_mx_bytes", "lbq_mx_quantize", "lbq_mx_quantize_t", "lbq_mx_dequantize", "lbq_mx_matmul_workspace",
     "lbq_mx_matmul", "lbq_mx_linear_workspace", "lbq_mx_linear_forward", "lbq_mx_grouped_workspace",
     "lbq_mx_grouped_forward", "lbq_moe_sort_workspace", "lbq_moe_sort", "lbq_moe_gather", "lbq_moe_gather_backward",
-    "lbq_moe_combine", "lbq_moe_combine_backward",
+    "lbq_moe_combine", "lbq_moe_combine_backward", "lbq_moe_select", "lbq_moe_select_backward",
+    "lbq_adapters_workspace", "lbq_adapters_backward_workspace", "lbq_adapters_forward", "lbq_adapters_backward",
 ]
 
 
@@ -68,6 +70,17 @@ class Readout(ctypes.Structure):
 class Mx(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("codes", ctypes.c_void_p),
                 ("scales", ctypes.c_void_p)]
+
+
+class Router(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_picks", ctypes.c_int32), ("renormalise", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class AdaptersView(ctypes.Structure):
+    _fields_ = [("L", ctypes.c_int32), ("K", ctypes.c_int32), ("N", ctypes.c_int32), ("r", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -127,6 +140,14 @@ def lib() -> ctypes.CDLL:
         L.lbq_moe_combine.argtypes = [c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp]
         L.lbq_moe_combine_backward.argtypes = [c_vp, c_vp, c_i32, c_i32, c_i32, c_vp, c_vp, c_i32, c_i32, c_vp, c_vp,
                                                c_vp]
+        p_ad, p_router = ctypes.POINTER(AdaptersView), ctypes.POINTER(Router)
+        L.lbq_moe_select.argtypes = [p_router, c_vp, c_i32, c_i32, c_vp, c_vp, c_vp, c_vp]
+        L.lbq_moe_select_backward.argtypes = [p_router, c_vp, c_vp, c_i32, c_vp, c_i32, c_vp, c_vp]
+        L.lbq_adapters_workspace.argtypes = [p_ad, c_i32, c_i32, p_sz]
+        L.lbq_adapters_backward_workspace.argtypes = [p_ad, c_i32, c_i32, p_sz]
+        L.lbq_adapters_forward.argtypes = [p_ad, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]
+        L.lbq_adapters_backward.argtypes = [p_ad, c_vp, c_vp, c_vp, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp,
+                                            c_sz, c_vp]
         for name in EXPORTS:
             if name != "lbq_status_string":
                 getattr(L, name).restype = c_i32
@@ -825,3 +846,196 @@ def moe_combine_backward(dy, o, pos, weights, d_o=None, d_weights=None, stream=N
             raise LbqError(st, "lbq_moe_combine_backward")
         return go_, gw
     return _on(gpu, stream, go, dy, o, pos, weights, d_o, d_weights)
+
+
+# ------------------------------------------------------------------ expert selection
+
+@functools.lru_cache(maxsize=256)
+def _router(E, top_k, score, groups, top_groups, group_picks, renormalise, scale):
+    for n in (E, top_k, score, groups, top_groups, group_picks):
+        if not -_MOST <= n <= _MOST:
+            raise LbqError(-2, f"router: {n}")
+    return ctypes.byref(Router(E, top_k, score, groups, top_groups, group_picks, bool(renormalise), scale))
+
+
+def moe_select(logits, top_k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1,
+               group_picks: int = 1, renormalise: bool = True, scale: float = 1.0, ids=None, weights=None, stream=None):
+    """lbq_moe_select of logits [M][E] (float16, bfloat16 or float32): (ids int32, weights float32), both [M][top_k].
+    Autograd does not see it; its gradient is moe_select_backward."""
+    L = _ready()
+    gpu, M, E = _rows("moe_select", logits)
+    dt = _dtype(logits.dtype, "moe_select")
+    r = _router(E, top_k, score, groups, top_groups, group_picks, renormalise, scale)
+    if bias is not None:
+        _need("moe_select", gpu, _torch.float32, (E,), bias)
+    if ids is not None:
+        _need("moe_select", gpu, _torch.int32, (M, top_k), ids)
+    if weights is not None:
+        _need("moe_select", gpu, _torch.float32, (M, top_k), weights)
+
+    def go(s):
+        i = logits.new_empty((M, top_k), dtype=_torch.int32) if ids is None else ids
+        w = logits.new_empty((M, top_k), dtype=_torch.float32) if weights is None else weights
+        st = L.lbq_moe_select(r, logits.data_ptr(), dt, M, None if bias is None else bias.data_ptr(), i.data_ptr(),
+                              w.data_ptr(), s)
+        if st:
+            raise LbqError(st, "lbq_moe_select")
+        return i, w
+    return _on(gpu, stream, go, logits, bias, ids, weights)
+
+
+def moe_select_backward(d_weights, logits, ids, score: int = SCORE_SOFTMAX, renormalise: bool = True,
+                        scale: float = 1.0, d_logits=None, stream=None):
+    """lbq_moe_select_backward: d_logits [M][E] in logits' type, for moe_select's ids of these logits (the bias and the
+    groups have no part in it)."""
+    L = _ready()
+    where = "moe_select_backward"
+    gpu, M, E = _rows(where, logits)
+    dt = _dtype(logits.dtype, where)
+    if ids.dim() != 2:
+        raise LbqError(-2, f"{where}: ids are [M][top_k]")
+    k = ids.shape[1]
+    _need(where, gpu, _torch.int32, (M, k), ids)
+    _need(where, gpu, _torch.float32, (M, k), d_weights)
+    if d_logits is not None:
+        _need(where, gpu, logits.dtype, (M, E), d_logits)
+    r = _router(E, k, score, 1, 1, 1, renormalise, scale)
+
+    def go(s):
+        d = logits.new_empty((M, E)) if d_logits is None else d_logits
+        st = L.lbq_moe_select_backward(r, d_weights.data_ptr(), logits.data_ptr(), dt, ids.data_ptr(), M, d.data_ptr(), s)
+        if st:
+            raise LbqError(st, "lbq_moe_select_backward")
+        return d
+    return _on(gpu, stream, go, d_weights, logits, ids, d_logits)
+
+
+# ------------------------------------------------------------------ low-rank adapters
+
+class Adapters:
+    """L low-rank adapters (see lbq_adapters in include/lbq.h): a [L][r][K] and b [L][N][r], both float16 or both
+    bfloat16, scales float32 [L].
+
+    It keeps the tensors and their addresses: what they hold may change, the tensors may not be replaced."""
+
+    __slots__ = ("L", "K", "N", "r", "dtype", "gpu", "_tensors", "struct", "ref")
+
+    def __init__(self, a, b, scales):
+        _ready()
+        where = "Adapters"
+        if a.dim() != 3 or b.dim() != 3:
+            raise LbqError(-2, f"{where}: a is [L][r][K] and b is [L][N][r]")
+        dt = _dtype(a.dtype, where)
+        L, r, K = a.shape
+        N = b.shape[1]
+        gpu = a.get_device()
+        if max(L, r, K, N) > _MOST:
+            raise LbqError(-2, f"{where}: {tuple(a.shape)}, {tuple(b.shape)}")
+        _need(where, gpu, a.dtype, None, a)
+        _need(where, gpu, a.dtype, (L, N, r), b)
+        _need(where, gpu, _torch.float32, (L,), scales)
+        self.L, self.K, self.N, self.r, self.dtype, self.gpu = L, K, N, r, a.dtype, gpu
+        self._tensors = (a, b, scales)
+        self.struct = AdaptersView(L, K, N, r, dt, a.data_ptr(), b.data_ptr(), scales.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+    @property
+    def a(self):
+        return self._tensors[0]
+
+    @property
+    def b(self):
+        return self._tensors[1]
+
+    @property
+    def scales(self):
+        return self._tensors[2]
+
+    def workspace_bytes(self, M: int, sorted: bool = False, backward: bool = False) -> int:
+        name = "lbq_adapters_backward_workspace" if backward else "lbq_adapters_workspace"
+        return _adapters_query(name, self.L, self.K, self.N, self.r, self.struct.dtype, int(M), bool(sorted))
+
+
+@functools.lru_cache(maxsize=4096)
+def _adapters_query(name, L, K, N, r, dtype, M, ordered) -> int:
+    if not -_MOST <= M <= _MOST:
+        raise LbqError(-2, f"{name}: {M}")
+    need = ctypes.c_size_t()
+    p = ctypes.c_void_p(16)   # aligned stand-in: queries look at sizes only
+    _check(getattr(lib(), name)(ctypes.byref(AdaptersView(L, K, N, r, dtype, p, p, p)), M, ordered, ctypes.byref(need)), name)
+    return need.value
+
+
+def _tokens(where: str, ad: Adapters, rows, cols: int, ids, order):
+    """(M, pointers of the order) after the checks that both directions share."""
+    if rows.dim() != 2 or rows.shape[1] != cols:
+        raise LbqError(-2, f"{where}: rows of {cols} are needed, got {tuple(rows.shape)}")
+    _need(where, ad.gpu, ad.dtype, None, rows)
+    M = rows.shape[0]
+    _need(where, ad.gpu, _torch.int32, (M,), ids)
+    if order is None:
+        return M, None, None
+    offsets, perm = order
+    _need(where, ad.gpu, _torch.int32, (ad.L + 1,), offsets)
+    _need(where, ad.gpu, _torch.int32, (M,), perm)
+    return M, offsets.data_ptr(), perm.data_ptr()
+
+
+def adapters_forward(ad: Adapters, x, ids, base=None, y=None, h=None, order=None, ws=None, stream=None):
+    """lbq_adapters_forward: y [M][N] = base + scales[ids] (x A^T) B^T, a token with an id outside [0, L) without the
+    second part. y may be base. h: float32 [M][r], written for adapters_backward. order: (offsets, perm) of
+    moe_sort(ids[:, None], L), where the program keeps it. Autograd does not see it."""
+    L = _ready()
+    where = "adapters_forward"
+    M, po, pp = _tokens(where, ad, x, ad.K, ids, order)
+    if base is not None:
+        _need(where, ad.gpu, ad.dtype, (M, ad.N), base)
+    if y is not None:
+        _need(where, ad.gpu, ad.dtype, (M, ad.N), y)
+    if h is not None:
+        _need(where, ad.gpu, _torch.float32, (M, ad.r), h)
+    need = _adapters_query("lbq_adapters_workspace", ad.L, ad.K, ad.N, ad.r, ad.struct.dtype, M, order is not None)
+
+    def go(s):
+        out = x.new_empty((M, ad.N)) if y is None else y
+        p, size, keep = _workspace(ws, need, x, ad.gpu, where)
+        st = L.lbq_adapters_forward(ad.ref, x.data_ptr(), M, ids.data_ptr(), po, pp,
+                                    None if base is None else base.data_ptr(), out.data_ptr(),
+                                    None if h is None else h.data_ptr(), p, size, s)
+        if st:
+            raise LbqError(st, "lbq_adapters_forward")
+        return out
+    return _on(ad.gpu, stream, go, *ad._tensors, x, ids, base, y, h, ws, *(order or ()))
+
+
+def adapters_backward(ad: Adapters, dy, x, h, ids, base=None, dx=None, d_a=None, d_b=None, order=None, ws=None,
+                      stream=None):
+    """lbq_adapters_backward: (dx [M][K], d_a float32 [L][r][K], d_b float32 [L][N][r]) from dy, x and the h that
+    adapters_forward wrote. base: the shared projection's own dx, added to dx; dx may be base."""
+    L = _ready()
+    where = "adapters_backward"
+    M, po, pp = _tokens(where, ad, x, ad.K, ids, order)
+    _need(where, ad.gpu, ad.dtype, (M, ad.N), dy)
+    _need(where, ad.gpu, _torch.float32, (M, ad.r), h)
+    for t in (base, dx):
+        if t is not None:
+            _need(where, ad.gpu, ad.dtype, (M, ad.K), t)
+    if d_a is not None:
+        _need(where, ad.gpu, _torch.float32, (ad.L, ad.r, ad.K), d_a)
+    if d_b is not None:
+        _need(where, ad.gpu, _torch.float32, (ad.L, ad.N, ad.r), d_b)
+    need = _adapters_query("lbq_adapters_backward_workspace", ad.L, ad.K, ad.N, ad.r, ad.struct.dtype, M,
+                           order is not None)
+
+    def go(s):
+        ox = x.new_empty((M, ad.K)) if dx is None else dx
+        oa = h.new_empty((ad.L, ad.r, ad.K)) if d_a is None else d_a
+        ob = h.new_empty((ad.L, ad.N, ad.r)) if d_b is None else d_b
+        p, size, keep = _workspace(ws, need, x, ad.gpu, where)
+        st = L.lbq_adapters_backward(ad.ref, dy.data_ptr(), x.data_ptr(), h.data_ptr(), M, ids.data_ptr(), po, pp,
+                                     None if base is None else base.data_ptr(), ox.data_ptr(), oa.data_ptr(),
+                                     ob.data_ptr(), p, size, s)
+        if st:
+            raise LbqError(st, "lbq_adapters_backward")
+        return ox, oa, ob
+    return _on(ad.gpu, stream, go, *ad._tensors, dy, x, h, ids, base, dx, d_a, d_b, ws, *(order or ()))

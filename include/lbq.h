@@ -539,6 +539,105 @@ lbq_status lbq_moe_combine_backward(const void *dy, const void *o, int32_t dtype
                                     const int32_t *pos, const float *weights, int32_t M, int32_t top_k, void *d_o,
                                     float *d_weights, void *stream);
 
+/* ---- Expert selection: scores, bias, groups, weights, and their gradient ----
+ *
+ * The router of an MoE block whose experts are the caller's own products
+ * (lbq_moe_sort, lbq_mx_grouped_forward, lbq_moe_combine take what it writes):
+ * lbq_moe_route's softmax over the picked logits is one of its forms. */
+
+typedef enum { LBQ_SCORE_SOFTMAX = 0, LBQ_SCORE_SIGMOID = 1 } lbq_score;
+
+/* Limits: E <= 1024, top_k <= 32 and at most the experts of top_groups groups,
+ * groups divides E, 1 <= top_groups <= groups, group_picks 1 or 2. */
+typedef struct {
+  int32_t E, top_k;
+  int32_t score;         /* lbq_score */
+  int32_t groups;        /* experts in this many equal runs; 1: no groups */
+  int32_t top_groups;    /* groups whose experts may be picked */
+  int32_t group_picks;   /* a group's value: the sum of its this many largest choice values */
+  int32_t renormalise;   /* nonzero: the weights of a token sum to scale */
+  float scale;
+} lbq_router;
+
+/* Per token t, with l = logits[t] ([M][E], dtype):
+ *   p_e = exp(l_e) / sum_i exp(l_i), or 1 / (1 + exp(-l_e));
+ *   choice value c_e = p_e + bias[e]; without bias and groups, l_e itself;
+ *   with groups: the top_groups groups with the largest values, ties to the lower
+ *   group, a group's value being the sum of its group_picks largest c (of one,
+ *   where it has one);
+ *   ids[t][j] = the expert with the j-th largest c in those groups, ties to the
+ *   lower id; weights[t][j] = scale p_id / (renormalise ? sum over the picks of
+ *   p : 1), fp32 (0 where that sum is 0).
+ * Larger is decided as 64-bit arithmetic decides it. An expert whose logit is
+ * -infinity or NaN has p = 0 and is not picked, nor is one whose bias is; a
+ * token with fewer experts than top_k has ids -1 and weights 0 behind them (no
+ * picks to lbq_moe_sort). Logits of +infinity count as the largest fp32 value.
+ *   bias: fp32 [E] or NULL; ids: int32 [M][top_k]; weights: fp32 [M][top_k];
+ *   M * top_k <= 2^24. logits 16-byte aligned.
+ * Errors, before any launch: LBQ_ERR_NULL, _SHAPE, _FORMAT (dtype, score),
+ * _ALIGN; LBQ_ERR_HIP. */
+lbq_status lbq_moe_select(const lbq_router *r, const void *logits, int32_t dtype, int32_t M, const float *bias,
+                          int32_t *ids, float *weights, void *stream);
+
+/* d_logits [M][E] (dtype) of the weights' gradient d_weights (fp32 [M][top_k]), for
+ * the picks ids that lbq_moe_select made of these logits: with S the sum of the
+ * picks' p (renormalise; else 1),
+ *   ds_j = scale (d_weights_j - [renormalise] sum_i p_i d_weights_i / S) / S,
+ * summed over the slots of an expert, and d_l_e = p_e (1 - p_e) ds_e (sigmoid) or
+ * p_e (ds_e - sum_i p_i ds_i) (softmax). The choice itself has no gradient, nor
+ * has the bias. Slots with ids outside [0, E) count nothing, whatever their
+ * d_weights. Experts that may not be picked get 0. d_logits may be logits. */
+lbq_status lbq_moe_select_backward(const lbq_router *r, const float *d_weights, const void *logits, int32_t dtype,
+                                   const int32_t *ids, int32_t M, void *d_logits, void *stream);
+
+/* ---- Low-rank adapters of many requests beside a shared projection ----
+ *
+ * L pairs (A, B) of rank r, and per token the pair of its request: what is
+ * trained and served on top of weights that stay packed. Token t with adapter
+ * a = ids[t], 0 <= a < L:
+ *   h_t = x_t A_a^T (fp32),   y_t = base_t + scales[a] h_t B_a^T, rounded once;
+ * a token with any other id has no adapter: y_t = base_t, h_t = 0. base is what
+ * the shared projection gave (lbq_linear_forward, lbq_mx_linear_forward), or
+ * NULL for none (zeros); it may be y itself.
+ * Adapters of lower rank are padded with zeros. Limits: L <= 1024, r <= 128, K a
+ * multiple of 128, K and N at most 2^24, M <= 2^20 (LBQ_ERR_SHAPE). */
+typedef struct {
+  int32_t L, K, N, r;
+  int32_t dtype;         /* LBQ_F16 or LBQ_BF16: a, b and the rows of x, base, y */
+  const void *a;         /* [L][r][K], 16-byte aligned */
+  const void *b;         /* [L][N][r], 16-byte aligned */
+  const float *scales;   /* [L] */
+} lbq_adapters;
+
+/* Workspace bytes of lbq_adapters_forward and lbq_adapters_backward for M tokens
+ * (host queries); sorted: nonzero where offsets and perm are given. */
+lbq_status lbq_adapters_workspace(const lbq_adapters *ad, int32_t M, int32_t sorted, size_t *bytes);
+lbq_status lbq_adapters_backward_workspace(const lbq_adapters *ad, int32_t M, int32_t sorted, size_t *bytes);
+
+/* y [M][N] as above, from x [M][K] and base [M][N] (or NULL), all in ad->dtype,
+ * row-major, 16-byte aligned; ids: int32 [M].
+ *   offsets [L + 1], perm [M]: the tokens sorted by adapter, as lbq_moe_sort
+ *     writes them for ids as [M][1]; both NULL: the call sorts for itself. One
+ *     order serves every layer of a batch. Contents that are not ids' order give
+ *     wrong rows, never an access out of bounds.
+ *   h: fp32 [M][r], written for the backward pass, or NULL.
+ * Repeat calls give identical bits. Errors as lbq_mx_matmul. */
+lbq_status lbq_adapters_forward(const lbq_adapters *ad, const void *x, int32_t M, const int32_t *ids,
+                                const int32_t *offsets, const int32_t *perm, const void *base, void *y, float *h,
+                                void *ws, size_t ws_bytes, void *stream);
+
+/* Its gradients, from dy [M][N], x [M][K] and the forward's h: with
+ * u_t = scales[a] dy_t B_a,
+ *   dx_t = base_t + u_t A_a (ad->dtype, rounded once; base [M][K] is the shared
+ *     projection's own dx, or NULL; it may be dx itself; dx_t = base_t without
+ *     an adapter),
+ *   d_a [L][r][K] = sum over a's tokens of u_t^T x_t, d_b [L][N][r] = scales[a] times
+ *     the sum of dy_t^T h_t, both fp32, zeros for an adapter without tokens.
+ * d_a and d_b are written, not added to. Sums have a fixed order. */
+lbq_status lbq_adapters_backward(const lbq_adapters *ad, const void *dy, const void *x, const float *h, int32_t M,
+                                 const int32_t *ids, const int32_t *offsets, const int32_t *perm, const void *base,
+                                 void *dx, float *d_a, float *d_b, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
