@@ -17,7 +17,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblbq.so")
 
 HIP_SOURCES = ["api.hip", "rotate.hip", "gemv.hip", "gemv_mfma.hip", "gemm.hip", "gemm_rtn.hip", "gemm_mx.hip", "pvq.hip", "pvq_mx.hip", "moe.hip", "moe_mx.hip", "unpack.hip", "measure.hip", "readout.hip",
-               "mxfp4.hip", "mx_gemm.hip", "mx_stream.hip", "dispatch.hip", "api_mx.hip", "select.hip", "adapters.hip", "api_adapters.hip"]
+               "mxfp4.hip", "mx_gemm.hip", "mx_stream.hip", "dispatch.hip", "api_mx.hip", "select.hip", "adapters.hip", "adapters_grad.hip", "api_adapters.hip"]
 HOST_SOURCES = ["pack.cpp", "gptq.cpp"]
 
 ARCH = os.environ.get("LBQ_OFFLOAD_ARCH", "gfx950")
@@ -31,9 +31,9 @@ HIP_FLAGS = [
     "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-Wno-unused-result",
 ]
-# mx_gemm.hip: a wave's accumulators (up to 256 registers) live in AGPRs, next
-# to operands in the 256 VGPRs an instruction can name
-AGPR_SOURCES = {"mx_gemm.hip"}
+# mx_gemm.hip, adapters_grad.hip: a wave's accumulators (up to 256 registers) live
+# in AGPRs, next to operands in the 256 VGPRs an instruction can name
+AGPR_SOURCES = {"mx_gemm.hip", "adapters_grad.hip"}
 HOST_FLAGS = ["-O2", "-fPIC", "-std=c++17", "-ffp-contract=off", "-pthread",
               "-I/opt/rocm/include", "-D__HIP_PLATFORM_AMD__"]
 

@@ -71,7 +71,7 @@ AdapterLayout adapter_layout(const AdapterArgs &g, bool sorts, bool backward) {
     l.sort = l.pos + round_up(4 * static_cast<size_t>(g.M), kAlign);
     l.scratch = l.sort + round_up(moe_sort_ws_bytes(g.M, g.L), kAlign);
   }
-  l.total = l.scratch + adapters_ws_bytes(g, backward);
+  l.total = l.scratch + (backward ? adapters_backward_ws_bytes(g) : adapters_forward_ws_bytes(g));
   return l;
 }
 

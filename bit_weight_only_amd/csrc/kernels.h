@@ -240,7 +240,7 @@ hipError_t launch_moe_select(const MoeSelect &r, const void *logits, int dtype, 
 hipError_t launch_moe_select_backward(const MoeSelect &r, const float *d_w, const void *logits, int dtype, int M,
                                       const int32_t *ids, void *d_logits, hipStream_t s);
 
-// Low-rank adapters (adapters.hip): a [L][r][K], b [L][N][r] and rows in dtype
+// Low-rank adapters (adapters.hip, adapters_grad.hip): a [L][r][K], b [L][N][r] and rows in dtype
 // (16 bits), ids [M]; offsets [L + 1] and perm [M] the tokens sorted by adapter.
 constexpr int kAdapterMaxRank = 128;
 struct AdapterArgs {
@@ -252,9 +252,10 @@ struct AdapterArgs {
   void *y;                     // the forward's y, the backward's dx
   float *h;                    // [M][r], the forward's: null where it is not kept
   float *d_a, *d_b;
-  void *scratch;               // adapters_ws_bytes of it
+  void *scratch;               // adapters_*_ws_bytes of it
 };
-size_t adapters_ws_bytes(const AdapterArgs &g, bool backward);
+size_t adapters_forward_ws_bytes(const AdapterArgs &g);
+size_t adapters_backward_ws_bytes(const AdapterArgs &g);
 // whether the forward reads offsets and perm
 bool adapters_forward_by_list(const AdapterArgs &g);
 hipError_t launch_adapters_forward(const AdapterArgs &g, hipStream_t s);
