@@ -35,22 +35,6 @@ __device__ __forceinline__ Oct load_oct_aligned(const uint16_t *p) {
 __device__ __forceinline__ void store_oct(uint16_t *p, const Oct &v) {
   *reinterpret_cast<OctAnywhere *>(p) = {{v.w[0], v.w[1], v.w[2], v.w[3]}};
 }
-// the first `valid` of eight values, the rest zero; room: values to the buffer's end
-__device__ __forceinline__ Oct load_oct_part(const uint16_t *p, int valid, size_t room) {
-  Oct o{{0, 0, 0, 0}};
-  if (valid <= 0) return o;
-  if (room >= 8) {
-    o = load_oct(p);
-#pragma unroll
-    for (int d = 0; d < 4; ++d) o.w[d] &= valid >= 2 * d + 2 ? ~0u : valid == 2 * d + 1 ? 0xFFFFu : 0u;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (i < valid) o.w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i & 1));
-  }
-  return o;
-}
-
 // D [16][16] += A [16][32] B [32][16]. Lane l gives row (column) l % 16 at k = 8 (l / 16)
 // .. + 7 and holds D's column l % 16, rows 4 (l / 16) .. + 3.
 template <int DT>
@@ -108,21 +92,29 @@ __device__ __forceinline__ Scale scale_for(float m) {
 struct Tile {
   int a, i0, n;
 };
+__device__ __forceinline__ void segment(const int32_t *__restrict__ offsets, int a, int M, int &lo, int &hi) {
+  lo = min(max(offsets[a], 0), M);
+  hi = min(max(offsets[a + 1], lo), M);
+}
+__device__ __forceinline__ int scan_lanes(int v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
 __device__ __forceinline__ Tile tile_of(const int32_t *__restrict__ offsets, int L, int M, int rows, int b) {
   const int lane = threadIdx.x & 63;
   const int per = (L + 63) / 64;
   const int first = min(lane * per, L), last = min(first + per, L);
-  int tiles = 0;
+  int lo = 0, hi = 0, tiles = 0;
   for (int a = first; a < last; ++a) {
-    const int lo = min(max(offsets[a], 0), M), hi = min(max(offsets[a + 1], lo), M);
+    segment(offsets, a, M, lo, hi);
     tiles += (hi - lo + rows - 1) / rows;
   }
-  int incl = tiles;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int o = __shfl_up(incl, d);
-    if (lane >= d) incl += o;
-  }
+  const int incl = scan_lanes(tiles);
   const uint64_t past = __ballot(incl > b);
   if (past == 0) return {-1, 0, 0};
   const int owner = __builtin_ctzll(past);
@@ -130,7 +122,7 @@ __device__ __forceinline__ Tile tile_of(const int32_t *__restrict__ offsets, int
   if (lane == owner) {
     int at = incl - tiles;
     for (int a = first; a < last; ++a) {
-      const int lo = min(max(offsets[a], 0), M), hi = min(max(offsets[a + 1], lo), M);
+      if (per > 1) segment(offsets, a, M, lo, hi);
       const int n = (hi - lo + rows - 1) / rows;
       if (b < at + n) {
         t = {a, lo + (b - at) * rows, min(hi - lo - (b - at) * rows, rows)};
@@ -141,6 +133,126 @@ __device__ __forceinline__ Tile tile_of(const int32_t *__restrict__ offsets, int
   }
   return {__builtin_amdgcn_readlane(t.a, owner), __builtin_amdgcn_readlane(t.i0, owner),
           __builtin_amdgcn_readlane(t.n, owner)};
+}
+
+// A chunk: the tokens of one adapter that one workgroup goes through, in steps of
+// `unit` tokens.
+struct Chunk {
+  int a, i0, n;     // adapter, first list entry, tokens
+  int step;         // number of its first step among all adapters'
+  int slot;         // its place among the partial sums, -1: the adapter has one chunk
+};
+
+// Where an adapter with more than one chunk keeps a chunk's sums. Its chunks but
+// the last are whole, so starts of two such lie `rows` apart, and so do two last
+// ones: at most one of each kind starts in any `rows` entries.
+__device__ __forceinline__ int slot_of(int i0, int rows, bool last) { return 2 * (i0 / rows) + (last ? 0 : 1); }
+
+// Chunk number b of `rows` tokens each (a multiple of unit), like tile_of. Offsets
+// that are no sort's can name more steps than M tokens have (max_steps, what the
+// workspace holds): a chunk with such a step is none.
+__device__ __forceinline__ Chunk chunk_of(const int32_t *__restrict__ offsets, int L, int M, int rows, int unit,
+                                          int max_steps, int b) {
+  const int lane = threadIdx.x & 63;
+  const int per = (L + 63) / 64;
+  const int first = min(lane * per, L), last = min(first + per, L);
+  int lo = 0, hi = 0, chunks = 0, steps = 0;
+  for (int a = first; a < last; ++a) {
+    segment(offsets, a, M, lo, hi);
+    chunks += (hi - lo + rows - 1) / rows;
+    steps += (hi - lo + unit - 1) / unit;
+  }
+  const int in_c = scan_lanes(chunks), in_s = scan_lanes(steps);
+  const uint64_t past = __ballot(in_c > b);
+  if (past == 0) return {-1, 0, 0, 0, -1};
+  const int owner = __builtin_ctzll(past);
+  Chunk t{-1, 0, 0, 0, -1};
+  if (lane == owner) {
+    int at = in_c - chunks, step = in_s - steps;
+    for (int a = first; a < last; ++a) {
+      if (per > 1) segment(offsets, a, M, lo, hi);
+      const int n = (hi - lo + rows - 1) / rows;
+      if (b < at + n) {
+        const int c = b - at, i0 = lo + c * rows;
+        const int s0 = step + c * (rows / unit), tokens = min(hi - i0, rows);
+        if (s0 + (tokens + unit - 1) / unit <= max_steps)
+          t = {a, i0, tokens, s0, n > 1 ? slot_of(i0, rows, c == n - 1) : -1};
+        break;
+      }
+      at += n;
+      step += (hi - lo + unit - 1) / unit;
+    }
+  }
+  auto all = [&](int v) { return __builtin_amdgcn_readlane(v, owner); };
+  return {all(t.a), all(t.i0), all(t.n), all(t.step), all(t.slot)};
+}
+
+// A step's tokens, one a lane (lanes `unit` and up the same again); past the last the
+// last once more.
+__device__ __forceinline__ int step_token(const int32_t *__restrict__ perm, const Chunk &c, int unit, int s) {
+  return perm[c.i0 + min(s * unit + (static_cast<int>(threadIdx.x) & (unit - 1)), c.n - 1)];
+}
+
+// Two steps' values in turn: the next step's loads are under way while a step is
+// computed. They are always made, the last step's again at the end: a load in a
+// branch would have the compiler wait for all that are under way.
+template <class V, class LOAD, class COMPUTE>
+__device__ __forceinline__ void in_turn(int steps, LOAD load, COMPUTE compute) {
+  V even, odd;
+  load(even, 0);
+  if (steps == 1) return compute(even, 0);
+  for (int s = 0;; s += 2) {
+    load(odd, min(s + 1, steps - 1));
+    compute(even, s);
+    if (s + 1 >= steps) return;
+    load(even, min(s + 2, steps - 1));
+    compute(odd, s + 1);
+    if (s + 2 >= steps) return;
+  }
+}
+
+// Copies columns from .. end of the tokens t0 .. t0 + 63 that have no adapter from base
+// (null: zeros) to y, rows of C; kThreads threads, eight columns and four rows of
+// them under way each. `list` is LDS.
+template <int kThreads>
+__device__ __forceinline__ void copy_others(const int32_t *__restrict__ ids, int t0, int M, int L, const uint16_t *base,
+                                            uint16_t *y, int C, int from, int end, int (&list)[64]) {
+  const int lane = threadIdx.x & 63;
+  int id = 0;
+  if (t0 + lane < M) id = ids[t0 + lane];
+  const uint64_t none = __ballot(t0 + lane < M && (id < 0 || id >= L));
+  if (none == 0 || from >= end) return;
+  if (threadIdx.x < 64 && (none >> lane & 1)) list[__builtin_popcountll(none & ((1ull << lane) - 1))] = t0 + lane;
+  __syncthreads();
+  const int units = (end - from + 7) / 8, total = __builtin_popcountll(none) * units;
+  for (int u0 = threadIdx.x; u0 < total; u0 += 4 * kThreads) {
+    Oct v[4];
+    size_t at[4];
+    int n[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = u0 + i * kThreads, c = from + u % units * 8;
+      n[i] = u < total ? min(end - c, 8) : 0;
+      at[i] = u < total ? static_cast<size_t>(list[u / units]) * C + c : 0;
+      v[i] = Oct{{0, 0, 0, 0}};
+      if (base && n[i] == 8) v[i] = load_oct(base + at[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (n[i] == 8) store_oct(y + at[i], v[i]);
+      for (int k = 0; n[i] < 8 && k < n[i]; ++k) y[at[i] + k] = base ? base[at[i] + k] : static_cast<uint16_t>(0);
+    }
+  }
+}
+
+// Rows of fewer than eight values with zeros up to eight: the kernels read eight at a
+// time.
+constexpr int kNarrow = 8;
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) adapters_pad_kernel(const uint16_t *__restrict__ x, int M, int N,
+                                                                uint16_t *__restrict__ out) {
+  const int i = blockIdx.x * kThreads + threadIdx.x, t = i / kNarrow, n = i % kNarrow;
+  if (t < M) out[i] = n < N ? x[t * N + n] : static_cast<uint16_t>(0);
 }
 
 }  // namespace adapters

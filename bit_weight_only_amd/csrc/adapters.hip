@@ -7,6 +7,7 @@
 #include "adapters.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace lbq {
 
@@ -21,29 +22,68 @@ __device__ __forceinline__ int adapter_of(const int32_t *ids, int t, int L) {
   return a >= 0 && a < L ? a : -1;
 }
 
+// Where eight values of h, and of a row of B, from j on are read: whole and inside
+// the row. Of those read twice (below j) h gives zeros.
+__device__ __forceinline__ int first_value(int j, int r) { return r > 8 && r % 8 != 0 ? min(j, r - 8) : j; }
+
+// One lane's share of h as an operand: values from j = 16 c + 8 (q % 2) on of a row of
+// h in LDS, in two 16-bit pieces: the first for q < 2, their rests for the others;
+// times a power of two of the token, whose inverse is `back`. Lane q's partner
+// holds the row's other values.
+template <int DT, int RC>
+__device__ __forceinline__ void pieces_of(const float *row, int r, int q, Oct (&out)[RC], float &back) {
+  float v[RC][8], top = 0.f;
+#pragma unroll
+  for (int c = 0; c < RC; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int j = 16 * c + 8 * (q & 1), at = first_value(j, r) + i;
+      v[c][i] = at >= j ? row[at] : 0.f;
+      top = fmaxf(top, fabsf(v[c][i]));
+    }
+  top = fmaxf(top, __uint_as_float(xor_lane_u32<16>(__float_as_uint(top))));
+  const Scale sc = scale_for<DT>(top);
+  back = sc.back;
+#pragma unroll
+  for (int c = 0; c < RC; ++c) {
+    Oct p[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[c][i] *= sc.to;
+    split8<DT, 2>(v[c], p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[c].w[i] = q < 2 ? p[0].w[i] : p[1].w[i];
+  }
+}
+
 // ------------------------------------------------------------------ x A^T
 
-// part[s][row][j] = sum over the s-th share of K of x[token(row)][k] A[a][j][k], a
-// tile of up to 16 TF tokens of one adapter per workgroup column. BY_TOKEN: every
-// token is a tile of its own, and a row its number; else rows are list entries.
+// 32 S values of a lane's rows, on their way while the block before is multiplied.
+template <int TF, int RF, int S>
+struct Block {
+  Oct x[TF][S], w[RF][S];
+  __device__ __forceinline__ void load(const uint16_t *const (&xr)[TF], const uint16_t *const (&wr)[RF], int b) {
+#pragma unroll
+    for (int f = 0; f < TF; ++f)
+#pragma unroll
+      for (int i = 0; i < S; ++i) x[f][i] = load_oct_aligned(xr[f] + 32 * (S * b + i));
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+      for (int i = 0; i < S; ++i) w[f][i] = load_oct_aligned(wr[f] + 32 * (S * b + i));
+  }
+};
+
+// The sums over blocks lo + wave, lo + wave + WAVES, .. below hi of a tile of up to
+// 16 TF tokens and 16 RF values.
 //
 // Both operands are contiguous along k, so they go from memory into the matrix
-// instruction as they are. The waves take blocks of 128 values in turn, and add
-// up at the end. Rows and columns past the last are copies of the last (their
-// results are dropped), so nothing is masked.
-template <int DT, int TF, int RF, bool BY_TOKEN>
-__global__ void __launch_bounds__(kThreads) adapters_shrink_kernel(const uint16_t *__restrict__ x, int M, int K, int r,
-                                                                   const uint16_t *__restrict__ A, int L,
-                                                                   const int32_t *__restrict__ ids,
-                                                                   const int32_t *__restrict__ offsets,
-                                                                   const int32_t *__restrict__ perm,
-                                                                   float *__restrict__ part) {
-  __shared__ float4_t red[(kWaves - 1) * TF * RF * 64];
+// instruction as they are. Rows and values past the last are copies of the last
+// (their results are dropped), so nothing is masked.
+template <int DT, int TF, int RF, int S, int WAVES, bool BY_TOKEN>
+__device__ __forceinline__ void shrink(const uint16_t *__restrict__ x, int M, int K, int r,
+                                       const uint16_t *__restrict__ A, const int32_t *__restrict__ perm,
+                                       const Tile &tile, int lo, int hi, float4_t (&acc)[TF][RF]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  Tile tile;
-  if constexpr (BY_TOKEN) tile = {adapter_of(ids, blockIdx.x, L), static_cast<int>(blockIdx.x), 1};
-  else tile = tile_of(offsets, L, M, 16 * TF, blockIdx.x);
-  if (tile.a < 0) return;
   const uint16_t *xr[TF], *wr[RF];
 #pragma unroll
   for (int f = 0; f < TF; ++f) {
@@ -54,47 +94,107 @@ __global__ void __launch_bounds__(kThreads) adapters_shrink_kernel(const uint16_
 #pragma unroll
   for (int f = 0; f < RF; ++f)
     wr[f] = A + (static_cast<size_t>(tile.a) * r + min(16 * f + col, r - 1)) * K + 8 * q;
-  float4_t acc[TF][RF] = {};
-  const int blocks = K / 128, splits = gridDim.y;
-  const int lo = static_cast<int>(static_cast<long>(blocks) * blockIdx.y / splits);
-  const int hi = static_cast<int>(static_cast<long>(blocks) * (blockIdx.y + 1) / splits);
-  for (int b = lo + wave; b < hi; b += kWaves) {
-    Oct xv[TF][4], wv[RF][4];
-#pragma unroll
-    for (int f = 0; f < TF; ++f)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) xv[f][i] = load_oct_aligned(xr[f] + 128 * b + 32 * i);
-#pragma unroll
-    for (int f = 0; f < RF; ++f)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) wv[f][i] = load_oct_aligned(wr[f] + 128 * b + 32 * i);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int f = 0; f < TF; ++f)
-#pragma unroll
-        for (int g = 0; g < RF; ++g) acc[f][g] = mfma<DT>(xv[f][i], wv[g][i], acc[f][g]);
-  }
-  if (wave > 0) {
-#pragma unroll
-    for (int f = 0; f < TF; ++f)
-#pragma unroll
-      for (int g = 0; g < RF; ++g) red[((wave - 1) * TF * RF + f * RF + g) * 64 + lane] = acc[f][g];
-  }
-  __syncthreads();
-  if (wave > 0) return;
-  float *out = part + (static_cast<size_t>(blockIdx.y) * M + tile.i0) * r;
 #pragma unroll
   for (int f = 0; f < TF; ++f)
 #pragma unroll
-    for (int g = 0; g < RF; ++g) {
-      float4_t v = acc[f][g];
+    for (int g = 0; g < RF; ++g) acc[f][g] = float4_t{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Block<TF, RF, S> &v) {
 #pragma unroll
-      for (int w = 0; w < kWaves - 1; ++w) v += red[(w * TF * RF + f * RF + g) * 64 + lane];
+    for (int i = 0; i < S; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * f + 4 * q + i, j = 16 * g + col;
-        if (t < tile.n && j < r) out[static_cast<size_t>(t) * r + j] = v[i];
+      for (int f = 0; f < TF; ++f)
+#pragma unroll
+        for (int g = 0; g < RF; ++g) acc[f][g] = mfma<DT>(v.x[f][i], v.w[g][i], acc[f][g]);
+  };
+  const int count = (hi - lo - wave + WAVES - 1) / WAVES;
+  if (count > 0)
+    in_turn<Block<TF, RF, S>>(
+        count, [&](Block<TF, RF, S> &v, int i) { v.load(xr, wr, lo + wave + i * WAVES); },
+        [&](const Block<TF, RF, S> &v, int) { multiply(v); });
+}
+
+// The waves' sums added up; value j of token t to put(t, j, v).
+template <int TF, int RF, int WAVES, class F>
+__device__ __forceinline__ void join(const float4_t (&acc)[TF][RF], float4_t *red, F put) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int f = 0; f < TF; ++f)
+#pragma unroll
+    for (int g = 0; g < RF; ++g) red[((wave * TF + f) * RF + g) * 64 + lane] = acc[f][g];
+  __syncthreads();
+  for (int u = threadIdx.x; u < TF * RF * 64; u += 64 * WAVES) {
+    float4_t v = red[u];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) v += red[w * TF * RF * 64 + u];
+    const int f = u / (RF * 64), g = u / 64 % RF, l = u % 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) put(16 * f + 4 * (l >> 4) + i, 16 * g + (l & 15), v[i]);
+  }
+}
+
+// Few tokens: part[s][row][j] = the sum over the s-th share of K, a tile per
+// workgroup column. BY_TOKEN: every token is a tile of its own, and a row its
+// number; else rows are list entries.
+template <int DT, int RF, bool BY_TOKEN>
+__global__ void __launch_bounds__(kThreads) adapters_shares_kernel(const uint16_t *__restrict__ x, int M, int K, int r,
+                                                                   const uint16_t *__restrict__ A, int L,
+                                                                   const int32_t *__restrict__ ids,
+                                                                   const int32_t *__restrict__ offsets,
+                                                                   const int32_t *__restrict__ perm,
+                                                                   float *__restrict__ part) {
+  __shared__ float4_t red[kWaves * RF * 64];
+  Tile tile;
+  if constexpr (BY_TOKEN) tile = {adapter_of(ids, blockIdx.x, L), static_cast<int>(blockIdx.x), 1};
+  else tile = tile_of(offsets, L, M, 16, blockIdx.x);
+  if (tile.a < 0) return;
+  const int blocks = K / 128, splits = gridDim.y;
+  const int lo = static_cast<int>(static_cast<long>(blocks) * blockIdx.y / splits);
+  const int hi = static_cast<int>(static_cast<long>(blocks) * (blockIdx.y + 1) / splits);
+  float4_t acc[1][RF];
+  shrink<DT, 1, RF, 4, kWaves, BY_TOKEN>(x, M, K, r, A, perm, tile, lo, hi, acc);
+  float *out = part + (static_cast<size_t>(blockIdx.y) * M + tile.i0) * r;
+  join<1, RF, kWaves>(acc, red, [&](int t, int j, float v) {
+    if (t < tile.n && j < r) out[static_cast<size_t>(t) * r + j] = v;
+  });
+}
+
+// Many tokens: a workgroup takes a tile's whole K, and leaves h as the operands
+// that the second product loads: pieces[(tile TF + f) RC + c][lane], back[tile 16 TF + t].
+// Shares of K with their sums made in the second product, once per 2048 columns, cost
+// more than they gave (1777 tokens, 5120 -> 17408, rank 64: both kernels 134 us).
+constexpr int kManyThreads = 512;
+template <int DT, int TF, int RF>
+__global__ void __launch_bounds__(kManyThreads) adapters_h_kernel(const uint16_t *__restrict__ x, int M, int K, int r,
+                                                                  const uint16_t *__restrict__ A, int L,
+                                                                  const int32_t *__restrict__ offsets,
+                                                                  const int32_t *__restrict__ perm,
+                                                                  Oct *__restrict__ pieces, float *__restrict__ back,
+                                                                  float *__restrict__ h) {
+  constexpr int kW = kManyThreads / 64, kStride = 16 * RF + 4, kS = RF == 8 ? 2 : 4;
+  __shared__ float4_t red[kW * TF * RF * 64];
+  __shared__ float hs[16 * TF * kStride];
+  const Tile tile = tile_of(offsets, L, M, 16 * TF, blockIdx.x);
+  if (tile.a < 0) return;
+  float4_t acc[TF][RF];
+  shrink<DT, TF, RF, kS, kW, false>(x, M, K, r, A, perm, tile, 0, K / (32 * kS), acc);
+  join<TF, RF, kW>(acc, red, [&](int t, int j, float v) { hs[t * kStride + j] = t < tile.n && j < r ? v : 0.f; });
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (wave < TF) {
+    Oct o[RF];
+    float b;
+    pieces_of<DT, RF>(hs + (16 * wave + (lane & 15)) * kStride, r, lane >> 4, o, b);
+    const size_t at = static_cast<size_t>(blockIdx.x) * TF + wave;
+#pragma unroll
+    for (int c = 0; c < RF; ++c) pieces[(at * RF + c) * 64 + lane] = o[c];
+    if (lane < 16) back[16 * at + lane] = b;
+  }
+  if (h)
+    for (int i = threadIdx.x; i < 16 * TF * 16 * RF; i += kManyThreads) {
+      const int t = i / (16 * RF), j = i % (16 * RF);
+      if (t < tile.n && j < r) {
+        const int token = perm[tile.i0 + t];
+        if (token >= 0 && token < M) h[static_cast<size_t>(token) * r + j] = hs[t * kStride + j];
       }
     }
 }
@@ -102,34 +202,114 @@ __global__ void __launch_bounds__(kThreads) adapters_shrink_kernel(const uint16_
 // ------------------------------------------------------------------ base + s h B^T
 
 // y[t] = base[t] + s_a h_t B_a^T for a tile of tokens, kSpan = 256 columns a step (64 a
-// wave); h_t the sum of the shares that the kernel above wrote, in two 16-bit
+// wave); h_t in two 16-bit
 // pieces side by side along the instruction's k: 16 values of h and their rests
 // against the same 16 values of B twice.
 //
 // D's rows are columns of y, in an order that leaves a lane eight neighbours:
-// row 4 q + i of instruction m is column 8 q + 4 m + i.
-constexpr int kSpan = 64 * kWaves;
+// row 4 q + i of instruction m is column 8 q + 4 m + i. A piece of eight columns, or
+// of eight values of B, that would reach past the last starts earlier, so that
+// every load is whole and none is in a branch; what it has twice is not stored, or
+// meets a zero of h.
+constexpr int kSpan = 64 * kWaves, kMostShares = 16;
 
-template <int DT>
-__device__ __forceinline__ void copy_row(const uint16_t *base, uint16_t *y, size_t row, int N, int n, int end) {
-  // n: this thread's first column, eight a thread
-  for (; n < end; n += 8 * kThreads) {
-    const size_t at = row * N + n;
-    if (n + 8 <= end) {
-      store_oct(y + at, base ? load_oct(base + at) : Oct{{0, 0, 0, 0}});
-    } else {
-      for (int i = 0; i < end - n; ++i) y[at + i] = base ? base[at + i] : static_cast<uint16_t>(0);
+// RANK: kWhole, r a multiple of 8; kMore, above 8; kLess, below (single loads).
+enum { kWhole, kMore, kLess };
+
+// B_a's values for the columns n0 .. n0 + 63: instruction 2 k + m's operand rows.
+template <int RC, int RANK>
+__device__ __forceinline__ void load_weights(Oct (&b)[4][RC], const uint16_t *__restrict__ Ba, int n0, int N, int width,
+                                             int r) {
+  const int lane = threadIdx.x & 63, col = lane & 15, q = lane >> 4;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int n = min(min(n0 + 32 * (m >> 1) + 8 * (col >> 2), width - 8) + 4 * (m & 1) + (col & 3), N - 1);
+    const uint16_t *p = Ba + static_cast<size_t>(n) * r;
+#pragma unroll
+    for (int c = 0; c < RC; ++c) {
+      const int j = 16 * c + 8 * (q & 1);
+      if constexpr (RANK == kLess) {
+        uint32_t e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          e[i] = p[min(j + i, r - 1)];
+          e[i] = j + i < r ? e[i] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[m][c].w[i] = e[2 * i] | e[2 * i + 1] << 16;
+      } else {
+        // (past r all of h's values are zeros, and B's from here its own)
+        b[m][c] = load_oct(p + min(j, r - 8));
+      }
     }
   }
 }
 
-template <int DT, int TF, int RC, bool BY_TOKEN, bool R8>
-__global__ void __launch_bounds__(kThreads) adapters_expand_kernel(
+// The 64 columns from n0 of 16 tokens: base + back (h B^T), stored to the token's row
+// `to` where it is live. y: base's values, 32 columns each.
+template <int DT, int RC>
+__device__ __forceinline__ void add_product(const Oct (&b)[4][RC], const Oct (&hv)[RC], float back, const Oct (&y)[2],
+                                            uint16_t *to, bool live, int n0, int N, int width) {
+  const int q = threadIdx.x >> 4 & 3;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float4_t d[2] = {};
+#pragma unroll
+    for (int c = 0; c < RC; ++c)
+#pragma unroll
+      for (int m = 0; m < 2; ++m) d[m] = mfma<DT>(b[2 * k + m][c], hv[c], d[m]);
+    Oct o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4_t &z = d[i >> 1];
+      const uint32_t v = y[k].w[i];
+      o.w[i] = pack2<DT>(fmaf(z[2 * (i & 1)], back, to_f32<DT>(static_cast<uint16_t>(v))),
+                         fmaf(z[2 * (i & 1) + 1], back, to_f32<DT>(static_cast<uint16_t>(v >> 16))));
+    }
+    const int n = n0 + 32 * k + 8 * q;
+    if (!live) continue;
+    if (n + 8 <= N) {
+      store_oct(to + n, o);
+    } else {
+      const int first = min(n, width - 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (first + i >= n && first + i < N) to[first + i] = static_cast<uint16_t>(o.w[i / 2] >> (16 * (i & 1)));
+    }
+  }
+}
+
+// base's values of the 64 columns from n0; null: zeros.
+__device__ __forceinline__ void load_base(Oct (&y)[2], const uint16_t *base, size_t row, int n0, int width) {
+  const int q = threadIdx.x >> 4 & 3;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    y[k] = Oct{{0, 0, 0, 0}};
+    if (base) y[k] = load_oct(base + row * width + min(n0 + 32 * k + 8 * q, width - 8));
+  }
+}
+
+// The tokens t0 .. t0 + 63 without an adapter: y = base, h = 0.
+__device__ __forceinline__ void others(const int32_t *ids, int t0, int M, int L, int N, int r, const uint16_t *base,
+                                       uint16_t *y, float *h, int from, int end) {
+  __shared__ int list[64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (h && from == 0)
+    for (int t = t0 + wave; t < min(t0 + 64, M); t += kWaves)
+      if (adapter_of(ids, t, L) < 0)
+        for (int j = lane; j < r; j += 64) h[static_cast<size_t>(t) * r + j] = 0.f;
+  if (base != y) copy_others<kThreads>(ids, t0, M, L, base, y, N, from, end, list);
+}
+
+// Few tokens: one tile of up to 16 a workgroup column, h the sum of the shares.
+template <int DT, int RC, bool BY_TOKEN, int RANK>
+__global__ void __launch_bounds__(kThreads) adapters_few_kernel(
     const float *__restrict__ part, int splits, int M, int N, int r, const uint16_t *__restrict__ B,
     const float *__restrict__ scales, int L, const int32_t *__restrict__ ids, const int32_t *__restrict__ offsets,
-    const int32_t *__restrict__ perm, const uint16_t *base, uint16_t *y, float *__restrict__ h, int tiles, int steps) {
-  constexpr int kRows = 16 * TF, kStride = 16 * RC + 4;
-  __shared__ float hs[kRows * kStride];
+    const int32_t *__restrict__ perm, const uint16_t *base, const uint16_t *rows_of_base, uint16_t *y,
+    float *__restrict__ h, int tiles, int steps) {
+  constexpr int kStride = 16 * RC + 4;
+  __shared__ float hs[16 * kStride];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const int from = blockIdx.y * steps * kSpan, end = min(from + steps * kSpan, N);
   Tile tile;
@@ -137,34 +317,35 @@ __global__ void __launch_bounds__(kThreads) adapters_expand_kernel(
     const int t = blockIdx.x;
     tile = {adapter_of(ids, t, L), t, 1};
     if (tile.a < 0) {
-      if (base != y) copy_row<DT>(base, y, t, N, from + 8 * threadIdx.x, end);
+      for (int n = from + threadIdx.x; base != y && n < end; n += kThreads)
+        y[static_cast<size_t>(t) * N + n] = base ? base[static_cast<size_t>(t) * N + n] : static_cast<uint16_t>(0);
       if (h && blockIdx.y == 0)
         for (int j = threadIdx.x; j < r; j += kThreads) h[static_cast<size_t>(t) * r + j] = 0.f;
       return;
     }
   } else {
-    if (static_cast<int>(blockIdx.x) >= tiles) {   // 64 tokens: those without an adapter
-      const int t0 = (blockIdx.x - tiles) * 64;
-      const uint64_t none = __ballot(t0 + lane < M && adapter_of(ids, min(t0 + lane, M - 1), L) < 0);
-      for (uint64_t left = none; left; left &= left - 1) {
-        const int t = t0 + __builtin_ctzll(left);
-        if (base != y) copy_row<DT>(base, y, t, N, from + 8 * threadIdx.x, end);
-        if (h && blockIdx.y == 0)
-          for (int j = threadIdx.x; j < r; j += kThreads) h[static_cast<size_t>(t) * r + j] = 0.f;
-      }
-      return;
-    }
-    tile = tile_of(offsets, L, M, kRows, blockIdx.x);
+    if (static_cast<int>(blockIdx.x) >= tiles)
+      return others(ids, (blockIdx.x - tiles) * 64, M, L, N, r, base, y, h, from, end);
+    tile = tile_of(offsets, L, M, 16, blockIdx.x);
     if (tile.a < 0) return;
   }
-  // h of the tile's tokens; zeros in the columns past r and, so that nothing
-  // unset is read, the rows past the last
-  for (int i = threadIdx.x; i < kRows * 16 * RC; i += kThreads) {
+  const int width = max(N, kNarrow);   // columns of a row of rows_of_base
+  int token = tile.i0 + min(col, tile.n - 1);
+  if constexpr (!BY_TOKEN) token = perm[token];
+  const bool live = col < tile.n && token >= 0 && token < M;
+  const size_t row = static_cast<size_t>(min(max(token, 0), M - 1));
+  // the shares added up; zeros past r and, so that nothing unset is read, past the
+  // tile's last token
+  for (int i = threadIdx.x; i < 16 * 16 * RC; i += kThreads) {
     const int t = i / (16 * RC), j = i % (16 * RC);
     float v = 0.f;
     if (t < tile.n && j < r) {
       const float *p = part + static_cast<size_t>(tile.i0 + t) * r + j;
-      for (int s = 0; s < splits; ++s) v += p[static_cast<size_t>(s) * M * r];
+      float w[kMostShares];   // all under way at once
+#pragma unroll
+      for (int s = 0; s < kMostShares; ++s) w[s] = s < splits ? p[static_cast<size_t>(s) * M * r] : 0.f;
+#pragma unroll
+      for (int s = 0; s < kMostShares; ++s) v += w[s];
       if (h && blockIdx.y == 0) {
         const int at = BY_TOKEN ? tile.i0 : perm[tile.i0 + t];
         if (at >= 0 && at < M) h[static_cast<size_t>(at) * r + j] = v;
@@ -173,176 +354,192 @@ __global__ void __launch_bounds__(kThreads) adapters_expand_kernel(
     hs[t * kStride + j] = v;
   }
   __syncthreads();
-  Oct hv[TF][RC];
-  float back[TF];
-  size_t row[TF];
-  bool live[TF];
-  const float sa = scales[tile.a];
-#pragma unroll
-  for (int f = 0; f < TF; ++f) {
-    const int t = 16 * f + col;
-    int at = tile.i0 + min(t, tile.n - 1);
-    if constexpr (!BY_TOKEN) at = perm[at];
-    live[f] = t < tile.n && at >= 0 && at < M;
-    row[f] = static_cast<size_t>(live[f] ? at : 0) * N;
-    float v[RC][8], top = 0.f;
-#pragma unroll
-    for (int c = 0; c < RC; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[c][i] = hs[t * kStride + 16 * c + 8 * (q & 1) + i];
-        top = fmaxf(top, fabsf(v[c][i]));
-      }
-    top = fmaxf(top, __uint_as_float(xor_lane_u32<16>(__float_as_uint(top))));
-    const Scale sc = scale_for<DT>(top);
-    back[f] = sa * sc.back;
-#pragma unroll
-    for (int c = 0; c < RC; ++c) {
-      Oct p[2];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[c][i] *= sc.to;
-      split8<DT, 2>(v[c], p);
-      hv[f][c] = q < 2 ? p[0] : p[1];
-    }
-  }
+  Oct hv[RC];
+  float back;
+  pieces_of<DT, RC>(hs + col * kStride, r, q, hv, back);
+  back *= scales[tile.a];
   const uint16_t *Ba = B + static_cast<size_t>(tile.a) * N * r;
-  const size_t total = static_cast<size_t>(L) * N * r;
-  for (int n0 = from + 64 * wave; n0 < end; n0 += kSpan) {
-    Oct bv[4][RC];
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const int n = min(n0 + 32 * (m >> 1) + 8 * (col >> 2) + 4 * (m & 1) + (col & 3), N - 1);
-#pragma unroll
-      for (int c = 0; c < RC; ++c) {
-        const int j = 16 * c + 8 * (q & 1);
-        const size_t at = static_cast<size_t>(n) * r + j;
-        if constexpr (R8) {
-          bv[m][c] = j < r ? load_oct(Ba + at) : Oct{{0, 0, 0, 0}};
-        } else {
-          bv[m][c] = load_oct_part(Ba + at, r - j, total - min(total, static_cast<size_t>(tile.a) * N * r + at));
-        }
-      }
-    }
-    Oct yv[TF][2];
-#pragma unroll
-    for (int f = 0; f < TF; ++f)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int n = n0 + 32 * k + 8 * q;
-        yv[f][k] = Oct{{0, 0, 0, 0}};
-        if (base && live[f]) {
-          if (n + 8 <= N) yv[f][k] = load_oct(base + row[f] + n);
-          else yv[f][k] = load_oct_part(base + row[f] + n, N - n, 0);
-        }
-      }
-#pragma unroll
-    for (int f = 0; f < TF; ++f)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float4_t d[2] = {};
-#pragma unroll
-        for (int c = 0; c < RC; ++c)
-#pragma unroll
-          for (int m = 0; m < 2; ++m) d[m] = mfma<DT>(bv[2 * k + m][c], hv[f][c], d[m]);
-        Oct o;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float4_t &v = d[i >> 1];
-          const uint32_t b = yv[f][k].w[i];
-          const float lo = fmaf(v[2 * (i & 1)], back[f], to_f32<DT>(static_cast<uint16_t>(b)));
-          const float hi = fmaf(v[2 * (i & 1) + 1], back[f], to_f32<DT>(static_cast<uint16_t>(b >> 16)));
-          o.w[i] = pack2<DT>(lo, hi);
-        }
-        const int n = n0 + 32 * k + 8 * q;
-        if (live[f]) {
-          if (n + 8 <= N) {
-            store_oct(y + row[f] + n, o);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (n + i < N) y[row[f] + n + i] = static_cast<uint16_t>(o.w[i / 2] >> (16 * (i & 1)));
-          }
-        }
-      }
-  }
+  struct Step {
+    Oct b[4][RC], y[2];
+  };
+  const int n0 = from + 64 * wave, count = (end - n0 + kSpan - 1) / kSpan;
+  if (n0 < end)
+    in_turn<Step>(
+        count,
+        [&](Step &v, int s) {
+          load_weights<RC, RANK>(v.b, Ba, n0 + s * kSpan, N, width, r);
+          load_base(v.y, base ? rows_of_base : nullptr, row, n0 + s * kSpan, width);
+        },
+        [&](const Step &v, int s) {
+          add_product<DT, RC>(v.b, hv, back, v.y, y + row * N, live, n0 + s * kSpan, N, width);
+        });
 }
+
+// Many tokens: a workgroup takes kSpan columns, whose part of B stays in registers,
+// and goes through a chunk of an adapter's tokens, 16 TF a step.
+template <int DT, int TF, int RC, int RANK>
+__global__ void __launch_bounds__(kThreads) adapters_y_kernel(
+    const Oct *__restrict__ pieces, const float *__restrict__ backs, int M, int N, int r,
+    const uint16_t *__restrict__ B, const float *__restrict__ scales, int L, const int32_t *__restrict__ ids,
+    const int32_t *__restrict__ offsets, const int32_t *__restrict__ perm, const uint16_t *base,
+    const uint16_t *rows_of_base, uint16_t *y, float *__restrict__ h, int rows, int chunks, int max_steps) {
+  constexpr int kUnit = 16 * TF;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15;
+  const int from = blockIdx.x * kSpan, end = min(from + kSpan, N);
+  if (static_cast<int>(blockIdx.y) >= chunks)
+    return others(ids, (blockIdx.y - chunks) * 64, M, L, N, r, base, y, h, from, end);
+  const Chunk c = chunk_of(offsets, L, M, rows, kUnit, max_steps, blockIdx.y);
+  const int n0 = from + 64 * wave;
+  if (c.a < 0 || n0 >= N) return;
+  const int width = max(N, kNarrow);   // columns of a row of rows_of_base
+  Oct b[4][RC];
+  load_weights<RC, RANK>(b, B + static_cast<size_t>(c.a) * N * r, n0, N, width, r);
+  const float sa = scales[c.a];
+  struct Step {
+    Oct h[TF][RC], y[TF][2];
+    float back[TF];
+    size_t row[TF];
+    bool live[TF];
+  };
+  int token = step_token(perm, c, kUnit, 0);   // of the step whose loads come next
+  in_turn<Step>(
+      (c.n + kUnit - 1) / kUnit,
+      [&](Step &v, int s) {
+#pragma unroll
+        for (int f = 0; f < TF; ++f) {
+          const int t = __shfl(token, 16 * f + col);
+          const size_t at = static_cast<size_t>(c.step + s) * TF + f;
+          v.live[f] = s * kUnit + 16 * f + col < c.n && t >= 0 && t < M;
+          v.row[f] = static_cast<size_t>(min(max(t, 0), M - 1));
+          load_base(v.y[f], base ? rows_of_base : nullptr, v.row[f], n0, width);
+          v.back[f] = backs[16 * at + col];
+#pragma unroll
+          for (int k = 0; k < RC; ++k) v.h[f][k] = pieces[(at * RC + k) * 64 + lane];
+        }
+        token = step_token(perm, c, kUnit, s + 1);
+      },
+      [&](const Step &v, int) {
+#pragma unroll
+        for (int f = 0; f < TF; ++f)
+          add_product<DT, RC>(b, v.h[f], v.back[f] * sa, v.y[f], y + v.row[f] * N, v.live[f], n0, N, width);
+      });
+}
+
+// ------------------------------------------------------------------ plan
 
 // How the forward pass is cut up.
 struct ForwardPlan {
-  bool by_token;
-  int tf, rf;           // 16-token and 16-column pieces of a tile
+  bool few, by_token;
+  int tf, rf;           // 16-token and 16-value pieces of a tile
   int tiles;            // at most
   int splits;           // shares of K
-  int steps, chunks;    // kSpan-column steps of a workgroup, workgroups along N
+  int steps;            // kSpan-column steps of a workgroup
+  int rows, chunks;     // many tokens: of a chunk, at most
+  size_t pieces, back, pad, total;   // where in the workspace (part at its start)
 };
 constexpr int kFewTokens = 64;
-constexpr int kWant = 1024;   // workgroups that fill the card
 
 ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
   ForwardPlan p{};
+  p.few = g.M <= kFewTokens;
   p.by_token = !by_list;
   const int frags = (g.r + 15) / 16;
   p.rf = frags <= 1 ? 1 : frags <= 2 ? 2 : frags <= 4 ? 4 : 8;
+  const int some = std::max(1, std::min(g.L, g.M));
   // tokens of an adapter on average decide the tile
-  const int each = p.by_token ? 1 : g.M / std::max(1, std::min(g.L, g.M));
-  p.tf = p.by_token || each <= 16 ? 1 : each <= 48 || p.rf >= 4 ? 2 : 4;
-  const int rows = 16 * p.tf;
-  p.tiles = p.by_token ? g.M : g.M / rows + std::min(g.L, g.M);
-  const int likely = p.by_token ? g.M : std::max(1, g.M / rows);
-  const int blocks = g.K / 128;
-  // (the same for few tokens with and without an order: so is the result)
-  const int cut = g.M <= kFewTokens ? std::max(1, g.M) : likely;
-  p.splits = std::max(1, std::min({(kWant + cut - 1) / cut, (blocks + kWaves - 1) / kWaves, 16}));
-  const int spans = (g.N + kSpan - 1) / kSpan;
-  p.steps = std::max(1, std::min(8, static_cast<int>(static_cast<long>(spans) * likely / kWant)));
-  p.chunks = (spans + p.steps - 1) / p.steps;
+  p.tf = p.few || g.M / some <= 16 || p.rf == 8 ? 1 : 2;
+  const int unit = 16 * p.tf, spans = (g.N + kSpan - 1) / kSpan;
+  p.tiles = p.few && p.by_token ? g.M : g.M / unit + some;
+  if (p.few) {
+    // (the same with and without an order: so is the result)
+    p.splits = std::max(1, std::min({512 / std::max(1, g.M), (g.K / 128 + kWaves - 1) / kWaves, kMostShares}));
+    p.steps = std::max(1, std::min(8, static_cast<int>(static_cast<long>(spans) * g.M / 512)));
+  } else {
+    const long rows = static_cast<long>(g.M) * spans / 2048;
+    p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, 128l), 1024l));
+    p.chunks = g.M / p.rows + some;
+  }
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  if (!p.few) {
+    p.back = up(static_cast<size_t>(p.tiles) * p.tf * p.rf * 64 * sizeof(Oct));
+    p.pad = p.back + up(static_cast<size_t>(p.tiles) * unit * 4);
+  } else {
+    p.pad = up(static_cast<size_t>(p.splits) * g.M * g.r * 4);
+  }
+  p.total = p.pad + (g.N < kNarrow ? static_cast<size_t>(g.M) * kNarrow * 2 : 0);
   return p;
 }
 
-template <int DT, int TF, int RC, bool BY_TOKEN>
-void forward_go(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
+template <int DT, int RC>
+void forward_rank(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
   const uint16_t *x = static_cast<const uint16_t *>(g.x), *a = static_cast<const uint16_t *>(g.a);
   const uint16_t *b = static_cast<const uint16_t *>(g.b), *base = static_cast<const uint16_t *>(g.base);
   uint16_t *y = static_cast<uint16_t *>(g.y);
-  float *part = static_cast<float *>(g.scratch);
+  uint8_t *ws = static_cast<uint8_t *>(g.scratch);
   const dim3 block(kThreads);
-  hipLaunchKernelGGL((adapters_shrink_kernel<DT, TF, RC, BY_TOKEN>), dim3(p.tiles, p.splits), block, 0, s, x, g.M, g.K,
-                     g.r, a, g.L, g.ids, g.offsets, g.perm, part);
-  const int others = BY_TOKEN || (base == y && !g.h) ? 0 : (g.M + 63) / 64;
-  const dim3 grid(p.tiles + others, p.chunks);
-  if (g.r % 8 == 0)
-    hipLaunchKernelGGL((adapters_expand_kernel<DT, TF, RC, BY_TOKEN, true>), grid, block, 0, s, part, p.splits, g.M, g.N,
-                       g.r, b, g.scales, g.L, g.ids, g.offsets, g.perm, base, y, g.h, p.tiles, p.steps);
-  else
-    hipLaunchKernelGGL((adapters_expand_kernel<DT, TF, RC, BY_TOKEN, false>), grid, block, 0, s, part, p.splits, g.M,
-                       g.N, g.r, b, g.scales, g.L, g.ids, g.offsets, g.perm, base, y, g.h, p.tiles, p.steps);
-}
-
-template <int DT, int RC>
-void forward_tiles(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
-  if (p.by_token) return forward_go<DT, 1, RC, true>(g, p, s);
-  if (p.tf == 1) return forward_go<DT, 1, RC, false>(g, p, s);
-  if constexpr (RC < 4) {
-    if (p.tf == 4) return forward_go<DT, 4, RC, false>(g, p, s);
+  const uint16_t *wide = base;
+  if (base && g.N < kNarrow) {
+    uint16_t *pad = reinterpret_cast<uint16_t *>(ws + p.pad);
+    hipLaunchKernelGGL(adapters_pad_kernel<kThreads>, dim3((g.M * kNarrow + kThreads - 1) / kThreads), block, 0, s, base,
+                       g.M, g.N, pad);
+    wide = pad;
   }
-  forward_go<DT, 2, RC, false>(g, p, s);
+  const unsigned spans = (g.N + kSpan - 1) / kSpan, rest = base == y && !g.h ? 0 : (g.M + 63) / 64;
+  const int rank = g.r % 8 == 0 ? kWhole : g.r > 8 ? kMore : kLess;
+  if (p.few) {
+    float *part = reinterpret_cast<float *>(ws);
+    auto go = [&](auto first, auto second, bool by_token) {
+      hipLaunchKernelGGL(first, dim3(p.tiles, p.splits), block, 0, s, x, g.M, g.K, g.r, a, g.L, g.ids, g.offsets,
+                         g.perm, part);
+      hipLaunchKernelGGL(second, dim3(p.tiles + (by_token ? 0 : rest), (spans + p.steps - 1) / p.steps), block, 0, s,
+                         part, p.splits, g.M, g.N, g.r, b, g.scales, g.L, g.ids, g.offsets, g.perm, base, wide, y, g.h,
+                         p.tiles, p.steps);
+    };
+    auto pick = [&](auto by_token) {
+      constexpr bool kBy = decltype(by_token)::value;
+      auto first = adapters_shares_kernel<DT, RC, kBy>;
+      if (rank == kWhole) go(first, adapters_few_kernel<DT, RC, kBy, kWhole>, kBy);
+      else if (rank == kMore) go(first, adapters_few_kernel<DT, RC, kBy, kMore>, kBy);
+      else if constexpr (RC == 1) go(first, adapters_few_kernel<DT, RC, kBy, kLess>, kBy);
+    };
+    if (p.by_token) pick(std::true_type{});
+    else pick(std::false_type{});
+    return;
+  }
+  Oct *pieces = reinterpret_cast<Oct *>(ws);
+  float *back = reinterpret_cast<float *>(ws + p.back);
+  auto go = [&](auto first, auto second) {
+    hipLaunchKernelGGL(first, dim3(p.tiles), dim3(kManyThreads), 0, s, x, g.M, g.K, g.r, a, g.L, g.offsets, g.perm,
+                       pieces, back, g.h);
+    hipLaunchKernelGGL(second, dim3(spans, p.chunks + rest), block, 0, s, pieces, back, g.M, g.N, g.r, b, g.scales, g.L,
+                       g.ids, g.offsets, g.perm, base, wide, y, g.h, p.rows, p.chunks, p.tiles);
+  };
+  auto pick = [&](auto tf) {
+    constexpr int kTF = decltype(tf)::value;
+    auto first = adapters_h_kernel<DT, kTF, RC>;
+    if (rank == kWhole) go(first, adapters_y_kernel<DT, kTF, RC, kWhole>);
+    else if (rank == kMore) go(first, adapters_y_kernel<DT, kTF, RC, kMore>);
+    else if constexpr (RC == 1) go(first, adapters_y_kernel<DT, kTF, RC, kLess>);
+  };
+  if constexpr (RC < 8) {
+    if (p.tf == 2) return pick(std::integral_constant<int, 2>{});
+  }
+  pick(std::integral_constant<int, 1>{});
 }
 
 template <int DT>
 void forward_ranks(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
-  if (p.rf == 1) forward_tiles<DT, 1>(g, p, s);
-  else if (p.rf == 2) forward_tiles<DT, 2>(g, p, s);
-  else if (p.rf == 4) forward_tiles<DT, 4>(g, p, s);
-  else forward_tiles<DT, 8>(g, p, s);
+  if (p.rf == 1) forward_rank<DT, 1>(g, p, s);
+  else if (p.rf == 2) forward_rank<DT, 2>(g, p, s);
+  else if (p.rf == 4) forward_rank<DT, 4>(g, p, s);
+  else forward_rank<DT, 8>(g, p, s);
 }
 
 }  // namespace
 
 bool adapters_forward_by_list(const AdapterArgs &g) { return g.M > kFewTokens; }
 
-size_t adapters_forward_ws_bytes(const AdapterArgs &g) {
-  return static_cast<size_t>(g.M) * g.r * 4 * forward_plan(g, true).splits;
-}
+size_t adapters_forward_ws_bytes(const AdapterArgs &g) { return forward_plan(g, true).total; }
 
 hipError_t launch_adapters_forward(const AdapterArgs &g, hipStream_t s) {
   const ForwardPlan p = forward_plan(g, g.offsets != nullptr);

@@ -22,78 +22,13 @@ namespace {
 using namespace adapters;
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kPieceThreads = 512;
 constexpr int kStep = 32;   // tokens of one step: the instruction's k
 
 // Pieces of h and u in the sums over tokens, which stay fp32: as exact as fp32
 // itself (two pieces of fp16 hold 22 bits, of bf16 only 16).
 template <int DT>
 constexpr int kPieces = DT == kF16 ? 2 : 3;
-
-// A chunk: the tokens whose sums one workgroup keeps in registers.
-struct Chunk {
-  int a, i0, n;     // adapter, first list entry, tokens
-  int step;         // number of its first step among all adapters'
-  int slot;         // its place among the partial sums, -1: the adapter has one chunk
-};
-
-// Where an adapter with more than one chunk keeps a chunk's sums. Its chunks but
-// the last are whole, so starts of two such lie `rows` apart, and so do two last
-// ones: at most one of each kind starts in any `rows` entries.
-__device__ __forceinline__ int slot_of(int i0, int rows, bool last) { return 2 * (i0 / rows) + (last ? 0 : 1); }
-
-__device__ __forceinline__ void segment(const int32_t *offsets, int a, int M, int &lo, int &hi) {
-  lo = min(max(offsets[a], 0), M);
-  hi = min(max(offsets[a + 1], lo), M);
-}
-
-// Chunk number b of `rows` tokens each (a multiple of kStep), like tile_of. Offsets
-// that are no sort's can name more steps than M tokens have (max_steps, what the
-// workspace holds): a chunk with such a step is none.
-__device__ __forceinline__ Chunk chunk_of(const int32_t *__restrict__ offsets, int L, int M, int rows, int max_steps,
-                                          int b) {
-  const int lane = threadIdx.x & 63;
-  const int per = (L + 63) / 64;
-  const int first = min(lane * per, L), last = min(first + per, L);
-  int chunks = 0, steps = 0;
-  for (int a = first; a < last; ++a) {
-    int lo, hi;
-    segment(offsets, a, M, lo, hi);
-    chunks += (hi - lo + rows - 1) / rows;
-    steps += (hi - lo + kStep - 1) / kStep;
-  }
-  int in_c = chunks, in_s = steps;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int c = __shfl_up(in_c, d), s = __shfl_up(in_s, d);
-    if (lane >= d) {
-      in_c += c;
-      in_s += s;
-    }
-  }
-  const uint64_t past = __ballot(in_c > b);
-  if (past == 0) return {-1, 0, 0, 0, -1};
-  const int owner = __builtin_ctzll(past);
-  Chunk t{-1, 0, 0, 0, -1};
-  if (lane == owner) {
-    int at = in_c - chunks, step = in_s - steps;
-    for (int a = first; a < last; ++a) {
-      int lo, hi;
-      segment(offsets, a, M, lo, hi);
-      const int n = (hi - lo + rows - 1) / rows;
-      if (b < at + n) {
-        const int c = b - at, i0 = lo + c * rows;
-        const int s0 = step + c * (rows / kStep), tokens = min(hi - i0, rows);
-        if (s0 + (tokens + kStep - 1) / kStep <= max_steps)
-          t = {a, i0, tokens, s0, n > 1 ? slot_of(i0, rows, c == n - 1) : -1};
-        break;
-      }
-      at += n;
-      step += (hi - lo + kStep - 1) / kStep;
-    }
-  }
-  auto all = [&](int v) { return __builtin_amdgcn_readlane(v, owner); };
-  return {all(t.a), all(t.i0), all(t.n), all(t.step), all(t.slot)};
-}
 
 // ------------------------------------------------------------------ pieces
 
@@ -111,19 +46,19 @@ struct Pieces {
 // One workgroup per step: v[t][j] = scale * sum of `shares` shares (share s at src +
 // s M r, rows by list entry), or the rows of h by token.
 template <int DT, int RF, bool OF_H>
-__global__ void __launch_bounds__(kThreads) adapters_pieces_kernel(const float *__restrict__ src, int shares, int M,
+__global__ void __launch_bounds__(kPieceThreads) adapters_pieces_kernel(const float *__restrict__ src, int shares, int M,
                                                                    int r, const float *__restrict__ scales, int L,
                                                                    const int32_t *__restrict__ offsets,
                                                                    const int32_t *__restrict__ perm, Pieces out) {
   constexpr int kP = kPieces<DT>, kCols = 16 * RF, kStride = kCols + 4;
   __shared__ float v[kStep * kStride];
-  __shared__ float top[kWaves];
-  const Chunk c = chunk_of(offsets, L, M, kStep, gridDim.x, blockIdx.x);
+  __shared__ float top[kPieceThreads / 64];
+  const Chunk c = chunk_of(offsets, L, M, kStep, kStep, gridDim.x, blockIdx.x);
   if (c.a < 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const float sa = OF_H ? 1.f : scales[c.a];
   float m = 0.f;
-  for (int i = threadIdx.x; i < kStep * kCols; i += kThreads) {
+  for (int i = threadIdx.x; i < kStep * kCols; i += kPieceThreads) {
     const int t = i / kCols, j = i % kCols;
     float s = 0.f;
     if (t < c.n && j < r) {
@@ -134,14 +69,13 @@ __global__ void __launch_bounds__(kThreads) adapters_pieces_kernel(const float *
         const float *p = src + static_cast<size_t>(c.i0 + t) * r + j;
         const size_t next = static_cast<size_t>(M) * r;
         int k = 0;
-        for (; k + 8 <= shares; k += 8) {
-          float w[8];
+        for (; k < shares; k += 16) {   // sixteen under way
+          float w[16];
 #pragma unroll
-          for (int n = 0; n < 8; ++n) w[n] = p[(k + n) * next];
+          for (int n = 0; n < 16; ++n) w[n] = k + n < shares ? p[(k + n) * next] : 0.f;
 #pragma unroll
-          for (int n = 0; n < 8; ++n) s += w[n];
+          for (int n = 0; n < 16; ++n) s += w[n];
         }
-        for (; k < shares; ++k) s += p[k * next];
         s *= sa;
       }
     }
@@ -152,10 +86,10 @@ __global__ void __launch_bounds__(kThreads) adapters_pieces_kernel(const float *
   if (lane == 0) top[wave] = m;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, top[w]);
+  for (int w = 0; w < kPieceThreads / 64; ++w) m = fmaxf(m, top[w]);
   const Scale sc = scale_for<DT>(m);
   if (threadIdx.x == 0) out.over_back[c.step] = sc.back;
-  for (int g = wave; g < RF; g += kWaves) {
+  for (int g = wave; g < RF; g += kPieceThreads / 64) {
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = v[(8 * q + i) * kStride + 16 * g + col] * sc.to;
@@ -165,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) adapters_pieces_kernel(const float *
     for (int p = 0; p < kP; ++p) out.over[((static_cast<size_t>(c.step) * RF + g) * kP + p) * 64 + lane] = o[p];
   }
   if constexpr (!OF_H) {
-    for (int f = wave; f < 2; f += kWaves) {
+    for (int f = wave; f < 2; f += kPieceThreads / 64) {
       const int t = 16 * f + col;
       float w[RF][8], mt = 0.f;
 #pragma unroll
@@ -184,7 +118,10 @@ __global__ void __launch_bounds__(kThreads) adapters_pieces_kernel(const float *
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[k][i] *= st.to;
         split8<DT, 2>(w[k], o);
-        out.along[((static_cast<size_t>(c.step) * 2 + f) * RF + k) * 64 + lane] = q < 2 ? o[0] : o[1];
+        Oct mine;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine.w[i] = q < 2 ? o[0].w[i] : o[1].w[i];
+        out.along[((static_cast<size_t>(c.step) * 2 + f) * RF + k) * 64 + lane] = mine;
       }
     }
   }
@@ -198,30 +135,16 @@ struct Rows {
   uint32_t w[8][E / 2];
 };
 
-// Values E col .. of tokens 8 q + i of the step at list entry i0; end: columns there
-// are in all (past it zeros).
 template <int E>
-__device__ __forceinline__ void load_rows(Rows<E> &v, const uint16_t *__restrict__ x, const size_t row[8], int n, int end) {
+__device__ __forceinline__ void load_rows(Rows<E> &v, const uint16_t *__restrict__ x, const size_t row[8], int n) {
   struct __attribute__((packed, aligned(2))) Anywhere {
     uint32_t w[E / 2];
   };
-  if (n + E <= end) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const Anywhere a = *reinterpret_cast<const Anywhere *>(x + row[i] + n);
+  for (int i = 0; i < 8; ++i) {
+    const Anywhere a = *reinterpret_cast<const Anywhere *>(x + row[i] + n);
 #pragma unroll
-      for (int d = 0; d < E / 2; ++d) v.w[i][d] = a.w[d];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int d = 0; d < E / 2; ++d) {
-        uint32_t w = 0;
-        if (n + 2 * d < end) w = x[row[i] + n + 2 * d];
-        if (n + 2 * d + 1 < end) w |= static_cast<uint32_t>(x[row[i] + n + 2 * d + 1]) << 16;
-        v.w[i][d] = w;
-      }
+    for (int d = 0; d < E / 2; ++d) v.w[i][d] = a.w[d];
   }
 }
 
@@ -245,8 +168,6 @@ __device__ __forceinline__ void drop_rows(Rows<E> &v, int first, int n) {
     }
 }
 
-__device__ __forceinline__ int token_at(const int32_t *perm, int i, int M) { return min(max(perm[min(i, M - 1)], 0), M - 1); }
-
 // Sums of a chunk: v for (column n, value j) to the gradient [a][..] times scale, or to
 // the partial sums [slot][..].
 __device__ __forceinline__ void put(float *out, float *part, const Chunk &c, size_t size, size_t at, float v, float scale) {
@@ -267,9 +188,21 @@ __device__ __forceinline__ void clear(float *out, int r, int n0, int n1, size_t 
 
 // ------------------------------------------------------------------ dy: dB and u
 
-// Workgroup (chunk, slice): 16 E columns of dy a wavefront.
+// What a step reads, on its way while the step before is computed: dy's values once
+// by rows for the sums over tokens, once along them for u (from the caches).
 template <int DT, int E, int RF>
-__global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *__restrict__ dy, int M, int N, int r,
+struct DyStep {
+  Rows<E> x;
+  Oct a[2][E / 2], h[RF][kPieces<DT>];
+  float back;
+};
+
+// Workgroup (chunk, slice): 16 E columns of dy a wavefront. width: columns of a row
+// of dy, N or, where that is less, 8. A piece of columns that would reach past
+// the last starts earlier, so that every load is whole and none is in a branch;
+// what it has twice is not stored, or meets a zero of B.
+template <int DT, int E, int RF>
+__global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *__restrict__ dy, int width, int M, int N, int r,
                                                                const uint16_t *__restrict__ B,
                                                                const float *__restrict__ scales, int L,
                                                                const int32_t *__restrict__ offsets,
@@ -280,17 +213,17 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
   constexpr int kStride = 16 * RF + 1;
   __shared__ float red[2][kWaves][kStep * kStride];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  if (static_cast<int>(blockIdx.x) >= chunks) {
+  if (static_cast<int>(blockIdx.y) >= chunks) {
     int lo, hi;
-    const int a = blockIdx.x - chunks;
+    const int a = blockIdx.y - chunks;
     segment(offsets, a, M, lo, hi);
     if (lo == hi)
-      clear(dB + static_cast<size_t>(a) * N * r, r, blockIdx.y * kSlice, min(N, static_cast<int>(blockIdx.y + 1) * kSlice), r, 1);
+      clear(dB + static_cast<size_t>(a) * N * r, r, blockIdx.x * kSlice, min(N, static_cast<int>(blockIdx.x + 1) * kSlice), r, 1);
     return;
   }
-  const Chunk c = chunk_of(offsets, L, M, rows, max_steps, blockIdx.x);
+  const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
   if (c.a < 0) return;
-  const int n0 = blockIdx.y * kSlice + wave * kCols;
+  const int n0 = blockIdx.x * kSlice + wave * kCols;
   // B of these columns: value 16 g + col of columns n0 + 32 k + 8 q .. + 7
   Oct bv[kK][RF];
   const uint16_t *Ba = B + static_cast<size_t>(c.a) * N * r;
@@ -302,37 +235,36 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
       uint32_t e[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int n = n0 + 32 * k + 8 * q + i;
-        e[i] = n < N && j < r ? Ba[static_cast<size_t>(n) * r + j] : 0;
+        const int m = n0 + 32 * k + 8 * q, n = min(m, width - 8) + i;
+        e[i] = Ba[static_cast<size_t>(min(n, N - 1)) * r + min(j, r - 1)];
+        e[i] = n >= m && n < N && j < r ? e[i] : 0;
       }
 #pragma unroll
       for (int d = 0; d < 4; ++d) bv[k][g].w[d] = e[2 * d] | e[2 * d + 1] << 16;
     }
   float4_t acc[E][RF] = {};
   const int steps = (c.n + kStep - 1) / kStep;
-  for (int s = 0; s < steps; ++s) {
-    const int i0 = c.i0 + s * kStep, n = min(c.n - s * kStep, kStep);
+  auto load = [&](DyStep<DT, E, RF> &v, int s, int token) {
+    token = min(max(token, 0), M - 1);
     size_t row[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(token_at(perm, i0 + min(8 * q + i, n - 1), M)) * N;
-    Rows<E> v;
-    load_rows<E>(v, dy, row, n0 + E * col, N);
-    Oct a[2][kK];
+    for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(token, 8 * q + i)) * width;
+    load_rows<E>(v.x, dy, row, min(n0 + E * col, width - E));
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      const size_t at = static_cast<size_t>(token_at(perm, i0 + min(16 * f + col, n - 1), M)) * N;
+      const size_t at = static_cast<size_t>(__shfl(token, 16 * f + col)) * width;
 #pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        const int m = n0 + 32 * k + 8 * q;
-        a[f][k] = m + 8 <= N ? load_oct(dy + at + m) : load_oct_part(dy + at + m, N - m, 0);
-      }
+      for (int k = 0; k < kK; ++k) v.a[f][k] = load_oct(dy + at + min(n0 + 32 * k + 8 * q, width - 8));
     }
-    Oct hv[RF][kP];
     const size_t step = c.step + s;
 #pragma unroll
     for (int g = 0; g < RF; ++g)
 #pragma unroll
-      for (int p = 0; p < kP; ++p) hv[g][p] = h.over[((step * RF + g) * kP + p) * 64 + lane];
+      for (int p = 0; p < kP; ++p) v.h[g][p] = h.over[((step * RF + g) * kP + p) * 64 + lane];
+    v.back = DT == kF16 ? h.over_back[step] : 1.f;
+  };
+  auto compute = [&](DyStep<DT, E, RF> &v, int s) {
+    const int i0 = c.i0 + s * kStep, n = min(c.n - s * kStep, kStep);
     // this wavefront's share of u
     float *mine = red[s & 1][wave];
 #pragma unroll
@@ -341,41 +273,50 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
       for (int g = 0; g < RF; ++g) {
         float4_t d = {};
 #pragma unroll
-        for (int k = 0; k < kK; ++k) d = mfma<DT>(a[f][k], bv[k][g], d);
+        for (int k = 0; k < kK; ++k) d = mfma<DT>(v.a[f][k], bv[k][g], d);
 #pragma unroll
         for (int i = 0; i < 4; ++i) mine[(16 * f + 4 * q + i) * kStride + 16 * g + col] = d[i];
       }
-    if (n < kStep) drop_rows<E>(v, 8 * q, n);
-    const float back = DT == kF16 ? h.over_back[step] : 1.f;
+    if (n < kStep) drop_rows<E>(v.x, 8 * q, n);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const Oct x = column<E>(v, e);
+      const Oct x = column<E>(v.x, e);
 #pragma unroll
       for (int g = 0; g < RF; ++g) {
         if constexpr (DT == kF16) {
           float4_t d = {};
 #pragma unroll
-          for (int p = 0; p < kP; ++p) d = mfma<DT>(x, hv[g][p], d);
+          for (int p = 0; p < kP; ++p) d = mfma<DT>(x, v.h[g][p], d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[i], back, acc[e][g][i]);
+          for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[i], v.back, acc[e][g][i]);
         } else {
 #pragma unroll
-          for (int p = 0; p < kP; ++p) acc[e][g] = mfma<DT>(x, hv[g][p], acc[e][g]);
+          for (int p = 0; p < kP; ++p) acc[e][g] = mfma<DT>(x, v.h[g][p], acc[e][g]);
         }
       }
     }
     // the slice's share of u (the other half of `red` is written next, so one
-    // barrier a step is enough)
-    __syncthreads();
-    float *out = u_part + (static_cast<size_t>(blockIdx.y) * M + i0) * r;
-    for (int i = threadIdx.x; i < n * r; i += kThreads) {
-      const int t = i / r, j = i % r;
+    // barrier a step is enough; it orders LDS alone, and leaves the loads under way)
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    float *out = u_part + (static_cast<size_t>(blockIdx.x) * M + i0) * r;
+    for (int i = threadIdx.x; i < kStep * 16 * RF; i += kThreads) {
+      const int t = i / (16 * RF), j = i % (16 * RF);
       float sum = 0.f;
 #pragma unroll
       for (int w = 0; w < kWaves; ++w) sum += red[s & 1][w][t * kStride + j];
-      out[i] = sum;
+      if (t < n && j < r) out[t * r + j] = sum;
     }
-  }
+  };
+  int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
+  in_turn<DyStep<DT, E, RF>>(
+      steps,
+      [&](DyStep<DT, E, RF> &v, int s) {
+        load(v, s, token);
+        token = step_token(perm, c, kStep, s + 1);
+      },
+      compute);
   const float sa = scales[c.a];
 #pragma unroll
   for (int e = 0; e < E; ++e)
@@ -383,13 +324,22 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
     for (int g = 0; g < RF; ++g)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int n = n0 + E * (4 * q + i) + e, j = 16 * g + col;
-        if (n < N && j < r)
+        const int m = n0 + E * (4 * q + i), n = min(m, width - E) + e, j = 16 * g + col;
+        if (n >= m && n < N && j < r)
           put(dB, part, c, static_cast<size_t>(N) * r, static_cast<size_t>(n) * r + j, acc[e][g][i], sa);
       }
 }
 
 // ------------------------------------------------------------------ x: dA and dx
+
+template <int DT, int E, int RF>
+struct XStep {
+  Rows<E> x;
+  Oct base[2][E / 2], over[RF][kPieces<DT>], along[2][RF];
+  float back, token_back[2];
+  size_t at[2];
+  bool live[2];
+};
 
 template <int DT, int E, int RF>
 __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__restrict__ x, int M, int K, int r,
@@ -401,26 +351,20 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
                                                               float *__restrict__ dA, float *__restrict__ part) {
   constexpr int kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  const int s0 = blockIdx.y * kSlice, s1 = min(K, s0 + kSlice);
-  if (static_cast<int>(blockIdx.x) >= chunks + L) {   // 64 tokens: those without an adapter
-    const int t0 = (blockIdx.x - chunks - L) * 64;
-    int id = 0;
-    if (t0 + lane < M) id = ids[t0 + lane];
-    for (uint64_t left = __ballot(t0 + lane < M && (id < 0 || id >= L)); left; left &= left - 1) {
-      const size_t at = static_cast<size_t>(t0 + __builtin_ctzll(left)) * K;
-      for (int k = s0 + 8 * threadIdx.x; k < s1; k += 8 * kThreads)
-        store_oct(dx + at + k, base ? load_oct_aligned(base + at + k) : Oct{{0, 0, 0, 0}});
-    }
+  const int s0 = blockIdx.x * kSlice, s1 = min(K, s0 + kSlice);
+  if (static_cast<int>(blockIdx.y) >= chunks + L) {   // 64 tokens: those without an adapter
+    __shared__ int list[64];
+    copy_others<kThreads>(ids, (blockIdx.y - chunks - L) * 64, M, L, base, dx, K, s0, s1, list);
     return;
   }
-  if (static_cast<int>(blockIdx.x) >= chunks) {
+  if (static_cast<int>(blockIdx.y) >= chunks) {
     int lo, hi;
-    const int a = blockIdx.x - chunks;
+    const int a = blockIdx.y - chunks;
     segment(offsets, a, M, lo, hi);
     if (lo == hi) clear(dA + static_cast<size_t>(a) * r * K, r, s0, s1, 1, K);
     return;
   }
-  const Chunk c = chunk_of(offsets, L, M, rows, max_steps, blockIdx.x);
+  const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
   if (c.a < 0) return;
   const int k0 = s0 + wave * kCols;
   if (k0 >= K) return;   // K is a multiple of 128, kCols of 64: all or nothing
@@ -436,7 +380,7 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(min(j + i, r - 1)) * K;
       Rows<E> v;
-      load_rows<E>(v, Aa, row, k0 + E * col, K);
+      load_rows<E>(v, Aa, row, k0 + E * col);
       drop_rows<E>(v, j, r);
 #pragma unroll
       for (int e = 0; e < E; ++e) av[e][g] = column<E>(v, e);
@@ -444,52 +388,61 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
   }
   float4_t acc[E][RF] = {};
   const int steps = (c.n + kStep - 1) / kStep;
-  for (int s = 0; s < steps; ++s) {
-    const int i0 = c.i0 + s * kStep, n = min(c.n - s * kStep, kStep);
+  // dx: a lane holds columns k0 + 4 E q .. + 4 E - 1 of token 16 f + col
+  auto load = [&](XStep<DT, E, RF> &v, int s, int token) {
+    const int n = min(c.n - s * kStep, kStep);
     const size_t step = c.step + s;
+    const int safe = min(max(token, 0), M - 1);
     size_t row[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(token_at(perm, i0 + min(8 * q + i, n - 1), M)) * K;
-    Rows<E> v;
-    load_rows<E>(v, x, row, k0 + E * col, K);
-    // dx: a lane holds columns k0 + 4 E q .. + 4 E - 1 of token 16 f + col
-    Oct bv[2][E / 2];
-    size_t at[2];
-    bool live[2];
+    for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(safe, 8 * q + i)) * K;
+    load_rows<E>(v.x, x, row, k0 + E * col);
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
-      const int t = perm[i0 + min(16 * f + col, n - 1)];
-      live[f] = 16 * f + col < n && t >= 0 && t < M;
-      at[f] = static_cast<size_t>(live[f] ? t : 0) * K + k0 + 4 * E * q;
-#pragma unroll
-      for (int k = 0; k < E / 2; ++k)
-        bv[f][k] = base && live[f] ? load_oct_aligned(base + at[f] + 8 * k) : Oct{{0, 0, 0, 0}};
+      const int t = __shfl(token, 16 * f + col);
+      v.live[f] = 16 * f + col < n && t >= 0 && t < M;
+      v.at[f] = static_cast<size_t>(min(max(t, 0), M - 1)) * K + k0 + 4 * E * q;
     }
-    Oct uo[RF][kP], ua[2][RF];
+    if (base) {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) v.base[f][k] = load_oct_aligned(base + v.at[f] + 8 * k);
+    } else {
+#pragma unroll
+      for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int k = 0; k < E / 2; ++k) v.base[f][k] = Oct{{0, 0, 0, 0}};
+    }
 #pragma unroll
     for (int g = 0; g < RF; ++g)
 #pragma unroll
-      for (int p = 0; p < kP; ++p) uo[g][p] = u.over[((step * RF + g) * kP + p) * 64 + lane];
+      for (int p = 0; p < kP; ++p) v.over[g][p] = u.over[((step * RF + g) * kP + p) * 64 + lane];
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
-      for (int g = 0; g < RF; ++g) ua[f][g] = u.along[((step * 2 + f) * RF + g) * 64 + lane];
-    if (n < kStep) drop_rows<E>(v, 8 * q, n);
-    const float back = DT == kF16 ? u.over_back[step] : 1.f;
+      for (int g = 0; g < RF; ++g) v.along[f][g] = u.along[((step * 2 + f) * RF + g) * 64 + lane];
+    v.back = DT == kF16 ? u.over_back[step] : 1.f;
+#pragma unroll
+    for (int f = 0; f < 2; ++f) v.token_back[f] = DT == kF16 ? u.along_back[step * kStep + 16 * f + col] : 1.f;
+  };
+  auto compute = [&](XStep<DT, E, RF> &v, int s) {
+    const int n = min(c.n - s * kStep, kStep);
+    if (n < kStep) drop_rows<E>(v.x, 8 * q, n);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const Oct xv = column<E>(v, e);
+      const Oct xv = column<E>(v.x, e);
 #pragma unroll
       for (int g = 0; g < RF; ++g) {
         if constexpr (DT == kF16) {
           float4_t d = {};
 #pragma unroll
-          for (int p = 0; p < kP; ++p) d = mfma<DT>(uo[g][p], xv, d);
+          for (int p = 0; p < kP; ++p) d = mfma<DT>(v.over[g][p], xv, d);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[i], back, acc[e][g][i]);
+          for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[i], v.back, acc[e][g][i]);
         } else {
 #pragma unroll
-          for (int p = 0; p < kP; ++p) acc[e][g] = mfma<DT>(uo[g][p], xv, acc[e][g]);
+          for (int p = 0; p < kP; ++p) acc[e][g] = mfma<DT>(v.over[g][p], xv, acc[e][g]);
         }
       }
     }
@@ -499,24 +452,32 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
 #pragma unroll
       for (int e = 0; e < E; ++e)
 #pragma unroll
-        for (int g = 0; g < RF; ++g) d[e] = mfma<DT>(av[e][g], ua[f][g], d[e]);
-      const float tb = DT == kF16 ? u.along_back[step * kStep + 16 * f + col] : 1.f;
-      if (!live[f]) continue;
+        for (int g = 0; g < RF; ++g) d[e] = mfma<DT>(av[e][g], v.along[f][g], d[e]);
+      if (!v.live[f]) continue;
       // column 4 E q + E i + e is d[e][i]
+      const float tb = v.token_back[f];
 #pragma unroll
       for (int k = 0; k < E / 2; ++k) {
         Oct o;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const int c0 = 8 * k + 2 * w;
-          const uint32_t b = bv[f][k].w[w];
+          const uint32_t b = v.base[f][k].w[w];
           o.w[w] = pack2<DT>(fmaf(d[c0 % E][c0 / E], tb, to_f32<DT>(static_cast<uint16_t>(b))),
                              fmaf(d[(c0 + 1) % E][(c0 + 1) / E], tb, to_f32<DT>(static_cast<uint16_t>(b >> 16))));
         }
-        store_oct(dx + at[f] + 8 * k, o);
+        store_oct(dx + v.at[f] + 8 * k, o);
       }
     }
-  }
+  };
+  int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
+  in_turn<XStep<DT, E, RF>>(
+      steps,
+      [&](XStep<DT, E, RF> &v, int s) {
+        load(v, s, token);
+        token = step_token(perm, c, kStep, s + 1);
+      },
+      compute);
 #pragma unroll
   for (int g = 0; g < RF; ++g)
 #pragma unroll
@@ -557,11 +518,11 @@ constexpr size_t kAlign = 256;
 size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Plan {
-  int rf, e;
+  int rf, e_y, e_x;             // columns of a lane in the passes over dy and x
   int steps;                    // at most
   int rows_y, chunks_y, rows_x, chunks_x;
   int slices_y, slices_x;
-  size_t over, along, over_back, along_back, u_part, sums, total;   // where in the workspace
+  size_t over, along, over_back, along_back, u_part, sums, pad, total;   // where in the workspace
 };
 
 // Tokens of a chunk: as many workgroups as fill the card, and chunks long enough
@@ -576,10 +537,10 @@ Plan plan_of(const AdapterArgs &g) {
   Plan p{};
   const int frags = (g.r + 15) / 16;
   p.rf = frags <= 1 ? 1 : frags <= 2 ? 2 : frags <= 4 ? 4 : 8;
-  p.e = p.rf <= 2 ? 8 : 4;
-  const int slice = 16 * p.e * kWaves;
-  p.slices_y = (g.N + slice - 1) / slice;
-  p.slices_x = (g.K + slice - 1) / slice;
+  p.e_y = p.rf <= 1 ? 8 : 4;
+  p.e_x = 4;
+  p.slices_y = (g.N + 16 * p.e_y * kWaves - 1) / (16 * p.e_y * kWaves);
+  p.slices_x = (g.K + 16 * p.e_x * kWaves - 1) / (16 * p.e_x * kWaves);
   const int some = std::min(g.L, g.M);
   p.steps = g.M / kStep + some;
   p.rows_y = chunk_rows(g.M, p.slices_y);
@@ -601,11 +562,12 @@ Plan plan_of(const AdapterArgs &g) {
   const size_t sums_y = g.M > p.rows_y ? 2 * (static_cast<size_t>(g.M) / p.rows_y + 1) * g.N * g.r * 4 : 0;
   const size_t sums_x = g.M > p.rows_x ? 2 * (static_cast<size_t>(g.M) / p.rows_x + 1) * g.K * g.r * 4 : 0;
   p.sums = take(std::max(sums_y, sums_x));   // dB's are done with when dA's begin
+  p.pad = take(g.N < kNarrow ? static_cast<size_t>(g.M) * kNarrow * 2 : 0);
   p.total = at;
   return p;
 }
 
-template <int DT, int E, int RF>
+template <int DT, int EY, int EX, int RF>
 void backward_go(const AdapterArgs &g, const Plan &p, hipStream_t s) {
   uint8_t *ws = static_cast<uint8_t *>(g.scratch);
   const Pieces q{reinterpret_cast<Oct *>(ws + p.over), reinterpret_cast<Oct *>(ws + p.along),
@@ -620,17 +582,24 @@ void backward_go(const AdapterArgs &g, const Plan &p, hipStream_t s) {
     hipLaunchKernelGGL(adapters_sum_kernel, dim3(blocks, g.L), block, 0, s, sums, size, g.M, scales, g.offsets, rows, out);
   };
   if (p.steps > 0)
-    hipLaunchKernelGGL((adapters_pieces_kernel<DT, RF, true>), dim3(p.steps), block, 0, s, g.h, 1, g.M, g.r, g.scales,
+    hipLaunchKernelGGL((adapters_pieces_kernel<DT, RF, true>), dim3(p.steps), dim3(kPieceThreads), 0, s, g.h, 1, g.M, g.r, g.scales,
                        g.L, g.offsets, g.perm, q);
-  hipLaunchKernelGGL((adapters_dy_kernel<DT, E, RF>), dim3(p.chunks_y + g.L, p.slices_y), block, 0, s,
-                     static_cast<const uint16_t *>(g.dy), g.M, g.N, g.r, b, g.scales, g.L, g.offsets, g.perm, p.rows_y,
+  const uint16_t *dy = static_cast<const uint16_t *>(g.dy);
+  if (g.M > 0 && g.N < kNarrow) {
+    uint16_t *pad = reinterpret_cast<uint16_t *>(ws + p.pad);
+    hipLaunchKernelGGL(adapters_pad_kernel<kThreads>, dim3((g.M * kNarrow + kThreads - 1) / kThreads), block, 0, s, dy,
+                       g.M, g.N, pad);
+    dy = pad;
+  }
+  hipLaunchKernelGGL((adapters_dy_kernel<DT, EY, RF>), dim3(p.slices_y, p.chunks_y + g.L), block, 0, s, dy,
+                     std::max(g.N, kNarrow), g.M, g.N, g.r, b, g.scales, g.L, g.offsets, g.perm, p.rows_y,
                      p.chunks_y, p.steps, q, u_part, g.d_b, sums);
   if (g.M > p.rows_y) sum(static_cast<size_t>(g.N) * g.r, g.scales, p.rows_y, g.d_b);
   if (p.steps > 0)
-    hipLaunchKernelGGL((adapters_pieces_kernel<DT, RF, false>), dim3(p.steps), block, 0, s, u_part, p.slices_y, g.M, g.r,
+    hipLaunchKernelGGL((adapters_pieces_kernel<DT, RF, false>), dim3(p.steps), dim3(kPieceThreads), 0, s, u_part, p.slices_y, g.M, g.r,
                        g.scales, g.L, g.offsets, g.perm, q);
   const int others = base == dx ? 0 : (g.M + 63) / 64;
-  hipLaunchKernelGGL((adapters_x_kernel<DT, E, RF>), dim3(p.chunks_x + g.L + others, p.slices_x), block, 0, s,
+  hipLaunchKernelGGL((adapters_x_kernel<DT, EX, RF>), dim3(p.slices_x, p.chunks_x + g.L + others), block, 0, s,
                      static_cast<const uint16_t *>(g.x), g.M, g.K, g.r, a, g.L, g.ids, g.offsets, g.perm, p.rows_x,
                      p.chunks_x, p.steps, q, base, dx, g.d_a, sums);
   if (g.M > p.rows_x) sum(static_cast<size_t>(g.K) * g.r, nullptr, p.rows_x, g.d_a);
@@ -638,10 +607,10 @@ void backward_go(const AdapterArgs &g, const Plan &p, hipStream_t s) {
 
 template <int DT>
 void backward_ranks(const AdapterArgs &g, const Plan &p, hipStream_t s) {
-  if (p.rf == 1) backward_go<DT, 8, 1>(g, p, s);
-  else if (p.rf == 2) backward_go<DT, 8, 2>(g, p, s);
-  else if (p.rf == 4) backward_go<DT, 4, 4>(g, p, s);
-  else backward_go<DT, 4, 8>(g, p, s);
+  if (p.rf == 1) backward_go<DT, 8, 4, 1>(g, p, s);
+  else if (p.rf == 2) backward_go<DT, 4, 4, 2>(g, p, s);
+  else if (p.rf == 4) backward_go<DT, 4, 4, 4>(g, p, s);
+  else backward_go<DT, 4, 4, 8>(g, p, s);
 }
 
 }  // namespace
