@@ -85,6 +85,78 @@ __device__ __forceinline__ Scale scale_for(float m) {
   return {__uint_as_float(static_cast<uint32_t>(127 + e) << 23), __uint_as_float(static_cast<uint32_t>(127 - e) << 23)};
 }
 
+// E neighbouring values of R rows: eight (16 bytes) or four. Sixteen lanes hold 16 E
+// neighbours of a row, so that a load's neighbouring lanes read neighbouring bytes:
+// where they read different rows, as an operand's lanes do, the cache looks up 64
+// places for the load and not 16 (470 MB through such loads and stores 111 us,
+// 92 through a copy).
+template <int E, int R = 8>
+struct Rows {
+  uint32_t w[R][E / 2];
+};
+
+template <int E, int R>
+__device__ __forceinline__ void load_rows(Rows<E, R> &v, const uint16_t *x, const size_t (&row)[R], int n) {
+  struct __attribute__((packed, aligned(2))) Anywhere {
+    uint32_t w[E / 2];
+  };
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const Anywhere a = *reinterpret_cast<const Anywhere *>(x + row[i] + n);
+#pragma unroll
+    for (int d = 0; d < E / 2; ++d) v.w[i][d] = a.w[d];
+  }
+}
+
+// Column e of the eight rows.
+template <int E>
+__device__ __forceinline__ Oct column(const Rows<E> &v, int e) {
+  const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+  Oct o;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) o.w[d] = __builtin_amdgcn_perm(v.w[2 * d + 1][e / 2], v.w[2 * d][e / 2], sel);
+  return o;
+}
+
+template <int E>
+__device__ __forceinline__ void drop_rows(Rows<E> &v, int first, int n) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (first + i >= n) {
+#pragma unroll
+      for (int d = 0; d < E / 2; ++d) v.w[i][d] = 0;
+    }
+}
+
+// out[row][n0 + E col ..] = base + back (P Q^T) for R = 4 tokens of a lane: d[e][i] is
+// column e of token i. own: the first of the E columns that are this lane's and not
+// its neighbour's (a piece that would reach past the last column starts earlier).
+template <int DT, int E>
+__device__ __forceinline__ void add_rows(uint16_t *out, const size_t (&row)[4], const bool (&live)[4], int n, int own,
+                                         int end, const float4_t (&d)[E], const float4_t &back, const Rows<E, 4> &base) {
+  struct __attribute__((packed, aligned(2))) Anywhere {
+    uint32_t w[E / 2];
+  };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (!live[i]) continue;
+    Anywhere o;
+#pragma unroll
+    for (int w = 0; w < E / 2; ++w) {
+      const uint32_t b = base.w[i][w];
+      o.w[w] = pack2<DT>(fmaf(d[2 * w][i], back[i], to_f32<DT>(static_cast<uint16_t>(b))),
+                         fmaf(d[2 * w + 1][i], back[i], to_f32<DT>(static_cast<uint16_t>(b >> 16))));
+    }
+    if (n + own + E <= end) {
+      *reinterpret_cast<Anywhere *>(out + row[i] + n) = o;
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (e >= own && n + e < end) out[row[i] + n + e] = static_cast<uint16_t>(o.w[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
 // Tile number b of `rows` list entries each, adapter after adapter: its adapter
 // (-1: past the last), first entry and count. One wavefront's lanes share the
 // adapters; every lane gets the answer. Bad offsets give entries in [0, M) all

@@ -57,60 +57,89 @@ __device__ __forceinline__ void pieces_of(const float *row, int r, int q, Oct (&
 
 // ------------------------------------------------------------------ x A^T
 
-// 32 S values of a lane's rows, on their way while the block before is multiplied.
-template <int TF, int RF, int S>
-struct Block {
-  Oct x[TF][S], w[RF][S];
-  __device__ __forceinline__ void load(const uint16_t *const (&xr)[TF], const uint16_t *const (&wr)[RF], int b) {
+// 32 S values of 16 F rows on their way from memory through registers and LDS into
+// operands: neighbouring lanes read neighbouring bytes (see Rows), which operands
+// straight from memory do not. A row's 16-byte pieces lie in an order that keeps
+// the banks apart.
+template <int F, int S>
+struct Staged {
+  static constexpr int kPer = 4 * S, kRows = 64 / kPer, kLoads = 16 * F / kRows;   // pieces of a row, rows of a load
+  Oct v[kLoads];
+  template <class ROW>
+  __device__ __forceinline__ void load(ROW row, int b) {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-    for (int f = 0; f < TF; ++f)
+    for (int i = 0; i < kLoads; ++i) v[i] = load_oct_aligned(row(i) + 32 * S * b + 8 * (lane % kPer));
+  }
+  __device__ __forceinline__ void lay(uint16_t *lds) const {
+    const int lane = threadIdx.x & 63;
 #pragma unroll
-      for (int i = 0; i < S; ++i) x[f][i] = load_oct_aligned(xr[f] + 32 * (S * b + i));
-#pragma unroll
-    for (int f = 0; f < RF; ++f)
-#pragma unroll
-      for (int i = 0; i < S; ++i) w[f][i] = load_oct_aligned(wr[f] + 32 * (S * b + i));
+    for (int i = 0; i < kLoads; ++i) {
+      const int t = kRows * i + lane / kPer;
+      *reinterpret_cast<uint4 *>(lds + (t * kPer + ((lane % kPer) ^ (t % kPer))) * 8) =
+          make_uint4(v[i].w[0], v[i].w[1], v[i].w[2], v[i].w[3]);
+    }
+  }
+  static __device__ __forceinline__ Oct operand(const uint16_t *lds, int f, int s) {
+    const int lane = threadIdx.x & 63, t = 16 * f + (lane & 15);
+    return load_oct_aligned(lds + (t * kPer + ((4 * s + (lane >> 4)) ^ (t % kPer))) * 8);
   }
 };
 
 // The sums over blocks lo + wave, lo + wave + WAVES, .. below hi of a tile of up to
-// 16 TF tokens and 16 RF values.
-//
-// Both operands are contiguous along k, so they go from memory into the matrix
-// instruction as they are. Rows and values past the last are copies of the last
-// (their results are dropped), so nothing is masked.
+// 16 TF tokens and 16 RF values. Rows and values past the last are copies of the
+// last (their results are dropped), so nothing is masked.
+template <int TF, int RF, int S>
+constexpr int kStage = (TF + RF) * 16 * 32 * S;   // LDS values of a wavefront
 template <int DT, int TF, int RF, int S, int WAVES, bool BY_TOKEN>
 __device__ __forceinline__ void shrink(const uint16_t *__restrict__ x, int M, int K, int r,
                                        const uint16_t *__restrict__ A, const int32_t *__restrict__ perm,
-                                       const Tile &tile, int lo, int hi, float4_t (&acc)[TF][RF]) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
-  const uint16_t *xr[TF], *wr[RF];
+                                       const Tile &tile, int lo, int hi, uint16_t *lds, float4_t (&acc)[TF][RF]) {
+  using X = Staged<TF, S>;
+  using W = Staged<RF, S>;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint16_t *xr[X::kLoads];
 #pragma unroll
-  for (int f = 0; f < TF; ++f) {
-    int t = tile.i0 + min(16 * f + col, tile.n - 1);
+  for (int i = 0; i < X::kLoads; ++i) {
+    int t = tile.i0 + min(X::kRows * i + lane / X::kPer, tile.n - 1);
     if constexpr (!BY_TOKEN) t = min(max(perm[t], 0), M - 1);
-    xr[f] = x + static_cast<size_t>(t) * K + 8 * q;
+    xr[i] = x + static_cast<size_t>(t) * K;
   }
-#pragma unroll
-  for (int f = 0; f < RF; ++f)
-    wr[f] = A + (static_cast<size_t>(tile.a) * r + min(16 * f + col, r - 1)) * K + 8 * q;
+  const uint16_t *Aa = A + static_cast<size_t>(tile.a) * r * K;
+  uint16_t *xl = lds + wave * kStage<TF, RF, S>, *wl = xl + TF * 16 * 32 * S;
 #pragma unroll
   for (int f = 0; f < TF; ++f)
 #pragma unroll
     for (int g = 0; g < RF; ++g) acc[f][g] = float4_t{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const Block<TF, RF, S> &v) {
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-#pragma unroll
-      for (int f = 0; f < TF; ++f)
-#pragma unroll
-        for (int g = 0; g < RF; ++g) acc[f][g] = mfma<DT>(v.x[f][i], v.w[g][i], acc[f][g]);
+  struct Block {
+    X x;
+    W w;
   };
   const int count = (hi - lo - wave + WAVES - 1) / WAVES;
-  if (count > 0)
-    in_turn<Block<TF, RF, S>>(
-        count, [&](Block<TF, RF, S> &v, int i) { v.load(xr, wr, lo + wave + i * WAVES); },
-        [&](const Block<TF, RF, S> &v, int) { multiply(v); });
+  if (count <= 0) return;
+  in_turn<Block>(
+      count,
+      [&](Block &v, int i) {
+        const int b = lo + wave + i * WAVES;
+        v.x.load([&](int n) { return xr[n]; }, b);
+        v.w.load([&](int n) { return Aa + static_cast<size_t>(min(W::kRows * n + lane / W::kPer, r - 1)) * K; }, b);
+      },
+      [&](const Block &v, int) {
+        v.x.lay(xl);
+        v.w.lay(wl);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+          Oct a[TF];
+#pragma unroll
+          for (int f = 0; f < TF; ++f) a[f] = X::operand(xl, f, s);
+#pragma unroll
+          for (int g = 0; g < RF; ++g) {
+            const Oct w = W::operand(wl, g, s);
+#pragma unroll
+            for (int f = 0; f < TF; ++f) acc[f][g] = mfma<DT>(a[f], w, acc[f][g]);
+          }
+        }
+      });
 }
 
 // The waves' sums added up; value j of token t to put(t, j, v).
@@ -142,16 +171,20 @@ __global__ void __launch_bounds__(kThreads) adapters_shares_kernel(const uint16_
                                                                    const int32_t *__restrict__ offsets,
                                                                    const int32_t *__restrict__ perm,
                                                                    float *__restrict__ part) {
-  __shared__ float4_t red[kWaves * RF * 64];
+  constexpr int kS = RF == 8 ? 2 : 4;
+  constexpr size_t kLds = std::max(sizeof(float4_t) * kWaves * RF * 64, sizeof(uint16_t) * kWaves * kStage<1, RF, kS>);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   Tile tile;
   if constexpr (BY_TOKEN) tile = {adapter_of(ids, blockIdx.x, L), static_cast<int>(blockIdx.x), 1};
   else tile = tile_of(offsets, L, M, 16, blockIdx.x);
   if (tile.a < 0) return;
-  const int blocks = K / 128, splits = gridDim.y;
+  const int blocks = K / (32 * kS), splits = gridDim.y;
   const int lo = static_cast<int>(static_cast<long>(blocks) * blockIdx.y / splits);
   const int hi = static_cast<int>(static_cast<long>(blocks) * (blockIdx.y + 1) / splits);
   float4_t acc[1][RF];
-  shrink<DT, 1, RF, 4, kWaves, BY_TOKEN>(x, M, K, r, A, perm, tile, lo, hi, acc);
+  shrink<DT, 1, RF, kS, kWaves, BY_TOKEN>(x, M, K, r, A, perm, tile, lo, hi, reinterpret_cast<uint16_t *>(lds), acc);
+  __syncthreads();
+  float4_t *red = reinterpret_cast<float4_t *>(lds);
   float *out = part + (static_cast<size_t>(blockIdx.y) * M + tile.i0) * r;
   join<1, RF, kWaves>(acc, red, [&](int t, int j, float v) {
     if (t < tile.n && j < r) out[static_cast<size_t>(t) * r + j] = v;
@@ -170,13 +203,16 @@ __global__ void __launch_bounds__(kManyThreads) adapters_h_kernel(const uint16_t
                                                                   const int32_t *__restrict__ perm,
                                                                   Oct *__restrict__ pieces, float *__restrict__ back,
                                                                   float *__restrict__ h) {
-  constexpr int kW = kManyThreads / 64, kStride = 16 * RF + 4, kS = RF == 8 ? 2 : 4;
-  __shared__ float4_t red[kW * TF * RF * 64];
+  constexpr int kW = kManyThreads / 64, kStride = 16 * RF + 4, kS = RF >= 4 ? 2 : 4;
+  constexpr size_t kLds = std::max(sizeof(float4_t) * kW * TF * RF * 64, sizeof(uint16_t) * kW * kStage<TF, RF, kS>);
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
   __shared__ float hs[16 * TF * kStride];
   const Tile tile = tile_of(offsets, L, M, 16 * TF, blockIdx.x);
   if (tile.a < 0) return;
   float4_t acc[TF][RF];
-  shrink<DT, TF, RF, kS, kW, false>(x, M, K, r, A, perm, tile, 0, K / (32 * kS), acc);
+  shrink<DT, TF, RF, kS, kW, false>(x, M, K, r, A, perm, tile, 0, K / (32 * kS), reinterpret_cast<uint16_t *>(lds), acc);
+  __syncthreads();
+  float4_t *red = reinterpret_cast<float4_t *>(lds);
   join<TF, RF, kW>(acc, red, [&](int t, int j, float v) { hs[t * kStride + j] = t < tile.n && j < r ? v : 0.f; });
   __syncthreads();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -216,31 +252,25 @@ constexpr int kSpan = 64 * kWaves, kMostShares = 16;
 // RANK: kWhole, r a multiple of 8; kMore, above 8; kLess, below (single loads).
 enum { kWhole, kMore, kLess };
 
-// B_a's values for the columns n0 .. n0 + 63: instruction 2 k + m's operand rows.
+// A row of B as an operand's share: values from 16 c + 8 (q % 2) on.
 template <int RC, int RANK>
-__device__ __forceinline__ void load_weights(Oct (&b)[4][RC], const uint16_t *__restrict__ Ba, int n0, int N, int width,
-                                             int r) {
-  const int lane = threadIdx.x & 63, col = lane & 15, q = lane >> 4;
+__device__ __forceinline__ void load_weights(Oct (&b)[RC], const uint16_t *__restrict__ row, int r) {
+  const int q = threadIdx.x >> 4 & 3;
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    const int n = min(min(n0 + 32 * (m >> 1) + 8 * (col >> 2), width - 8) + 4 * (m & 1) + (col & 3), N - 1);
-    const uint16_t *p = Ba + static_cast<size_t>(n) * r;
+  for (int c = 0; c < RC; ++c) {
+    const int j = 16 * c + 8 * (q & 1);
+    if constexpr (RANK == kLess) {
+      uint32_t e[8];
 #pragma unroll
-    for (int c = 0; c < RC; ++c) {
-      const int j = 16 * c + 8 * (q & 1);
-      if constexpr (RANK == kLess) {
-        uint32_t e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          e[i] = p[min(j + i, r - 1)];
-          e[i] = j + i < r ? e[i] : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) b[m][c].w[i] = e[2 * i] | e[2 * i + 1] << 16;
-      } else {
-        // (past r all of h's values are zeros, and B's from here its own)
-        b[m][c] = load_oct(p + min(j, r - 8));
+      for (int i = 0; i < 8; ++i) {
+        e[i] = row[min(j + i, r - 1)];
+        e[i] = j + i < r ? e[i] : 0;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[c].w[i] = e[2 * i] | e[2 * i + 1] << 16;
+    } else {
+      // (past r all of h's values are zeros, and B's from here its own)
+      b[c] = load_oct(row + min(j, r - 8));
     }
   }
 }
@@ -367,7 +397,11 @@ __global__ void __launch_bounds__(kThreads) adapters_few_kernel(
     in_turn<Step>(
         count,
         [&](Step &v, int s) {
-          load_weights<RC, RANK>(v.b, Ba, n0 + s * kSpan, N, width, r);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const int n = min(n0 + s * kSpan + 32 * (m >> 1) + 8 * (col >> 2), width - 8) + 4 * (m & 1) + (col & 3);
+            load_weights<RC, RANK>(v.b[m], Ba + static_cast<size_t>(min(n, N - 1)) * r, r);
+          }
           load_base(v.y, base ? rows_of_base : nullptr, row, n0 + s * kSpan, width);
         },
         [&](const Step &v, int s) {
@@ -375,53 +409,79 @@ __global__ void __launch_bounds__(kThreads) adapters_few_kernel(
         });
 }
 
-// Many tokens: a workgroup takes kSpan columns, whose part of B stays in registers,
-// and goes through a chunk of an adapter's tokens, 16 TF a step.
-template <int DT, int TF, int RC, int RANK>
+// Many tokens: a wavefront takes 16 E columns, whose part of B stays in registers,
+// and goes through a chunk of an adapter's tokens, 16 TF a step. D's rows are tokens,
+// so that a lane holds E neighbouring columns of four of them. UNIT: tokens of the
+// tiles in which h's operands were made.
+template <int DT, int E, int TF, int RC, int RANK>
 __global__ void __launch_bounds__(kThreads) adapters_y_kernel(
-    const Oct *__restrict__ pieces, const float *__restrict__ backs, int M, int N, int r,
+    const Oct *__restrict__ pieces, const float *__restrict__ backs, int unit, int M, int N, int r,
     const uint16_t *__restrict__ B, const float *__restrict__ scales, int L, const int32_t *__restrict__ ids,
     const int32_t *__restrict__ offsets, const int32_t *__restrict__ perm, const uint16_t *base,
     const uint16_t *rows_of_base, uint16_t *y, float *__restrict__ h, int rows, int chunks, int max_steps) {
-  constexpr int kUnit = 16 * TF;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15;
-  const int from = blockIdx.x * kSpan, end = min(from + kSpan, N);
+  constexpr int kStep = 16 * TF, kColumns = 16 * E;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
+  const int from = blockIdx.x * kColumns * kWaves;
   if (static_cast<int>(blockIdx.y) >= chunks)
-    return others(ids, (blockIdx.y - chunks) * 64, M, L, N, r, base, y, h, from, end);
-  const Chunk c = chunk_of(offsets, L, M, rows, kUnit, max_steps, blockIdx.y);
-  const int n0 = from + 64 * wave;
+    return others(ids, (blockIdx.y - chunks) * 64, M, L, N, r, base, y, h, from, min(from + kColumns * kWaves, N));
+  const Chunk c = chunk_of(offsets, L, M, rows, unit, max_steps, blockIdx.y);
+  const int n0 = from + kColumns * wave;
   if (c.a < 0 || n0 >= N) return;
   const int width = max(N, kNarrow);   // columns of a row of rows_of_base
-  Oct b[4][RC];
-  load_weights<RC, RANK>(b, B + static_cast<size_t>(c.a) * N * r, n0, N, width, r);
+  // columns n .. n + E - 1, of which those from n + own on are this lane's
+  const int n = min(n0 + E * col, width - E), own = n0 + E * col - n;
+  Oct b[E][RC];
+#pragma unroll
+  for (int e = 0; e < E; ++e) load_weights<RC, RANK>(b[e], B + (static_cast<size_t>(c.a) * N + min(n + e, N - 1)) * r, r);
   const float sa = scales[c.a];
   struct Step {
-    Oct h[TF][RC], y[TF][2];
-    float back[TF];
-    size_t row[TF];
-    bool live[TF];
+    Oct h[TF][RC];
+    Rows<E, 4> y[TF];
+    float4_t back[TF];
+    int token;   // as step_token gives them
   };
-  int token = step_token(perm, c, kUnit, 0);   // of the step whose loads come next
+  int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
   in_turn<Step>(
-      (c.n + kUnit - 1) / kUnit,
+      (c.n + kStep - 1) / kStep,
       [&](Step &v, int s) {
+        v.token = token;
+        const int safe = min(max(token, 0), M - 1);
 #pragma unroll
         for (int f = 0; f < TF; ++f) {
-          const int t = __shfl(token, 16 * f + col);
-          const size_t at = static_cast<size_t>(c.step + s) * TF + f;
-          v.live[f] = s * kUnit + 16 * f + col < c.n && t >= 0 && t < M;
-          v.row[f] = static_cast<size_t>(min(max(t, 0), M - 1));
-          load_base(v.y[f], base ? rows_of_base : nullptr, v.row[f], n0, width);
-          v.back[f] = backs[16 * at + col];
+          // (a chunk's steps are whole but for the last, whose second half may be none)
+          const size_t at = static_cast<size_t>(c.step) * (unit / 16) + min(s * TF + f, (c.n - 1) / 16);
+          if (base) {
+            size_t row[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) row[i] = static_cast<size_t>(__shfl(safe, 16 * f + 4 * q + i)) * width;
+            load_rows(v.y[f], rows_of_base, row, n);
+          } else {
+            v.y[f] = Rows<E, 4>{};
+          }
+          v.back[f] = *reinterpret_cast<const float4_t *>(backs + 16 * at + 4 * q);
 #pragma unroll
           for (int k = 0; k < RC; ++k) v.h[f][k] = pieces[(at * RC + k) * 64 + lane];
         }
-        token = step_token(perm, c, kUnit, s + 1);
+        token = step_token(perm, c, kStep, s + 1);
       },
-      [&](const Step &v, int) {
+      [&](const Step &v, int s) {
 #pragma unroll
-        for (int f = 0; f < TF; ++f)
-          add_product<DT, RC>(b, v.h[f], v.back[f] * sa, v.y[f], y + v.row[f] * N, v.live[f], n0, N, width);
+        for (int f = 0; f < TF; ++f) {
+          float4_t d[E] = {};
+#pragma unroll
+          for (int k = 0; k < RC; ++k)
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = mfma<DT>(v.h[f][k], b[e][k], d[e]);
+          size_t row[4];
+          bool live[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = 16 * f + 4 * q + i, to = __shfl(v.token, t);
+            live[i] = s * kStep + t < c.n && to >= 0 && to < M;
+            row[i] = static_cast<size_t>(max(to, 0)) * N;
+          }
+          add_rows<DT, E>(y, row, live, n, own, N, d, v.back[f] * sa, v.y[f]);
+        }
       });
 }
 
@@ -431,6 +491,7 @@ __global__ void __launch_bounds__(kThreads) adapters_y_kernel(
 struct ForwardPlan {
   bool few, by_token;
   int tf, rf;           // 16-token and 16-value pieces of a tile
+  int e;                // many tokens: columns of a lane
   int tiles;            // at most
   int splits;           // shares of K
   int steps;            // kSpan-column steps of a workgroup
@@ -450,12 +511,13 @@ ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
   p.tf = p.few || g.M / some <= 16 || p.rf == 8 ? 1 : 2;
   const int unit = 16 * p.tf, spans = (g.N + kSpan - 1) / kSpan;
   p.tiles = p.few && p.by_token ? g.M : g.M / unit + some;
+  p.e = p.rf <= 2 ? 8 : 4;
   if (p.few) {
     // (the same with and without an order: so is the result)
     p.splits = std::max(1, std::min({512 / std::max(1, g.M), (g.K / 128 + kWaves - 1) / kWaves, kMostShares}));
     p.steps = std::max(1, std::min(8, static_cast<int>(static_cast<long>(spans) * g.M / 512)));
   } else {
-    const long rows = static_cast<long>(g.M) * spans / 2048;
+    const long rows = static_cast<long>(g.M) * ((g.N + 64 * p.e - 1) / (64 * p.e)) / 1024;
     p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, 128l), 1024l));
     p.chunks = g.M / p.rows + some;
   }
@@ -511,15 +573,16 @@ void forward_rank(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
   auto go = [&](auto first, auto second) {
     hipLaunchKernelGGL(first, dim3(p.tiles), dim3(kManyThreads), 0, s, x, g.M, g.K, g.r, a, g.L, g.offsets, g.perm,
                        pieces, back, g.h);
-    hipLaunchKernelGGL(second, dim3(spans, p.chunks + rest), block, 0, s, pieces, back, g.M, g.N, g.r, b, g.scales, g.L,
-                       g.ids, g.offsets, g.perm, base, wide, y, g.h, p.rows, p.chunks, p.tiles);
+    hipLaunchKernelGGL(second, dim3((g.N + 64 * p.e - 1) / (64 * p.e), p.chunks + rest), block, 0, s, pieces, back,
+                       16 * p.tf, g.M, g.N, g.r, b, g.scales, g.L, g.ids, g.offsets, g.perm, base, wide, y, g.h, p.rows,
+                       p.chunks, p.tiles);
   };
   auto pick = [&](auto tf) {
-    constexpr int kTF = decltype(tf)::value;
-    auto first = adapters_h_kernel<DT, kTF, RC>;
-    if (rank == kWhole) go(first, adapters_y_kernel<DT, kTF, RC, kWhole>);
-    else if (rank == kMore) go(first, adapters_y_kernel<DT, kTF, RC, kMore>);
-    else if constexpr (RC == 1) go(first, adapters_y_kernel<DT, kTF, RC, kLess>);
+    constexpr int kTF = RC <= 1 ? decltype(tf)::value : 1, kE = RC <= 2 ? 8 : 4;
+    auto first = adapters_h_kernel<DT, decltype(tf)::value, RC>;
+    if (rank == kWhole) go(first, adapters_y_kernel<DT, kE, kTF, RC, kWhole>);
+    else if (rank == kMore) go(first, adapters_y_kernel<DT, kE, kTF, RC, kMore>);
+    else if constexpr (RC == 1) go(first, adapters_y_kernel<DT, kE, kTF, RC, kLess>);
   };
   if constexpr (RC < 8) {
     if (p.tf == 2) return pick(std::integral_constant<int, 2>{});

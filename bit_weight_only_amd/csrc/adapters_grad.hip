@@ -127,47 +127,6 @@ __global__ void __launch_bounds__(kPieceThreads) adapters_pieces_kernel(const fl
   }
 }
 
-// ------------------------------------------------------------------ rows of dy and x
-
-// E neighbouring values of eight rows: eight (16 bytes) or four.
-template <int E>
-struct Rows {
-  uint32_t w[8][E / 2];
-};
-
-template <int E>
-__device__ __forceinline__ void load_rows(Rows<E> &v, const uint16_t *__restrict__ x, const size_t row[8], int n) {
-  struct __attribute__((packed, aligned(2))) Anywhere {
-    uint32_t w[E / 2];
-  };
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const Anywhere a = *reinterpret_cast<const Anywhere *>(x + row[i] + n);
-#pragma unroll
-    for (int d = 0; d < E / 2; ++d) v.w[i][d] = a.w[d];
-  }
-}
-
-// Column e of the eight rows.
-template <int E>
-__device__ __forceinline__ Oct column(const Rows<E> &v, int e) {
-  const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
-  Oct o;
-#pragma unroll
-  for (int d = 0; d < 4; ++d) o.w[d] = __builtin_amdgcn_perm(v.w[2 * d + 1][e / 2], v.w[2 * d][e / 2], sel);
-  return o;
-}
-
-template <int E>
-__device__ __forceinline__ void drop_rows(Rows<E> &v, int first, int n) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (first + i >= n) {
-#pragma unroll
-      for (int d = 0; d < E / 2; ++d) v.w[i][d] = 0;
-    }
-}
-
 // Sums of a chunk: v for (column n, value j) to the gradient [a][..] times scale, or to
 // the partial sums [slot][..].
 __device__ __forceinline__ void put(float *out, float *part, const Chunk &c, size_t size, size_t at, float v, float scale) {
@@ -188,12 +147,12 @@ __device__ __forceinline__ void clear(float *out, int r, int n0, int n1, size_t 
 
 // ------------------------------------------------------------------ dy: dB and u
 
-// What a step reads, on its way while the step before is computed: dy's values once
-// by rows for the sums over tokens, once along them for u (from the caches).
+// What a step reads, on its way while the step before is computed. dy's values lie
+// by rows for the sums over tokens; for u they go through LDS.
 template <int DT, int E, int RF>
 struct DyStep {
   Rows<E> x;
-  Oct a[2][E / 2], h[RF][kPieces<DT>];
+  Oct h[RF][kPieces<DT>];
   float back;
 };
 
@@ -212,6 +171,7 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
   constexpr int kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves, kK = kCols / 32;
   constexpr int kStride = 16 * RF + 1;
   __shared__ float red[2][kWaves][kStep * kStride];
+  __shared__ __attribute__((aligned(16))) uint16_t tile[kWaves][kStep * kCols];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   if (static_cast<int>(blockIdx.y) >= chunks) {
     int lo, hi;
@@ -224,7 +184,8 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
   const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
   if (c.a < 0) return;
   const int n0 = blockIdx.x * kSlice + wave * kCols;
-  // B of these columns: value 16 g + col of columns n0 + 32 k + 8 q .. + 7
+  // B of these columns: value 16 g + col of the columns that lie at 32 k + 8 q .. + 7 of
+  // a row in LDS, zero for those that lie there twice or are none
   Oct bv[kK][RF];
   const uint16_t *Ba = B + static_cast<size_t>(c.a) * N * r;
 #pragma unroll
@@ -235,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
       uint32_t e[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int m = n0 + 32 * k + 8 * q, n = min(m, width - 8) + i;
+        const int at = 32 * k + 8 * q + i, m = n0 + at / E * E, n = min(m, width - E) + at % E;
         e[i] = Ba[static_cast<size_t>(min(n, N - 1)) * r + min(j, r - 1)];
         e[i] = n >= m && n < N && j < r ? e[i] : 0;
       }
@@ -249,13 +210,7 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
     size_t row[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(token, 8 * q + i)) * width;
-    load_rows<E>(v.x, dy, row, min(n0 + E * col, width - E));
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const size_t at = static_cast<size_t>(__shfl(token, 16 * f + col)) * width;
-#pragma unroll
-      for (int k = 0; k < kK; ++k) v.a[f][k] = load_oct(dy + at + min(n0 + 32 * k + 8 * q, width - 8));
-    }
+    load_rows(v.x, dy, row, min(n0 + E * col, width - E));
     const size_t step = c.step + s;
 #pragma unroll
     for (int g = 0; g < RF; ++g)
@@ -265,22 +220,38 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
   };
   auto compute = [&](DyStep<DT, E, RF> &v, int s) {
     const int i0 = c.i0 + s * kStep, n = min(c.n - s * kStep, kStep);
-    // this wavefront's share of u
+    // this wavefront's share of u: its values laid out in LDS and read as operands,
+    // 16-byte pieces of a row in an order that keeps the banks apart
+    constexpr int kRow = 16 * E, kMask = E == 8 ? 15 : 7;
+    uint16_t *lay = tile[wave];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int t = 8 * q + i;
+      if constexpr (E == 8)
+        *reinterpret_cast<uint4 *>(lay + t * kRow + (col ^ (t & kMask)) * 8) = make_uint4(v.x.w[i][0], v.x.w[i][1], v.x.w[i][2], v.x.w[i][3]);
+      else
+        *reinterpret_cast<uint2 *>(lay + t * kRow + ((col >> 1) ^ (t & kMask)) * 8 + 4 * (col & 1)) = make_uint2(v.x.w[i][0], v.x.w[i][1]);
+    }
     float *mine = red[s & 1][wave];
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+    for (int f = 0; f < 2; ++f) {
+      float4_t d[RF] = {};
 #pragma unroll
-      for (int g = 0; g < RF; ++g) {
-        float4_t d = {};
+      for (int k = 0; k < kK; ++k) {
+        const int t = 16 * f + col;
+        const Oct a = load_oct_aligned(lay + t * kRow + ((4 * k + q) ^ (t & kMask)) * 8);
 #pragma unroll
-        for (int k = 0; k < kK; ++k) d = mfma<DT>(v.a[f][k], bv[k][g], d);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mine[(16 * f + 4 * q + i) * kStride + 16 * g + col] = d[i];
+        for (int g = 0; g < RF; ++g) d[g] = mfma<DT>(a, bv[k][g], d[g]);
       }
-    if (n < kStep) drop_rows<E>(v.x, 8 * q, n);
+#pragma unroll
+      for (int g = 0; g < RF; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mine[(16 * f + 4 * q + i) * kStride + 16 * g + col] = d[g][i];
+    }
+    if (n < kStep) drop_rows(v.x, 8 * q, n);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const Oct x = column<E>(v.x, e);
+      const Oct x = column(v.x, e);
 #pragma unroll
       for (int g = 0; g < RF; ++g) {
         if constexpr (DT == kF16) {
@@ -335,10 +306,11 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
 template <int DT, int E, int RF>
 struct XStep {
   Rows<E> x;
-  Oct base[2][E / 2], over[RF][kPieces<DT>], along[2][RF];
-  float back, token_back[2];
-  size_t at[2];
-  bool live[2];
+  Rows<E, 4> base[2];
+  Oct over[RF][kPieces<DT>], along[2][RF];
+  float back;
+  float4_t token_back[2];
+  int token;   // as step_token gives them
 };
 
 template <int DT, int E, int RF>
@@ -380,39 +352,32 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
 #pragma unroll
       for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(min(j + i, r - 1)) * K;
       Rows<E> v;
-      load_rows<E>(v, Aa, row, k0 + E * col);
-      drop_rows<E>(v, j, r);
+      load_rows(v, Aa, row, k0 + E * col);
+      drop_rows(v, j, r);
 #pragma unroll
-      for (int e = 0; e < E; ++e) av[e][g] = column<E>(v, e);
+      for (int e = 0; e < E; ++e) av[e][g] = column(v, e);
     }
   }
   float4_t acc[E][RF] = {};
   const int steps = (c.n + kStep - 1) / kStep;
-  // dx: a lane holds columns k0 + 4 E q .. + 4 E - 1 of token 16 f + col
   auto load = [&](XStep<DT, E, RF> &v, int s, int token) {
-    const int n = min(c.n - s * kStep, kStep);
     const size_t step = c.step + s;
+    v.token = token;
     const int safe = min(max(token, 0), M - 1);
     size_t row[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(safe, 8 * q + i)) * K;
-    load_rows<E>(v.x, x, row, k0 + E * col);
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      const int t = __shfl(token, 16 * f + col);
-      v.live[f] = 16 * f + col < n && t >= 0 && t < M;
-      v.at[f] = static_cast<size_t>(min(max(t, 0), M - 1)) * K + k0 + 4 * E * q;
-    }
+    load_rows(v.x, x, row, k0 + E * col);
     if (base) {
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
+      for (int f = 0; f < 2; ++f) {
+        size_t at[4];
 #pragma unroll
-        for (int k = 0; k < E / 2; ++k) v.base[f][k] = load_oct_aligned(base + v.at[f] + 8 * k);
+        for (int i = 0; i < 4; ++i) at[i] = static_cast<size_t>(__shfl(safe, 16 * f + 4 * q + i)) * K;
+        load_rows(v.base[f], base, at, k0 + E * col);
+      }
     } else {
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-#pragma unroll
-        for (int k = 0; k < E / 2; ++k) v.base[f][k] = Oct{{0, 0, 0, 0}};
+      v.base[0] = v.base[1] = Rows<E, 4>{};
     }
 #pragma unroll
     for (int g = 0; g < RF; ++g)
@@ -422,16 +387,19 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
     for (int f = 0; f < 2; ++f)
 #pragma unroll
       for (int g = 0; g < RF; ++g) v.along[f][g] = u.along[((step * 2 + f) * RF + g) * 64 + lane];
-    v.back = DT == kF16 ? u.over_back[step] : 1.f;
+    if constexpr (DT == kF16) {
+      v.back = u.over_back[step];
 #pragma unroll
-    for (int f = 0; f < 2; ++f) v.token_back[f] = DT == kF16 ? u.along_back[step * kStep + 16 * f + col] : 1.f;
+      for (int f = 0; f < 2; ++f)
+        v.token_back[f] = *reinterpret_cast<const float4_t *>(u.along_back + step * kStep + 16 * f + 4 * q);
+    }
   };
   auto compute = [&](XStep<DT, E, RF> &v, int s) {
     const int n = min(c.n - s * kStep, kStep);
-    if (n < kStep) drop_rows<E>(v.x, 8 * q, n);
+    if (n < kStep) drop_rows(v.x, 8 * q, n);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const Oct xv = column<E>(v.x, e);
+      const Oct xv = column(v.x, e);
 #pragma unroll
       for (int g = 0; g < RF; ++g) {
         if constexpr (DT == kF16) {
@@ -448,26 +416,22 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
     }
 #pragma unroll
     for (int f = 0; f < 2; ++f) {
+      // D's rows are tokens: a lane holds columns k0 + E col .. of tokens 4 q .. + 3
       float4_t d[E] = {};
 #pragma unroll
-      for (int e = 0; e < E; ++e)
+      for (int g = 0; g < RF; ++g)
 #pragma unroll
-        for (int g = 0; g < RF; ++g) d[e] = mfma<DT>(av[e][g], v.along[f][g], d[e]);
-      if (!v.live[f]) continue;
-      // column 4 E q + E i + e is d[e][i]
-      const float tb = v.token_back[f];
+        for (int e = 0; e < E; ++e) d[e] = mfma<DT>(v.along[f][g], av[e][g], d[e]);
+      size_t at[4];
+      bool live[4];
 #pragma unroll
-      for (int k = 0; k < E / 2; ++k) {
-        Oct o;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int c0 = 8 * k + 2 * w;
-          const uint32_t b = v.base[f][k].w[w];
-          o.w[w] = pack2<DT>(fmaf(d[c0 % E][c0 / E], tb, to_f32<DT>(static_cast<uint16_t>(b))),
-                             fmaf(d[(c0 + 1) % E][(c0 + 1) / E], tb, to_f32<DT>(static_cast<uint16_t>(b >> 16))));
-        }
-        store_oct(dx + v.at[f] + 8 * k, o);
+      for (int i = 0; i < 4; ++i) {
+        const int t = 16 * f + 4 * q + i, token = __shfl(v.token, t);
+        live[i] = t < n && token >= 0 && token < M;
+        at[i] = static_cast<size_t>(max(token, 0)) * K;
       }
+      const float4_t back = DT == kF16 ? v.token_back[f] : float4_t{1.f, 1.f, 1.f, 1.f};
+      add_rows<DT, E>(dx, at, live, k0 + E * col, 0, K, d, back, v.base[f]);
     }
   };
   int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
