@@ -215,12 +215,22 @@ struct Chunk {
   int slot;         // its place among the partial sums, -1: the adapter has one chunk
 };
 
-// Where an adapter with more than one chunk keeps a chunk's sums. Its chunks but
-// the last are whole, so starts of two such lie `rows` apart, and so do two last
-// ones: at most one of each kind starts in any `rows` entries.
-__device__ __forceinline__ int slot_of(int i0, int rows, bool last) { return 2 * (i0 / rows) + (last ? 0 : 1); }
+// An adapter's tokens in chunks of at most `rows`, about equal and of whole steps.
+struct Cut {
+  int chunks, each;
+};
+__device__ __forceinline__ Cut cut_of(int tokens, int rows, int unit) {
+  const int chunks = (tokens + rows - 1) / rows;
+  return {chunks, chunks > 1 ? ((tokens + chunks - 1) / chunks + unit - 1) / unit * unit : rows};
+}
 
-// Chunk number b of `rows` tokens each (a multiple of unit), like tile_of. Offsets
+// Where an adapter with more than one chunk keeps a chunk's sums. Its chunks but
+// the last have over rows / 2 tokens, so that starts of two such lie that far
+// apart, and so do two last ones: at most one of each kind starts in any
+// rows / 2 entries.
+__device__ __forceinline__ int slot_of(int i0, int rows, bool last) { return 2 * (i0 / (rows / 2)) + (last ? 0 : 1); }
+
+// Chunk number b of up to `rows` tokens (a multiple of unit), like tile_of. Offsets
 // that are no sort's can name more steps than M tokens have (max_steps, what the
 // workspace holds): a chunk with such a step is none.
 __device__ __forceinline__ Chunk chunk_of(const int32_t *__restrict__ offsets, int L, int M, int rows, int unit,
@@ -243,12 +253,13 @@ __device__ __forceinline__ Chunk chunk_of(const int32_t *__restrict__ offsets, i
     int at = in_c - chunks, step = in_s - steps;
     for (int a = first; a < last; ++a) {
       if (per > 1) segment(offsets, a, M, lo, hi);
-      const int n = (hi - lo + rows - 1) / rows;
+      const Cut cut = cut_of(hi - lo, rows, unit);
+      const int n = cut.chunks;
       if (b < at + n) {
-        const int c = b - at, i0 = lo + c * rows;
-        const int s0 = step + c * (rows / unit), tokens = min(hi - i0, rows);
+        const int c = b - at, i0 = lo + c * cut.each;
+        const int s0 = step + c * (cut.each / unit), tokens = min(hi - i0, cut.each);
         if (s0 + (tokens + unit - 1) / unit <= max_steps)
-          t = {a, i0, tokens, s0, n > 1 ? slot_of(i0, rows, c == n - 1) : -1};
+          t = {a, i0, max(tokens, 0), s0, n > 1 ? slot_of(i0, rows, c == n - 1) : -1};
         break;
       }
       at += n;

@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads) adapters_few_kernel(
 // so that a lane holds E neighbouring columns of four of them. UNIT: tokens of the
 // tiles in which h's operands were made.
 template <int DT, int E, int TF, int RC, int RANK>
-__global__ void __launch_bounds__(kThreads) adapters_y_kernel(
+__global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
     const Oct *__restrict__ pieces, const float *__restrict__ backs, int unit, int M, int N, int r,
     const uint16_t *__restrict__ B, const float *__restrict__ scales, int L, const int32_t *__restrict__ ids,
     const int32_t *__restrict__ offsets, const int32_t *__restrict__ perm, const uint16_t *base,
@@ -446,6 +446,7 @@ __global__ void __launch_bounds__(kThreads) adapters_y_kernel(
       [&](Step &v, int s) {
         v.token = token;
         const int safe = min(max(token, 0), M - 1);
+        token = step_token(perm, c, kStep, s + 1);   // (before what it would else wait for)
 #pragma unroll
         for (int f = 0; f < TF; ++f) {
           // (a chunk's steps are whole but for the last, whose second half may be none)
@@ -462,7 +463,6 @@ __global__ void __launch_bounds__(kThreads) adapters_y_kernel(
 #pragma unroll
           for (int k = 0; k < RC; ++k) v.h[f][k] = pieces[(at * RC + k) * 64 + lane];
         }
-        token = step_token(perm, c, kStep, s + 1);
       },
       [&](const Step &v, int s) {
 #pragma unroll
@@ -578,7 +578,7 @@ void forward_rank(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
                        p.chunks, p.tiles);
   };
   auto pick = [&](auto tf) {
-    constexpr int kTF = RC <= 1 ? decltype(tf)::value : 1, kE = RC <= 2 ? 8 : 4;
+    constexpr int kTF = RC != 2 && RC != 8 ? decltype(tf)::value : 1, kE = RC <= 2 ? 8 : 4;
     auto first = adapters_h_kernel<DT, decltype(tf)::value, RC>;
     if (rank == kWhole) go(first, adapters_y_kernel<DT, kE, kTF, RC, kWhole>);
     else if (rank == kMore) go(first, adapters_y_kernel<DT, kE, kTF, RC, kMore>);

@@ -2,8 +2,8 @@
 //
 //   dB_a = s_a sum_t dy_t^T h_t      dx_t = base_t + u_t A_a      dA_a = sum_t u_t^T x_t
 //
-// dy and x are read once each. One pass over dy gives dB and, per 4 * 16 E columns, a
-// share of u; one over x gives dA and dx. Between them the shares of u are added
+// dy and x are read once each. One pass over dy gives dB and, per 512 columns, a share
+// of u; one over x gives dA and dx. Between them the shares of u are added
 // up and split into the 16-bit pieces that the matrix instructions take, once for
 // all columns.
 //
@@ -21,7 +21,10 @@ namespace {
 
 using namespace adapters;
 
-constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kThreads = 256, kWaves = kThreads / 64;       // of the pass over x and the sums
+// of the pass over dy, by pieces of 16 values: as many columns share a u as fit LDS
+constexpr int dy_waves(int rf) { return rf == 8 ? 4 : 8; }
+constexpr int kE = 4;                                        // columns of a lane in both
 constexpr int kPieceThreads = 512;
 constexpr int kStep = 32;   // tokens of one step: the instruction's k
 
@@ -136,6 +139,7 @@ __device__ __forceinline__ void put(float *out, float *part, const Chunk &c, siz
 
 // Zeros to a slice of the gradient of an adapter without tokens: columns n0 .. n1;
 // value (n, j) at n * sn + j * sj.
+template <int kThreads>
 __device__ __forceinline__ void clear(float *out, int r, int n0, int n1, size_t sn, size_t sj) {
   const int n = max(n1 - n0, 0);
   for (long i = threadIdx.x; i < static_cast<long>(n) * r; i += kThreads) {
@@ -147,38 +151,61 @@ __device__ __forceinline__ void clear(float *out, int r, int n0, int n1, size_t 
 
 // ------------------------------------------------------------------ dy: dB and u
 
-// What a step reads, on its way while the step before is computed. dy's values lie
-// by rows for the sums over tokens; for u they go through LDS.
-template <int DT, int E, int RF>
-struct DyStep {
-  Rows<E> x;
-  Oct h[RF][kPieces<DT>];
-  float back;
+// The operands of a step (COUNT loads of 64 lanes) on their way through registers into
+// LDS, where all wavefronts read them.
+template <int COUNT, int WAVES>
+struct Shared {
+  static constexpr int kEach = (COUNT + WAVES - 1) / WAVES;
+  typedef uint32_t vec_t __attribute__((ext_vector_type(4)));
+  vec_t v[kEach];
+  __device__ __forceinline__ void load(const Oct *from) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      v[i] = reinterpret_cast<const vec_t *>(from)[min(wave + i * WAVES, COUNT - 1) * 64 + lane];
+  }
+  __device__ __forceinline__ void lay(Oct *lds) const {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i)
+      if (wave + i * WAVES < COUNT) reinterpret_cast<vec_t *>(lds)[(wave + i * WAVES) * 64 + lane] = v[i];
+  }
 };
+
+// A barrier that orders LDS alone, and leaves the loads under way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
 
 // Workgroup (chunk, slice): 16 E columns of dy a wavefront. width: columns of a row
 // of dy, N or, where that is less, 8. A piece of columns that would reach past
 // the last starts earlier, so that every load is whole and none is in a branch;
 // what it has twice is not stored, or meets a zero of B.
-template <int DT, int E, int RF>
-__global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *__restrict__ dy, int width, int M, int N, int r,
-                                                               const uint16_t *__restrict__ B,
-                                                               const float *__restrict__ scales, int L,
-                                                               const int32_t *__restrict__ offsets,
-                                                               const int32_t *__restrict__ perm, int rows, int chunks,
-                                                               int max_steps, Pieces h, float *__restrict__ u_part,
-                                                               float *__restrict__ dB, float *__restrict__ part) {
-  constexpr int kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves, kK = kCols / 32;
+//
+// dy's values lie by rows for the sums over tokens; for u they go through LDS, 16-byte
+// pieces of a row in an order that keeps the banks apart.
+template <int DT, int RF>
+__global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 : 1) adapters_dy_kernel(
+    const uint16_t *__restrict__ dy, int width, int M, int N, int r, const uint16_t *__restrict__ B,
+    const float *__restrict__ scales, int L, const int32_t *__restrict__ offsets, const int32_t *__restrict__ perm,
+    int rows, int chunks, int max_steps, Pieces h, float *__restrict__ u_part, float *__restrict__ dB,
+    float *__restrict__ part) {
+  constexpr int kDyWaves = dy_waves(RF), kDyThreads = 64 * kDyWaves;
+  constexpr int E = kE, kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kDyWaves, kK = kCols / 32;
   constexpr int kStride = 16 * RF + 1;
-  __shared__ float red[2][kWaves][kStep * kStride];
-  __shared__ __attribute__((aligned(16))) uint16_t tile[kWaves][kStep * kCols];
+  __shared__ float red[kDyWaves][kStep * kStride];
+  __shared__ __attribute__((aligned(16))) uint16_t tile[kDyWaves][kStep * kCols];
+  __shared__ Oct hs[RF * kP * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   if (static_cast<int>(blockIdx.y) >= chunks) {
     int lo, hi;
     const int a = blockIdx.y - chunks;
     segment(offsets, a, M, lo, hi);
     if (lo == hi)
-      clear(dB + static_cast<size_t>(a) * N * r, r, blockIdx.x * kSlice, min(N, static_cast<int>(blockIdx.x + 1) * kSlice), r, 1);
+      clear<kDyThreads>(dB + static_cast<size_t>(a) * N * r, r, blockIdx.x * kSlice,
+                        min(N, static_cast<int>(blockIdx.x + 1) * kSlice), r, 1);
     return;
   }
   const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
@@ -204,90 +231,88 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
       for (int d = 0; d < 4; ++d) bv[k][g].w[d] = e[2 * d] | e[2 * d + 1] << 16;
     }
   float4_t acc[E][RF] = {};
-  const int steps = (c.n + kStep - 1) / kStep;
-  auto load = [&](DyStep<DT, E, RF> &v, int s, int token) {
-    token = min(max(token, 0), M - 1);
-    size_t row[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(token, 8 * q + i)) * width;
-    load_rows(v.x, dy, row, min(n0 + E * col, width - E));
-    const size_t step = c.step + s;
-#pragma unroll
-    for (int g = 0; g < RF; ++g)
-#pragma unroll
-      for (int p = 0; p < kP; ++p) v.h[g][p] = h.over[((step * RF + g) * kP + p) * 64 + lane];
-    v.back = DT == kF16 ? h.over_back[step] : 1.f;
-  };
-  auto compute = [&](DyStep<DT, E, RF> &v, int s) {
-    const int i0 = c.i0 + s * kStep, n = min(c.n - s * kStep, kStep);
-    // this wavefront's share of u: its values laid out in LDS and read as operands,
-    // 16-byte pieces of a row in an order that keeps the banks apart
-    constexpr int kRow = 16 * E, kMask = E == 8 ? 15 : 7;
-    uint16_t *lay = tile[wave];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int t = 8 * q + i;
-      if constexpr (E == 8)
-        *reinterpret_cast<uint4 *>(lay + t * kRow + (col ^ (t & kMask)) * 8) = make_uint4(v.x.w[i][0], v.x.w[i][1], v.x.w[i][2], v.x.w[i][3]);
-      else
-        *reinterpret_cast<uint2 *>(lay + t * kRow + ((col >> 1) ^ (t & kMask)) * 8 + 4 * (col & 1)) = make_uint2(v.x.w[i][0], v.x.w[i][1]);
-    }
-    float *mine = red[s & 1][wave];
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      float4_t d[RF] = {};
-#pragma unroll
-      for (int k = 0; k < kK; ++k) {
-        const int t = 16 * f + col;
-        const Oct a = load_oct_aligned(lay + t * kRow + ((4 * k + q) ^ (t & kMask)) * 8);
-#pragma unroll
-        for (int g = 0; g < RF; ++g) d[g] = mfma<DT>(a, bv[k][g], d[g]);
-      }
-#pragma unroll
-      for (int g = 0; g < RF; ++g)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mine[(16 * f + 4 * q + i) * kStride + 16 * g + col] = d[g][i];
-    }
-    if (n < kStep) drop_rows(v.x, 8 * q, n);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const Oct x = column(v.x, e);
-#pragma unroll
-      for (int g = 0; g < RF; ++g) {
-        if constexpr (DT == kF16) {
-          float4_t d = {};
-#pragma unroll
-          for (int p = 0; p < kP; ++p) d = mfma<DT>(x, v.h[g][p], d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[i], v.back, acc[e][g][i]);
-        } else {
-#pragma unroll
-          for (int p = 0; p < kP; ++p) acc[e][g] = mfma<DT>(x, v.h[g][p], acc[e][g]);
-        }
-      }
-    }
-    // the slice's share of u (the other half of `red` is written next, so one
-    // barrier a step is enough; it orders LDS alone, and leaves the loads under way)
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-    float *out = u_part + (static_cast<size_t>(blockIdx.x) * M + i0) * r;
-    for (int i = threadIdx.x; i < kStep * 16 * RF; i += kThreads) {
-      const int t = i / (16 * RF), j = i % (16 * RF);
-      float sum = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) sum += red[s & 1][w][t * kStride + j];
-      if (t < n && j < r) out[t * r + j] = sum;
-    }
+  struct Step {
+    Rows<E> x;
+    Shared<RF * kP, kDyWaves> h;
+    float back;
   };
   int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
-  in_turn<DyStep<DT, E, RF>>(
-      steps,
-      [&](DyStep<DT, E, RF> &v, int s) {
-        load(v, s, token);
-        token = step_token(perm, c, kStep, s + 1);
+  in_turn<Step>(
+      (c.n + kStep - 1) / kStep,
+      [&](Step &v, int s) {
+        const int safe = min(max(token, 0), M - 1);
+        token = step_token(perm, c, kStep, s + 1);   // (before what it would else wait for)
+        const size_t step = c.step + s;
+        size_t row[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(safe, 8 * q + i)) * width;
+        load_rows(v.x, dy, row, min(n0 + E * col, width - E));
+        v.h.load(h.over + step * RF * kP * 64);
+        if constexpr (DT == kF16) v.back = h.over_back[step];
       },
-      compute);
+      [&](Step &v, int s) {
+        const int i0 = c.i0 + s * kStep, n = min(c.n - s * kStep, kStep);
+        uint16_t *lay = tile[wave];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int t = 8 * q + i;
+          *reinterpret_cast<uint2 *>(lay + t * kCols + ((col >> 1) ^ (t & 7)) * 8 + 4 * (col & 1)) =
+              make_uint2(v.x.w[i][0], v.x.w[i][1]);
+        }
+        v.h.lay(hs);
+        lds_barrier();
+        // this wavefront's share of u
+        float *mine = red[wave];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          float4_t d[RF] = {};
+#pragma unroll
+          for (int k = 0; k < kK; ++k) {
+            const int t = 16 * f + col;
+            const Oct a = load_oct_aligned(lay + t * kCols + ((4 * k + q) ^ (t & 7)) * 8);
+#pragma unroll
+            for (int g = 0; g < RF; ++g) d[g] = mfma<DT>(a, bv[k][g], d[g]);
+          }
+#pragma unroll
+          for (int g = 0; g < RF; ++g)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mine[(16 * f + 4 * q + i) * kStride + 16 * g + col] = d[g][i];
+        }
+        if (n < kStep) drop_rows(v.x, 8 * q, n);
+        Oct x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] = column(v.x, e);
+#pragma unroll
+        for (int g = 0; g < RF; ++g) {
+          float4_t d[E] = {};
+#pragma unroll
+          for (int p = 0; p < kP; ++p) {
+            const Oct w = hs[(g * kP + p) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              if constexpr (DT == kF16) d[e] = mfma<DT>(x[e], w, d[e]);
+              else acc[e][g] = mfma<DT>(x[e], w, acc[e][g]);
+            }
+          }
+          if constexpr (DT == kF16) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[e][i], v.back, acc[e][g][i]);
+          }
+        }
+        // the slice's share of u (what it reads, and hs, is written again behind the
+        // next step's first barrier, or behind this one)
+        lds_barrier();
+        float *out = u_part + (static_cast<size_t>(blockIdx.x) * M + i0) * r;
+        for (int i = threadIdx.x; i < kStep * 16 * RF; i += kDyThreads) {
+          const int t = i / (16 * RF), j = i % (16 * RF);
+          float sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < kDyWaves; ++w) sum += red[w][t * kStride + j];
+          if (t < n && j < r) out[t * r + j] = sum;
+        }
+      });
   const float sa = scales[c.a];
 #pragma unroll
   for (int e = 0; e < E; ++e)
@@ -303,43 +328,32 @@ __global__ void __launch_bounds__(kThreads) adapters_dy_kernel(const uint16_t *_
 
 // ------------------------------------------------------------------ x: dA and dx
 
-template <int DT, int E, int RF>
-struct XStep {
-  Rows<E> x;
-  Rows<E, 4> base[2];
-  Oct over[RF][kPieces<DT>], along[2][RF];
-  float back;
-  float4_t token_back[2];
-  int token;   // as step_token gives them
-};
-
-template <int DT, int E, int RF>
-__global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__restrict__ x, int M, int K, int r,
-                                                              const uint16_t *__restrict__ A, int L,
-                                                              const int32_t *__restrict__ ids,
-                                                              const int32_t *__restrict__ offsets,
-                                                              const int32_t *__restrict__ perm, int rows, int chunks,
-                                                              int max_steps, Pieces u, const uint16_t *base, uint16_t *dx,
-                                                              float *__restrict__ dA, float *__restrict__ part) {
-  constexpr int kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves;
+template <int DT, int RF>
+__global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
+    const uint16_t *__restrict__ x, int M, int K, int r, const uint16_t *__restrict__ A, int L,
+    const int32_t *__restrict__ ids, const int32_t *__restrict__ offsets, const int32_t *__restrict__ perm, int rows,
+    int chunks, int max_steps, Pieces u, const uint16_t *base, uint16_t *dx, float *__restrict__ dA,
+    float *__restrict__ part) {
+  constexpr int E = kE, kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves;
+  __shared__ Oct over[RF * kP * 64], along[2 * RF * 64];
+  __shared__ int list[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const int s0 = blockIdx.x * kSlice, s1 = min(K, s0 + kSlice);
-  if (static_cast<int>(blockIdx.y) >= chunks + L) {   // 64 tokens: those without an adapter
-    __shared__ int list[64];
-    copy_others<kThreads>(ids, (blockIdx.y - chunks - L) * 64, M, L, base, dx, K, s0, s1, list);
-    return;
-  }
+  if (static_cast<int>(blockIdx.y) >= chunks + L)   // 64 tokens: those without an adapter
+    return copy_others<kThreads>(ids, (blockIdx.y - chunks - L) * 64, M, L, base, dx, K, s0, s1, list);
   if (static_cast<int>(blockIdx.y) >= chunks) {
     int lo, hi;
     const int a = blockIdx.y - chunks;
     segment(offsets, a, M, lo, hi);
-    if (lo == hi) clear(dA + static_cast<size_t>(a) * r * K, r, s0, s1, 1, K);
+    if (lo == hi) clear<kThreads>(dA + static_cast<size_t>(a) * r * K, r, s0, s1, 1, K);
     return;
   }
   const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
   if (c.a < 0) return;
-  const int k0 = s0 + wave * kCols;
-  if (k0 >= K) return;   // K is a multiple of 128, kCols of 64: all or nothing
+  // (K is a multiple of 128: a wavefront's columns are all there or none is; those of
+  // none go along, for the barriers, on the last ones, and store nothing)
+  const bool mine = s0 + wave * kCols < K;
+  const int k0 = mine ? s0 + wave * kCols : K - kCols;
   // A of these columns, transposed like the rows of x: column k0 + E col + e of
   // values 16 g + 8 (q % 2) .. + 7
   Oct av[E][RF];
@@ -359,89 +373,99 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
     }
   }
   float4_t acc[E][RF] = {};
-  const int steps = (c.n + kStep - 1) / kStep;
-  auto load = [&](XStep<DT, E, RF> &v, int s, int token) {
-    const size_t step = c.step + s;
-    v.token = token;
-    const int safe = min(max(token, 0), M - 1);
-    size_t row[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(safe, 8 * q + i)) * K;
-    load_rows(v.x, x, row, k0 + E * col);
-    if (base) {
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        size_t at[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = static_cast<size_t>(__shfl(safe, 16 * f + 4 * q + i)) * K;
-        load_rows(v.base[f], base, at, k0 + E * col);
-      }
-    } else {
-      v.base[0] = v.base[1] = Rows<E, 4>{};
-    }
-#pragma unroll
-    for (int g = 0; g < RF; ++g)
-#pragma unroll
-      for (int p = 0; p < kP; ++p) v.over[g][p] = u.over[((step * RF + g) * kP + p) * 64 + lane];
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int g = 0; g < RF; ++g) v.along[f][g] = u.along[((step * 2 + f) * RF + g) * 64 + lane];
-    if constexpr (DT == kF16) {
-      v.back = u.over_back[step];
-#pragma unroll
-      for (int f = 0; f < 2; ++f)
-        v.token_back[f] = *reinterpret_cast<const float4_t *>(u.along_back + step * kStep + 16 * f + 4 * q);
-    }
-  };
-  auto compute = [&](XStep<DT, E, RF> &v, int s) {
-    const int n = min(c.n - s * kStep, kStep);
-    if (n < kStep) drop_rows(v.x, 8 * q, n);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const Oct xv = column(v.x, e);
-#pragma unroll
-      for (int g = 0; g < RF; ++g) {
-        if constexpr (DT == kF16) {
-          float4_t d = {};
-#pragma unroll
-          for (int p = 0; p < kP; ++p) d = mfma<DT>(v.over[g][p], xv, d);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[i], v.back, acc[e][g][i]);
-        } else {
-#pragma unroll
-          for (int p = 0; p < kP; ++p) acc[e][g] = mfma<DT>(v.over[g][p], xv, acc[e][g]);
-        }
-      }
-    }
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-      // D's rows are tokens: a lane holds columns k0 + E col .. of tokens 4 q .. + 3
-      float4_t d[E] = {};
-#pragma unroll
-      for (int g = 0; g < RF; ++g)
-#pragma unroll
-        for (int e = 0; e < E; ++e) d[e] = mfma<DT>(v.along[f][g], av[e][g], d[e]);
-      size_t at[4];
-      bool live[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = 16 * f + 4 * q + i, token = __shfl(v.token, t);
-        live[i] = t < n && token >= 0 && token < M;
-        at[i] = static_cast<size_t>(max(token, 0)) * K;
-      }
-      const float4_t back = DT == kF16 ? v.token_back[f] : float4_t{1.f, 1.f, 1.f, 1.f};
-      add_rows<DT, E>(dx, at, live, k0 + E * col, 0, K, d, back, v.base[f]);
-    }
+  struct Step {
+    Rows<E> x;
+    Rows<E, 4> base[2];
+    Shared<RF * kP, kWaves> over;
+    Shared<2 * RF, kWaves> along;
+    float back;
+    float4_t token_back[2];
+    int token;   // as step_token gives them
   };
   int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
-  in_turn<XStep<DT, E, RF>>(
-      steps,
-      [&](XStep<DT, E, RF> &v, int s) {
-        load(v, s, token);
-        token = step_token(perm, c, kStep, s + 1);
+  in_turn<Step>(
+      (c.n + kStep - 1) / kStep,
+      [&](Step &v, int s) {
+        const size_t step = c.step + s;
+        v.token = token;
+        const int safe = min(max(token, 0), M - 1);
+        token = step_token(perm, c, kStep, s + 1);   // (before what it would else wait for)
+        size_t row[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(safe, 8 * q + i)) * K;
+        load_rows(v.x, x, row, k0 + E * col);
+        if (base) {
+#pragma unroll
+          for (int f = 0; f < 2; ++f) {
+            size_t at[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at[i] = static_cast<size_t>(__shfl(safe, 16 * f + 4 * q + i)) * K;
+            load_rows(v.base[f], base, at, k0 + E * col);
+          }
+        } else {
+          v.base[0] = v.base[1] = Rows<E, 4>{};
+        }
+        v.over.load(u.over + step * RF * kP * 64);
+        v.along.load(u.along + step * 2 * RF * 64);
+        if constexpr (DT == kF16) {
+          v.back = u.over_back[step];
+#pragma unroll
+          for (int f = 0; f < 2; ++f)
+            v.token_back[f] = *reinterpret_cast<const float4_t *>(u.along_back + step * kStep + 16 * f + 4 * q);
+        }
       },
-      compute);
+      [&](Step &v, int s) {
+        const int n = min(c.n - s * kStep, kStep);
+        lds_barrier();   // the step before has read its operands
+        v.over.lay(over);
+        v.along.lay(along);
+        lds_barrier();
+        if (n < kStep) drop_rows(v.x, 8 * q, n);
+        Oct xv[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) xv[e] = column(v.x, e);
+#pragma unroll
+        for (int g = 0; g < RF; ++g) {
+          float4_t d[E] = {};
+#pragma unroll
+          for (int p = 0; p < kP; ++p) {
+            const Oct w = over[(g * kP + p) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              if constexpr (DT == kF16) d[e] = mfma<DT>(w, xv[e], d[e]);
+              else acc[e][g] = mfma<DT>(w, xv[e], acc[e][g]);
+            }
+          }
+          if constexpr (DT == kF16) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[e][i], v.back, acc[e][g][i]);
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          // D's rows are tokens: a lane holds columns k0 + E col .. of tokens 4 q .. + 3
+          float4_t d[E] = {};
+#pragma unroll
+          for (int g = 0; g < RF; ++g) {
+            const Oct w = along[(f * RF + g) * 64 + lane];
+#pragma unroll
+            for (int e = 0; e < E; ++e) d[e] = mfma<DT>(w, av[e][g], d[e]);
+          }
+          size_t at[4];
+          bool live[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int t = 16 * f + 4 * q + i, to = __shfl(v.token, t);
+            live[i] = mine && t < n && to >= 0 && to < M;
+            at[i] = static_cast<size_t>(max(to, 0)) * K;
+          }
+          const float4_t back = DT == kF16 ? v.token_back[f] : float4_t{1.f, 1.f, 1.f, 1.f};
+          add_rows<DT, E>(dx, at, live, k0 + E * col, 0, K, d, back, v.base[f]);
+        }
+      });
+  if (!mine) return;
 #pragma unroll
   for (int g = 0; g < RF; ++g)
 #pragma unroll
@@ -451,9 +475,7 @@ __global__ void __launch_bounds__(kThreads) adapters_x_kernel(const uint16_t *__
       const size_t at = static_cast<size_t>(j) * K + k0 + E * col;
       const size_t size = static_cast<size_t>(r) * K;
       float *out = c.slot >= 0 ? part + static_cast<size_t>(c.slot) * size : dA + static_cast<size_t>(c.a) * size;
-#pragma unroll
-      for (int e = 0; e < E; e += 4)
-        *reinterpret_cast<float4_t *>(out + at + e) = float4_t{acc[e][g][i], acc[e + 1][g][i], acc[e + 2][g][i], acc[e + 3][g][i]};
+      *reinterpret_cast<float4_t *>(out + at) = float4_t{acc[0][g][i], acc[1][g][i], acc[2][g][i], acc[3][g][i]};
     }
 }
 
@@ -466,12 +488,13 @@ __global__ void __launch_bounds__(kThreads) adapters_sum_kernel(const float *__r
   int lo, hi;
   segment(offsets, a, M, lo, hi);
   if (hi - lo <= rows) return;
+  const int each = cut_of(hi - lo, rows, kStep).each;
   const float sa = scales ? scales[a] : 1.f;
   for (size_t i = static_cast<size_t>(blockIdx.x) * kThreads + threadIdx.x; i < size;
        i += static_cast<size_t>(gridDim.x) * kThreads) {
     float s = 0.f;
 #pragma unroll 8
-    for (int at = lo; at < hi; at += rows) s += part[static_cast<size_t>(slot_of(at, rows, hi - at <= rows)) * size + i];
+    for (int at = lo; at < hi; at += each) s += part[static_cast<size_t>(slot_of(at, rows, hi - at <= each)) * size + i];
     out[static_cast<size_t>(a) * size + i] = s * sa;
   }
 }
@@ -482,18 +505,18 @@ constexpr size_t kAlign = 256;
 size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 
 struct Plan {
-  int rf, e_y, e_x;             // columns of a lane in the passes over dy and x
+  int rf;
   int steps;                    // at most
   int rows_y, chunks_y, rows_x, chunks_x;
   int slices_y, slices_x;
   size_t over, along, over_back, along_back, u_part, sums, pad, total;   // where in the workspace
 };
 
-// Tokens of a chunk: as many workgroups as fill the card, and chunks long enough
-// that their sums' way through memory stays small beside the rows'.
-int chunk_rows(int M, int slices) {
-  constexpr int kWant = 512;
-  const long rows = static_cast<long>(M) * slices / kWant;
+// Tokens of a chunk: so many that the workgroups of all slices fill `slots` once, and
+// chunks long enough that their sums' way through memory stays small beside the
+// rows'.
+int chunk_rows(int M, int slices, int slots) {
+  const long rows = (static_cast<long>(M) * slices + slots - 1) / slots;
   return static_cast<int>(std::min<long>(std::max<long>((rows + kStep - 1) / kStep * kStep, 128), 4096));
 }
 
@@ -501,14 +524,12 @@ Plan plan_of(const AdapterArgs &g) {
   Plan p{};
   const int frags = (g.r + 15) / 16;
   p.rf = frags <= 1 ? 1 : frags <= 2 ? 2 : frags <= 4 ? 4 : 8;
-  p.e_y = p.rf <= 1 ? 8 : 4;
-  p.e_x = 4;
-  p.slices_y = (g.N + 16 * p.e_y * kWaves - 1) / (16 * p.e_y * kWaves);
-  p.slices_x = (g.K + 16 * p.e_x * kWaves - 1) / (16 * p.e_x * kWaves);
+  p.slices_y = (g.N + 16 * kE * dy_waves(p.rf) - 1) / (16 * kE * dy_waves(p.rf));
+  p.slices_x = (g.K + 16 * kE * kWaves - 1) / (16 * kE * kWaves);
   const int some = std::min(g.L, g.M);
   p.steps = g.M / kStep + some;
-  p.rows_y = chunk_rows(g.M, p.slices_y);
-  p.rows_x = chunk_rows(g.M, p.slices_x);
+  p.rows_y = chunk_rows(g.M, p.slices_y, p.rf == 1 ? 512 : 256);
+  p.rows_x = chunk_rows(g.M, p.slices_x, 512);
   p.chunks_y = g.M / p.rows_y + some;
   p.chunks_x = g.M / p.rows_x + some;
   const int pieces = g.dtype == kF16 ? 2 : 3;
@@ -523,15 +544,15 @@ Plan plan_of(const AdapterArgs &g) {
   p.over_back = take(static_cast<size_t>(p.steps) * 4);
   p.along_back = take(static_cast<size_t>(p.steps) * kStep * 4);
   p.u_part = take(static_cast<size_t>(p.slices_y) * g.M * g.r * 4);
-  const size_t sums_y = g.M > p.rows_y ? 2 * (static_cast<size_t>(g.M) / p.rows_y + 1) * g.N * g.r * 4 : 0;
-  const size_t sums_x = g.M > p.rows_x ? 2 * (static_cast<size_t>(g.M) / p.rows_x + 1) * g.K * g.r * 4 : 0;
+  const size_t sums_y = g.M > p.rows_y ? 2 * (static_cast<size_t>(g.M) / (p.rows_y / 2) + 1) * g.N * g.r * 4 : 0;
+  const size_t sums_x = g.M > p.rows_x ? 2 * (static_cast<size_t>(g.M) / (p.rows_x / 2) + 1) * g.K * g.r * 4 : 0;
   p.sums = take(std::max(sums_y, sums_x));   // dB's are done with when dA's begin
   p.pad = take(g.N < kNarrow ? static_cast<size_t>(g.M) * kNarrow * 2 : 0);
   p.total = at;
   return p;
 }
 
-template <int DT, int EY, int EX, int RF>
+template <int DT, int RF>
 void backward_go(const AdapterArgs &g, const Plan &p, hipStream_t s) {
   uint8_t *ws = static_cast<uint8_t *>(g.scratch);
   const Pieces q{reinterpret_cast<Oct *>(ws + p.over), reinterpret_cast<Oct *>(ws + p.along),
@@ -555,7 +576,7 @@ void backward_go(const AdapterArgs &g, const Plan &p, hipStream_t s) {
                        g.M, g.N, pad);
     dy = pad;
   }
-  hipLaunchKernelGGL((adapters_dy_kernel<DT, EY, RF>), dim3(p.slices_y, p.chunks_y + g.L), block, 0, s, dy,
+  hipLaunchKernelGGL((adapters_dy_kernel<DT, RF>), dim3(p.slices_y, p.chunks_y + g.L), dim3(64 * dy_waves(RF)), 0, s, dy,
                      std::max(g.N, kNarrow), g.M, g.N, g.r, b, g.scales, g.L, g.offsets, g.perm, p.rows_y,
                      p.chunks_y, p.steps, q, u_part, g.d_b, sums);
   if (g.M > p.rows_y) sum(static_cast<size_t>(g.N) * g.r, g.scales, p.rows_y, g.d_b);
@@ -563,7 +584,7 @@ void backward_go(const AdapterArgs &g, const Plan &p, hipStream_t s) {
     hipLaunchKernelGGL((adapters_pieces_kernel<DT, RF, false>), dim3(p.steps), dim3(kPieceThreads), 0, s, u_part, p.slices_y, g.M, g.r,
                        g.scales, g.L, g.offsets, g.perm, q);
   const int others = base == dx ? 0 : (g.M + 63) / 64;
-  hipLaunchKernelGGL((adapters_x_kernel<DT, EX, RF>), dim3(p.slices_x, p.chunks_x + g.L + others), block, 0, s,
+  hipLaunchKernelGGL((adapters_x_kernel<DT, RF>), dim3(p.slices_x, p.chunks_x + g.L + others), block, 0, s,
                      static_cast<const uint16_t *>(g.x), g.M, g.K, g.r, a, g.L, g.ids, g.offsets, g.perm, p.rows_x,
                      p.chunks_x, p.steps, q, base, dx, g.d_a, sums);
   if (g.M > p.rows_x) sum(static_cast<size_t>(g.K) * g.r, nullptr, p.rows_x, g.d_a);
@@ -571,10 +592,10 @@ void backward_go(const AdapterArgs &g, const Plan &p, hipStream_t s) {
 
 template <int DT>
 void backward_ranks(const AdapterArgs &g, const Plan &p, hipStream_t s) {
-  if (p.rf == 1) backward_go<DT, 8, 4, 1>(g, p, s);
-  else if (p.rf == 2) backward_go<DT, 4, 4, 2>(g, p, s);
-  else if (p.rf == 4) backward_go<DT, 4, 4, 4>(g, p, s);
-  else backward_go<DT, 4, 4, 8>(g, p, s);
+  if (p.rf == 1) backward_go<DT, 1>(g, p, s);
+  else if (p.rf == 2) backward_go<DT, 2>(g, p, s);
+  else if (p.rf == 4) backward_go<DT, 4>(g, p, s);
+  else backward_go<DT, 8>(g, p, s);
 }
 
 }  // namespace
