@@ -270,27 +270,37 @@ __device__ __forceinline__ Chunk chunk_of(const int32_t *__restrict__ offsets, i
   return {all(t.a), all(t.i0), all(t.n), all(t.step), all(t.slot)};
 }
 
-// A step's tokens, one a lane (lanes `unit` and up the same again); past the last the
-// last once more.
-__device__ __forceinline__ int step_token(const int32_t *__restrict__ perm, const Chunk &c, int unit, int s) {
-  return perm[c.i0 + min(s * unit + (static_cast<int>(threadIdx.x) & (unit - 1)), c.n - 1)];
+// A chunk's tokens in LDS, -1 for what is none; up to a whole step the last once more.
+// From there their numbers come without a wait for the loads that are under way, as
+// a number that is loaded among them would.
+constexpr int kMostTokens = 1024;
+__device__ __forceinline__ void stage_tokens(const int32_t *__restrict__ perm, const Chunk &c, int unit, int M,
+                                             int (&tokens)[kMostTokens]) {
+  for (int i = threadIdx.x; i < (c.n + unit - 1) / unit * unit; i += blockDim.x) {
+    const int t = perm[c.i0 + min(i, c.n - 1)];
+    tokens[i] = t >= 0 && t < M ? t : -1;
+  }
+  __syncthreads();
 }
 
-// Two steps' values in turn: the next step's loads are under way while a step is
+// A few steps' values in turn: the next steps' loads are under way while a step is
 // computed. They are always made, the last step's again at the end: a load in a
 // branch would have the compiler wait for all that are under way.
-template <class V, class LOAD, class COMPUTE>
+// AHEAD: steps under way beside the one that is computed.
+template <class V, int AHEAD = 1, class LOAD, class COMPUTE>
 __device__ __forceinline__ void in_turn(int steps, LOAD load, COMPUTE compute) {
-  V even, odd;
-  load(even, 0);
-  if (steps == 1) return compute(even, 0);
-  for (int s = 0;; s += 2) {
-    load(odd, min(s + 1, steps - 1));
-    compute(even, s);
-    if (s + 1 >= steps) return;
-    load(even, min(s + 2, steps - 1));
-    compute(odd, s + 1);
-    if (s + 2 >= steps) return;
+  V v[AHEAD + 1];
+  load(v[0], 0);
+  if (steps == 1) return compute(v[0], 0);
+#pragma unroll
+  for (int i = 1; i < AHEAD; ++i) load(v[i], min(i, steps - 1));
+  for (int s = 0;; s += AHEAD + 1) {
+#pragma unroll
+    for (int i = 0; i <= AHEAD; ++i) {
+      load(v[(i + AHEAD) % (AHEAD + 1)], min(s + i + AHEAD, steps - 1));
+      compute(v[i], s + i);
+      if (s + i + 1 >= steps) return;
+    }
   }
 }
 

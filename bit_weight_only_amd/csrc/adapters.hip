@@ -426,7 +426,10 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
     return others(ids, (blockIdx.y - chunks) * 64, M, L, N, r, base, y, h, from, min(from + kColumns * kWaves, N));
   const Chunk c = chunk_of(offsets, L, M, rows, unit, max_steps, blockIdx.y);
   const int n0 = from + kColumns * wave;
-  if (c.a < 0 || n0 >= N) return;
+  if (c.a < 0) return;
+  __shared__ __attribute__((aligned(16))) int tokens[kMostTokens];
+  stage_tokens(perm, c, kStep, M, tokens);
+  if (n0 >= N) return;
   const int width = max(N, kNarrow);   // columns of a row of rows_of_base
   // columns n .. n + E - 1, of which those from n + own on are this lane's
   const int n = min(n0 + E * col, width - E), own = n0 + E * col - n;
@@ -438,15 +441,10 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
     Oct h[TF][RC];
     Rows<E, 4> y[TF];
     float4_t back[TF];
-    int token;   // as step_token gives them
   };
-  int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
   in_turn<Step>(
       (c.n + kStep - 1) / kStep,
       [&](Step &v, int s) {
-        v.token = token;
-        const int safe = min(max(token, 0), M - 1);
-        token = step_token(perm, c, kStep, s + 1);   // (before what it would else wait for)
 #pragma unroll
         for (int f = 0; f < TF; ++f) {
           // (a chunk's steps are whole but for the last, whose second half may be none)
@@ -454,7 +452,8 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
           if (base) {
             size_t row[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) row[i] = static_cast<size_t>(__shfl(safe, 16 * f + 4 * q + i)) * width;
+            for (int i = 0; i < 4; ++i)
+              row[i] = static_cast<size_t>(max(tokens[s * kStep + 16 * f + 4 * q + i], 0)) * width;
             load_rows(v.y[f], rows_of_base, row, n);
           } else {
             v.y[f] = Rows<E, 4>{};
@@ -476,8 +475,8 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
           bool live[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = 16 * f + 4 * q + i, to = __shfl(v.token, t);
-            live[i] = s * kStep + t < c.n && to >= 0 && to < M;
+            const int t = s * kStep + 16 * f + 4 * q + i, to = tokens[t];
+            live[i] = t < c.n && to >= 0;
             row[i] = static_cast<size_t>(max(to, 0)) * N;
           }
           add_rows<DT, E>(y, row, live, n, own, N, d, v.back[f] * sa, v.y[f]);
@@ -518,7 +517,7 @@ ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
     p.steps = std::max(1, std::min(8, static_cast<int>(static_cast<long>(spans) * g.M / 512)));
   } else {
     const long rows = static_cast<long>(g.M) * ((g.N + 64 * p.e - 1) / (64 * p.e)) / 1024;
-    p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, 128l), 1024l));
+    p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, 128l), static_cast<long>(kMostTokens)));
     p.chunks = g.M / p.rows + some;
   }
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
   __shared__ float red[kDyWaves][kStep * kStride];
   __shared__ __attribute__((aligned(16))) uint16_t tile[kDyWaves][kStep * kCols];
   __shared__ Oct hs[RF * kP * 64];
+  __shared__ __attribute__((aligned(16))) int tokens[kMostTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   if (static_cast<int>(blockIdx.y) >= chunks) {
     int lo, hi;
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
   const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
   if (c.a < 0) return;
   const int n0 = blockIdx.x * kSlice + wave * kCols;
+  stage_tokens(perm, c, kStep, M, tokens);
   // B of these columns: value 16 g + col of the columns that lie at 32 k + 8 q .. + 7 of
   // a row in LDS, zero for those that lie there twice or are none
   Oct bv[kK][RF];
@@ -230,22 +232,20 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
 #pragma unroll
       for (int d = 0; d < 4; ++d) bv[k][g].w[d] = e[2 * d] | e[2 * d + 1] << 16;
     }
+  constexpr int kAhead = 1;
   float4_t acc[E][RF] = {};
   struct Step {
     Rows<E> x;
     Shared<RF * kP, kDyWaves> h;
     float back;
   };
-  int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
-  in_turn<Step>(
+  in_turn<Step, kAhead>(
       (c.n + kStep - 1) / kStep,
       [&](Step &v, int s) {
-        const int safe = min(max(token, 0), M - 1);
-        token = step_token(perm, c, kStep, s + 1);   // (before what it would else wait for)
         const size_t step = c.step + s;
         size_t row[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(safe, 8 * q + i)) * width;
+        for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(max(tokens[s * kStep + 8 * q + i], 0)) * width;
         load_rows(v.x, dy, row, min(n0 + E * col, width - E));
         v.h.load(h.over + step * RF * kP * 64);
         if constexpr (DT == kF16) v.back = h.over_back[step];
@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     float *__restrict__ part) {
   constexpr int E = kE, kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves;
   __shared__ Oct over[RF * kP * 64], along[2 * RF * 64];
+  __shared__ __attribute__((aligned(16))) int tokens[kMostTokens];
   __shared__ int list[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const int s0 = blockIdx.x * kSlice, s1 = min(K, s0 + kSlice);
@@ -350,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
   }
   const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
   if (c.a < 0) return;
+  stage_tokens(perm, c, kStep, M, tokens);
   // (K is a multiple of 128: a wavefront's columns are all there or none is; those of
   // none go along, for the barriers, on the last ones, and store nothing)
   const bool mine = s0 + wave * kCols < K;
@@ -380,26 +382,22 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     Shared<2 * RF, kWaves> along;
     float back;
     float4_t token_back[2];
-    int token;   // as step_token gives them
   };
-  int token = step_token(perm, c, kStep, 0);   // of the step whose loads come next
   in_turn<Step>(
       (c.n + kStep - 1) / kStep,
       [&](Step &v, int s) {
         const size_t step = c.step + s;
-        v.token = token;
-        const int safe = min(max(token, 0), M - 1);
-        token = step_token(perm, c, kStep, s + 1);   // (before what it would else wait for)
+        const int *at32 = tokens + s * kStep;
         size_t row[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(__shfl(safe, 8 * q + i)) * K;
+        for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(max(at32[8 * q + i], 0)) * K;
         load_rows(v.x, x, row, k0 + E * col);
         if (base) {
 #pragma unroll
           for (int f = 0; f < 2; ++f) {
             size_t at[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) at[i] = static_cast<size_t>(__shfl(safe, 16 * f + 4 * q + i)) * K;
+            for (int i = 0; i < 4; ++i) at[i] = static_cast<size_t>(max(at32[16 * f + 4 * q + i], 0)) * K;
             load_rows(v.base[f], base, at, k0 + E * col);
           }
         } else {
@@ -457,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
           bool live[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int t = 16 * f + 4 * q + i, to = __shfl(v.token, t);
-            live[i] = mine && t < n && to >= 0 && to < M;
+            const int t = 16 * f + 4 * q + i, to = tokens[s * kStep + t];
+            live[i] = mine && t < n && to >= 0;
             at[i] = static_cast<size_t>(max(to, 0)) * K;
           }
           const float4_t back = DT == kF16 ? v.token_back[f] : float4_t{1.f, 1.f, 1.f, 1.f};
@@ -517,7 +515,7 @@ struct Plan {
 // rows'.
 int chunk_rows(int M, int slices, int slots) {
   const long rows = (static_cast<long>(M) * slices + slots - 1) / slots;
-  return static_cast<int>(std::min<long>(std::max<long>((rows + kStep - 1) / kStep * kStep, 128), 4096));
+  return static_cast<int>(std::min<long>(std::max<long>((rows + kStep - 1) / kStep * kStep, 128), kMostTokens));
 }
 
 Plan plan_of(const AdapterArgs &g) {
