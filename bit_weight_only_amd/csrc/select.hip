@@ -10,6 +10,8 @@
 #include "kernels.h"
 #include "mxfp4.h"
 
+#include <algorithm>
+
 namespace lbq {
 
 namespace {
@@ -30,254 +32,570 @@ __device__ __forceinline__ double wave_sum(double v) {
 __device__ __forceinline__ double wave_max(double v) {
   return wave_all(v, [](double a, double b) { return a > b ? a : b; });
 }
-__device__ __forceinline__ int wave_min(int v) {
-  return wave_all(v, [](int a, int b) { return a < b ? a : b; });
-}
 
-// One wavefront per token, expert e = lane + 64 i.
-template <int DT, int PER>
-__global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r, const void *__restrict__ logits, int M,
-                                                                    const float *__restrict__ bias,
-                                                                    int32_t *__restrict__ ids,
-                                                                    float *__restrict__ weights) {
+// Token t in 64 bits, by a whole wavefront: for the rare token whose order 32 bits leave
+// open (and for more groups than the fast form takes). cs, gs: LDS for E choice
+// values and the groups' values.
+template <int DT>
+__device__ __forceinline__ void select_exactly(const MoeSelect &r, const void *__restrict__ logits, int t,
+                                               const float *__restrict__ bias, double *cs, double *gs,
+                                               int32_t *__restrict__ ids, float *__restrict__ weights) {
   using T = typename Elem<DT>::type;
   const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (t >= M) return;
   const T *row = static_cast<const T *>(logits) + static_cast<size_t>(t) * r.E;
-  double l[PER], p[PER], c[PER];
-  double top = kNone;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    const float v = e < r.E ? to_f32<DT>(row[e]) : -INFINITY;
-    l[i] = v > -INFINITY ? fmin(static_cast<double>(v), 3.4028234663852886e38) : kNone;   // NaN: none
-    top = fmax(top, l[i]);
-  }
-  top = wave_max(top);
-  double sum = 0;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (r.score == kSoftmax) {
-      p[i] = l[i] > kNone ? exp(l[i] - top) : 0.;
-      sum += p[i];
-    } else {
-      p[i] = l[i] > kNone ? 1. / (1. + exp(-l[i])) : 0.;
-    }
-  }
+  auto logit = [&](int e) {   // NaN: none
+    const float v = to_f32<DT>(row[e]);
+    return v > -INFINITY ? static_cast<double>(fminf(v, 3.4028234663852886e38f)) : kNone;
+  };
+  double top = kNone, sum = 0.;
   if (r.score == kSoftmax) {
+    for (int e = lane; e < r.E; e += 64) top = fmax(top, logit(e));
+    top = wave_max(top);
+    for (int e = lane; e < r.E; e += 64) sum += logit(e) > kNone ? exp(logit(e) - top) : 0.;
     sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) p[i] = sum > 0 ? p[i] / sum : 0.;
   }
+  auto score = [&](double l) {
+    if (!(l > kNone)) return 0.;
+    return r.score == kSigmoid ? 1. / (1. + exp(-l)) : exp(l - top) / sum;
+  };
   const bool by_logit = !bias && r.groups == 1;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    const float b = bias && e < r.E ? bias[e] : 0.f;
-    c[i] = l[i] > kNone && b > -INFINITY ? (by_logit ? l[i] : p[i] + b) : kNone;
+  for (int e = lane; e < r.E; e += 64) {
+    const double l = logit(e);
+    const float b = bias ? bias[e] : 0.f;
+    cs[e] = l > kNone && b > -INFINITY ? (by_logit ? l : score(l) + b) : kNone;
   }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   if (r.groups > 1) {
     const int each = r.E / r.groups;
-    // lane g's group's value, 64 groups at a time, kept as a bit of `chosen`
-    double value[PER];   // group lane + 64 i
-#pragma unroll
-    for (int i = 0; i < PER; ++i) value[i] = kNone;
-    for (int g = 0; g < r.groups; ++g) {
-      double first = kNone, v = kNone;
-      int at = -1;
-      for (int n = 0; n < r.group_picks; ++n) {
-        double best = kNone;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const int e = lane + 64 * i;
-          if (e / each == g && e < r.E && e != at) best = fmax(best, c[i]);
-        }
-        best = wave_max(best);
-        if (n == 0) {
-          first = v = best;
-          int mine = r.E;
-#pragma unroll
-          for (int i = PER - 1; i >= 0; --i) {
-            const int e = lane + 64 * i;
-            if (e < r.E && e / each == g && c[i] == first) mine = e;
-          }
-          at = wave_min(mine);
-        } else if (best > kNone) {
-          v = first + best;
-        }
+    for (int g = lane; g < r.groups; g += 64) {
+      double first = kNone, second = kNone;
+      for (int i = 0; i < each; ++i) {
+        const double x = cs[g * each + i];
+        second = fmax(second, fmin(first, x));
+        first = fmax(first, x);
       }
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (lane + 64 * i == g) value[i] = v;
+      gs[g] = r.group_picks == 2 && second > kNone ? first + second : first;
     }
-    uint32_t chosen = 0;   // bit i: group lane + 64 i
-    for (int n = 0; n < r.top_groups; ++n) {
-      double best = kNone;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) best = fmax(best, value[i]);
-      best = wave_max(best);
-      if (best == kNone) break;
-      int mine = 64 * PER;
-#pragma unroll
-      for (int i = PER - 1; i >= 0; --i)
-        if (value[i] == best) mine = lane + 64 * i;
-      mine = wave_min(mine);
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (lane + 64 * i == mine) {
-          value[i] = kNone;
-          chosen |= 1u << i;
-        }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int g = lane; g < r.groups; g += 64) {
+      const double x = gs[g];
+      int rank = 0;
+      for (int o = 0; o < r.groups; ++o) rank += gs[o] > x || (gs[o] == x && o < g);
+      if (rank >= r.top_groups)
+        for (int i = 0; i < each; ++i) cs[g * each + i] = kNone;
     }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int g = min(lane + 64 * i, r.E - 1) / each;
-      bool kept = false;
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const uint32_t o = __shfl(chosen, g & 63);
-        if (j == (g >> 6)) kept = (o >> j) & 1;
-      }
-      if (!kept) c[i] = kNone;
-    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  // lane j keeps pick j's score
-  double mine = 0, total = 0;
+  // lane j keeps pick j
+  double mine = 0., total = 0.;
   int id = -1;
   for (int j = 0; j < r.top_k; ++j) {
     double best = kNone;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) best = fmax(best, c[i]);
-    best = wave_max(best);
-    if (best == kNone) break;
-    int e = 64 * PER;
-#pragma unroll
-    for (int i = PER - 1; i >= 0; --i)
-      if (c[i] == best) e = lane + 64 * i;
-    e = wave_min(e);
-    double s = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 64 * i == e) {
-        s = p[i];
-        c[i] = kNone;
+    int at = r.E;
+    for (int e = lane; e < r.E; e += 64)
+      if (cs[e] > best) {
+        best = cs[e];
+        at = e;
       }
-    s = __shfl(s, e & 63);
-    total += s;
-    if (lane == j) {
-      mine = s;
-      id = e;
+    for (int x = 32; x > 0; x /= 2) {
+      const double o = __shfl_xor(best, x);
+      const int oe = __shfl_xor(at, x);
+      if (o > best || (o == best && oe < at)) {
+        best = o;
+        at = oe;
+      }
     }
+    if (at >= r.E) break;
+    const double p = score(logit(at));
+    total += p;
+    if (lane == j) {
+      mine = p;
+      id = at;
+    }
+    if (lane == 0) cs[at] = kNone;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   if (lane < r.top_k) {
-    if (r.renormalise) mine = total > 0 ? mine / total : 0.;
+    if (r.renormalise) mine = total > 0. ? mine / total : 0.;
     ids[static_cast<size_t>(t) * r.top_k + lane] = id;
     weights[static_cast<size_t>(t) * r.top_k + lane] = r.scale * static_cast<float>(mine);
   }
 }
 
-// d_logits of the weights' gradient: with S = sum of the picked p (renormalised) or
-// 1, ds_j = scale (g_j - [renormalised] sum_i p_i g_i / S) / S, then the score's own
-// derivative: sigmoid p (1 - p) ds, softmax p_e (ds_e - sum p ds).
-template <int DT, int PER>
-__global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
-    MoeSelect r, const float *__restrict__ d_w, const void *__restrict__ logits, int M,
-    const int32_t *__restrict__ ids, void *__restrict__ d_logits) {
+// ------------------------------------------------------------------ rows of lanes
+
+// LANES lanes a token, V logits a lane in pieces of 16 bytes (V = 4: of four): a
+// lane's value i is expert first(i / P) + i % P. A piece that would reach past the
+// last expert starts earlier; what it has twice is left out.
+template <int DT, int LANES, int V>
+struct Row {
   using T = typename Elem<DT>::type;
-  const int lane = threadIdx.x & 63;
-  const int t = blockIdx.x * kWaves + (threadIdx.x >> 6);
-  if (t >= M) return;
-  const T *row = static_cast<const T *>(logits) + static_cast<size_t>(t) * r.E;
-  double l[PER], p[PER], ds[PER];
-  double top = kNone;
+  static constexpr int P = V == 4 ? 4 : 16 / sizeof(T), kPieces = V / P;
+  float v[V];
+  static __device__ __forceinline__ int expert(int i, int lane) { return (i / P * LANES + lane) * P + i % P; }
+  __device__ __forceinline__ void load(const T *row, int E, int lane) {
+    struct __attribute__((packed, aligned(sizeof(T)))) Piece {
+      T v[P];
+    };
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    const float v = e < r.E ? to_f32<DT>(row[e]) : -INFINITY;
-    l[i] = v > -INFINITY ? fmin(static_cast<double>(v), 3.4028234663852886e38) : kNone;
-    top = fmax(top, l[i]);
-    ds[i] = 0;
-  }
-  top = wave_max(top);
-  double sum = 0;
+    for (int k = 0; k < kPieces; ++k) {
+      const int e = (k * LANES + lane) * P, from = min(e, E - P);
+      Piece p;
+      if (E >= P) {
+        p = *reinterpret_cast<const Piece *>(row + from);
+      } else {
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    if (r.score == kSoftmax) {
-      p[i] = l[i] > kNone ? exp(l[i] - top) : 0.;
-      sum += p[i];
-    } else {
-      p[i] = l[i] > kNone ? 1. / (1. + exp(-l[i])) : 0.;
+        for (int i = 0; i < P; ++i) p.v[i] = row[min(e + i, E - 1)];
+      }
+      const int skip = E >= P ? e - from : 0;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        // value i is expert e + i: at i + skip of the piece
+        T x = p.v[i];
+        if (skip > 0) {
+#pragma unroll
+          for (int j = 0; j < P; ++j)
+            if (j == i + skip) x = p.v[j];
+        }
+        const float f = to_f32<DT>(x);
+        // NaN and experts past the last: none
+        v[k * P + i] = e + i < E && f > -INFINITY ? fminf(f, 3.4028234663852886e38f) : -INFINITY;
+      }
     }
   }
-  if (r.score == kSoftmax) {
-    sum = wave_sum(sum);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) p[i] = sum > 0 ? p[i] / sum : 0.;
+};
+
+// Over the LANES lanes of a token, in each of them.
+template <int LANES, class F>
+__device__ __forceinline__ float row_all(float v, F f) {
+  v = f(v, __uint_as_float(xor_lane_u32<1>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(xor_lane_u32<2>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(xor_lane_u32<4>(__float_as_uint(v))));
+  v = f(v, __uint_as_float(xor_lane_u32<8>(__float_as_uint(v))));
+  if constexpr (LANES == 64) {
+    v = f(v, __uint_as_float(xor_lane_u32<16>(__float_as_uint(v))));
+    v = f(v, __uint_as_float(xor_lane_u32<32>(__float_as_uint(v))));
   }
-  // the picks' scores and their sums
-  double S = 0, dot = 0;
-  for (int j = 0; j < r.top_k; ++j) {
-    const int e = ids[static_cast<size_t>(t) * r.top_k + j];
-    if (e < 0 || e >= r.E) continue;
-    double s = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i == (e >> 6)) s = p[i];
-    s = __shfl(s, e & 63);
-    S += s;
-    dot += s * d_w[static_cast<size_t>(t) * r.top_k + j];
+  return v;
+}
+template <int LANES>
+__device__ __forceinline__ float row_max(float v) {
+  return row_all<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+template <int LANES>
+__device__ __forceinline__ float row_sum(float v) {
+  return row_all<LANES>(v, [](float a, float b) { return a + b; });
+}
+
+// A choice value and its expert as one double that orders like the pair, larger
+// values first and of equal ones the lower expert: the whole number (value's order
+// << 10 | 1023 - expert) added to 2^52. One instruction compares it; 0 is none.
+__device__ __forceinline__ double pair_of(float c, int e) {
+  const uint32_t b = __float_as_uint(c + 0.f);   // -0 as 0
+  const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
+  return __hiloint2double(static_cast<int>(0x43300000u | o >> 22), static_cast<int>(o << 10 | (1023u - e)));
+}
+__device__ __forceinline__ int expert_of(double d) { return 1023 - (__double2loint(d) & 1023); }
+__device__ __forceinline__ float value_of(double d) {
+  const uint32_t o = static_cast<uint32_t>(__double2hiint(d)) << 22 | static_cast<uint32_t>(__double2loint(d)) >> 10;
+  return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
+}
+template <int X>
+__device__ __forceinline__ double max_xor(double v) {
+  return __builtin_fmax(v, __hiloint2double(static_cast<int>(xor_lane_u32<X>(static_cast<uint32_t>(__double2hiint(v)))),
+                                            static_cast<int>(xor_lane_u32<X>(static_cast<uint32_t>(__double2loint(v))))));
+}
+template <int LANES>
+__device__ __forceinline__ double row_best(double v) {
+  v = max_xor<1>(v);
+  v = max_xor<2>(v);
+  v = max_xor<4>(v);
+  v = max_xor<8>(v);
+  if constexpr (LANES == 64) {
+    v = max_xor<16>(v);
+    v = max_xor<32>(v);
   }
-  const double inv = r.renormalise ? (S > 0 ? 1. / S : 0.) : 1.;
-  for (int j = 0; j < r.top_k; ++j) {
-    const int e = ids[static_cast<size_t>(t) * r.top_k + j];
-    if (e < 0 || e >= r.E) continue;
-    const double g = d_w[static_cast<size_t>(t) * r.top_k + j];
+  return v;
+}
+
+// Larger first: an odd-even merge network.
+template <int V>
+__device__ __forceinline__ void sort_down(double (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane + 64 * i == e) ds[i] += r.scale * inv * (r.renormalise ? g - dot * inv : g);
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < V && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const double a = v[i + j], b = v[i + j + k];
+            v[i + j] = __builtin_fmax(a, b);
+            v[i + j + k] = __builtin_fmin(a, b);
+          }
+}
+
+__device__ __forceinline__ float score_of(float l, int score, float top) {
+  if (score == kSigmoid) return __builtin_amdgcn_rcpf(1.f + expf(-l));
+  return expf(l - top);
+}
+
+constexpr int kMostGroups = 64;
+
+// Each lane sorts its values once; then the heads of the lanes' lists are compared,
+// and the winner's next value comes from LDS.
+//
+// 32 bits decide, but where two neighbours among the picks, or the last pick and
+// the next, or the last group kept and the next, lie nearer than 32 bits can tell:
+// then the token is done again in 64. A score is off by at most 2^-20 of the row's
+// largest (exp and the reciprocal a few roundings each; softmax's argument by
+// |l - top| 2^-24, where p falls with e^(top - l)), the sum with the bias by 2^-24 of
+// itself; `near` is twice that and more.
+//
+// What bounds it is instructions: 4 tokens a wavefront, (top_k + 1) rounds.
+template <int DT, int LANES, int V>
+__global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r, const void *__restrict__ logits, int M,
+                                                                    const float *__restrict__ bias,
+                                                                    int32_t *__restrict__ ids,
+                                                                    float *__restrict__ weights) {
+  using T = typename Elem<DT>::type;
+  using R = Row<DT, LANES, V>;
+  constexpr int kTokens = 64 / LANES;   // of a wavefront
+  __shared__ double lists[kWaves][V * 64];
+  __shared__ double picks[kWaves][kTokens][kMoeMaxTopK + 2];
+  __shared__ float groups[kWaves][kTokens][kMostGroups];
+  __shared__ double exact_groups[kWaves][kMostGroups];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & (LANES - 1), mine = (threadIdx.x & 63) / LANES;
+  double *list = lists[wave] + (threadIdx.x & 63);
+  double *pick = picks[wave][mine];
+  const bool by_logit = !bias && r.groups == 1;
+  const bool whole = r.score == kSoftmax && (!by_logit || !r.renormalise);   // all scores of a row are needed
+  float b[V], most = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = R::expert(i, lane);
+    b[i] = bias && e < r.E ? bias[e] : 0.f;
+    b[i] = b[i] > -INFINITY ? b[i] : -INFINITY;
+    if (fabsf(b[i]) < INFINITY) most = fmaxf(most, fabsf(b[i]));
   }
-  double across = 0;
-  if (r.score == kSoftmax) {
+  most = row_max<LANES>(most);
+  const int each = r.E / r.groups;
+  const uint32_t inverse = ((1u << 20) + each - 1) / each;   // e / each = e inverse >> 20 for e < 1024
+  for (int t0 = (blockIdx.x * kWaves + wave) * kTokens; t0 < M; t0 += gridDim.x * kWaves * kTokens) {
+    const int t = min(t0 + mine, M - 1);
+    const T *row = static_cast<const T *>(logits) + static_cast<size_t>(t) * r.E;
+    R l;
+    l.load(row, r.E, lane);
+    float top = 0.f, inv = 1.f;
+    if (r.score == kSoftmax) {
+      top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) across += p[i] * ds[i];
-    across = wave_sum(across);
+      for (int i = 0; i < V; ++i) top = fmaxf(top, l.v[i]);
+      top = row_max<LANES>(top);
+    }
+    float c[V];
+    if (by_logit) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = l.v[i];
+    }
+    if (whole || !by_logit) {
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float p = l.v[i] > -INFINITY ? score_of(l.v[i], r.score, top) : 0.f;
+        sum += p;
+        if (!by_logit) c[i] = p;
+      }
+      if (r.score == kSoftmax) {
+        sum = row_sum<LANES>(sum);
+        inv = sum > 0.f ? 1.f / sum : 0.f;
+      }
+      if (!by_logit) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = l.v[i] > -INFINITY && b[i] > -INFINITY ? c[i] * inv + b[i] : -INFINITY;
+      }
+    }
+    const float near = 0x1p-18f * (r.score == kSoftmax ? inv : 1.f) + 0x1p-21f * most;
+    bool open = false;
+    if (r.groups > 1) {
+      // the choice values in LDS; a lane per group adds up its largest
+      float *cs = reinterpret_cast<float *>(lists[wave]) + mine * (LANES * V);
+#pragma unroll
+      for (int i = 0; i < V; ++i) cs[R::expert(i, lane)] = c[i];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      float *gs = groups[wave][mine];
+      for (int g = lane; g < r.groups; g += LANES) {
+        float first = -INFINITY, second = -INFINITY;
+        for (int i = 0; i < each; ++i) {
+          const float x = cs[g * each + i];
+          second = fmaxf(second, fminf(first, x));
+          first = fmaxf(first, x);
+        }
+        gs[g] = r.group_picks == 2 && second > -INFINITY ? first + second : first;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // a group's rank; the last one kept and the next
+      float last = -INFINITY, next = -INFINITY;
+      uint64_t kept = 0;
+      for (int g = lane; g < r.groups; g += LANES) {
+        const float x = gs[g];
+        int rank = 0;
+        for (int o = 0; o < r.groups; ++o) {
+          const float y = gs[o];
+          rank += y > x || (y == x && o < g);
+        }
+        if (rank < r.top_groups && x > -INFINITY) kept |= 1ull << g;
+        if (rank == r.top_groups - 1) last = x;
+        if (rank == r.top_groups) next = x;
+      }
+      last = row_max<LANES>(last);
+      next = row_max<LANES>(next);
+      open = next > -INFINITY && !(last - next > 2.f * near);
+      uint32_t lo = static_cast<uint32_t>(kept), hi = static_cast<uint32_t>(kept >> 32);
+#pragma unroll
+      for (int d = 1; d < LANES; d *= 2) {
+        lo |= __shfl_xor(lo, d);
+        hi |= __shfl_xor(hi, d);
+      }
+      kept = static_cast<uint64_t>(hi) << 32 | lo;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const uint32_t g = static_cast<uint32_t>(R::expert(i, lane)) * inverse >> 20;
+        if (!(kept >> (g & 63) & 1)) c[i] = -INFINITY;
+      }
+    }
+    double s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = c[i] > -INFINITY ? pair_of(c[i], R::expert(i, lane)) : 0.;
+    sort_down<V>(s);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+    for (int i = 1; i < V; ++i) list[64 * i] = s[i];
+    double head = s[0];
+    int at = 1;
+    // one round more than picks, for the one that was not taken
+    for (int j = 0; j < r.top_k + !by_logit; ++j) {
+      const double best = row_best<LANES>(head);
+      if (lane == 0) pick[j] = best;
+      if (head == best && best != 0.) {
+        head = at < V ? list[64 * at] : 0.;
+        ++at;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    float p[2] = {0.f, 0.f}, total = 0.f;
+    int id[2] = {-1, -1};
+#pragma unroll
+    for (int n = 0; n < (LANES == 16 ? 2 : 1); ++n) {
+      const int j = lane + LANES * n;
+      if (j >= r.top_k || pick[j] == 0.) continue;
+      id[n] = expert_of(pick[j]);
+      const float x = fminf(to_f32<DT>(row[id[n]]), 3.4028234663852886e38f);
+      p[n] = score_of(x, r.score, top);
+      if (!by_logit && pick[j + 1] != 0. && !(value_of(pick[j]) - value_of(pick[j + 1]) > near)) {
+        // as near as that, but for the same logit and bias
+        const int o = expert_of(pick[j + 1]);
+        const float y = fminf(to_f32<DT>(row[o]), 3.4028234663852886e38f);
+        open = open || x != y || (bias && bias[id[n]] != bias[o]);
+      }
+      total += p[n];
+    }
+    total = row_sum<LANES>(total);
+    // (sigmoids that 32 bits cannot hold still have a ratio)
+    open = open || (r.score == kSigmoid && r.renormalise && total < 0x1p-60f && pick[0] != 0.);
+    const float factor = r.scale * (!r.renormalise ? inv : total > 0.f ? 1.f / total : 0.f);
+    const uint64_t opens = __ballot(open);
+    constexpr uint64_t kRow = LANES == 64 ? ~0ull : (1ull << (LANES & 63)) - 1;
+    if (t0 + mine < M && !(opens >> (mine * LANES) & kRow)) {
+#pragma unroll
+      for (int n = 0; n < (LANES == 16 ? 2 : 1); ++n) {
+        const int j = lane + LANES * n;
+        if (j >= r.top_k) continue;
+        ids[static_cast<size_t>(t) * r.top_k + j] = id[n];
+        weights[static_cast<size_t>(t) * r.top_k + j] = p[n] * factor;
+      }
+    }
+    for (int n = 0; n < kTokens; ++n)
+      if (t0 + n < M && (opens >> (n * LANES) & kRow))
+        select_exactly<DT>(r, logits, t0 + n, bias, lists[wave], exact_groups[wave], ids, weights);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  T *out = static_cast<T *>(d_logits) + static_cast<size_t>(t) * r.E;
+}
+
+// All tokens in 64 bits.
+template <int DT>
+__global__ void __launch_bounds__(kSelectThreads) moe_select_exact_kernel(MoeSelect r, const void *__restrict__ logits,
+                                                                          int M, const float *__restrict__ bias,
+                                                                          int32_t *__restrict__ ids,
+                                                                          float *__restrict__ weights) {
+  __shared__ double cs[kWaves][kMoeMaxExperts], gs[kWaves][kMoeMaxExperts];
+  const int wave = threadIdx.x >> 6, t = blockIdx.x * kWaves + wave;
+  if (t < M) select_exactly<DT>(r, logits, t, bias, cs[wave], gs[wave], ids, weights);
+}
+
+// ------------------------------------------------------------------ gradient
+
+// d_logits of the weights' gradient: with S = sum of the picked p (renormalised) or
+// 1, ds_j = scale (g_j - [renormalised] sum_i p_i g_i / S) / S, then the score's own
+// derivative: sigmoid p (1 - p) ds, softmax p_e (ds_e - sum p ds). With renormalised
+// softmax the last sum is zero, and the logits that were not picked fall out of it: so
+// but for plain softmax a token's row is zeros and a few values, and of the logits
+// only the picked are read. What bounds it then is writing the rows.
+//
+// 16 lanes a token; the row is put together in LDS, slot after slot, so that an expert
+// named twice gets both.
+template <int DT, int V>
+__global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
+    MoeSelect r, const float *__restrict__ d_w, const void *logits, int M, const int32_t *__restrict__ ids,
+    void *d_logits) {
+  using T = typename Elem<DT>::type;
+  constexpr int kLanes = 16, kTokens = 4, kRow = kLanes * V;   // E <= kRow
+  __shared__ float rows[kWaves][kTokens][kRow];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 15, mine = (threadIdx.x & 63) / kLanes;
+  const bool dense = r.score == kSoftmax && !r.renormalise;
+  float *d = rows[wave][mine];
+  for (int t0 = (blockIdx.x * kWaves + wave) * kTokens; t0 < M; t0 += gridDim.x * kWaves * kTokens) {
+    const int t = min(t0 + mine, M - 1);
+    const T *row = static_cast<const T *>(logits) + static_cast<size_t>(t) * r.E;
+    auto logit = [&](int e) {   // NaN: none
+      const float v = to_f32<DT>(row[e]);
+      return v > -INFINITY ? fminf(v, 3.4028234663852886e38f) : -INFINITY;
+    };
+    int id[2];
+    float l[2], g[2], top = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane + 64 * i;
-    double d = 0;
-    if (l[i] > kNone) d = r.score == kSoftmax ? p[i] * (ds[i] - across) : ds[i] * p[i] * (1. / (1. + exp(l[i])));
-    if (e < r.E) out[e] = from_f32<DT>(static_cast<float>(d));
+    for (int n = 0; n < 2; ++n) {
+      const int j = lane + kLanes * n;
+      id[n] = j < r.top_k ? ids[static_cast<size_t>(t) * r.top_k + j] : -1;
+      if (id[n] < 0 || id[n] >= r.E) id[n] = -1;
+      l[n] = id[n] >= 0 ? logit(id[n]) : -INFINITY;
+      g[n] = id[n] >= 0 ? d_w[static_cast<size_t>(t) * r.top_k + j] : 0.f;
+      top = fmaxf(top, l[n]);
+    }
+    float inv = 1.f;
+    if (dense) {
+      float sum = 0.f;
+      top = -INFINITY;
+      for (int e = lane; e < r.E; e += kLanes) top = fmaxf(top, logit(e));
+      top = row_max<kLanes>(top);
+      for (int e = lane; e < r.E; e += kLanes) {
+        const float x = logit(e);
+        const float p = x > -INFINITY ? expf(x - top) : 0.f;
+        d[e] = p;
+        sum += p;
+      }
+      sum = row_sum<kLanes>(sum);
+      inv = sum > 0.f ? 1.f / sum : 0.f;
+    } else {
+      top = row_max<kLanes>(top);
+      for (int e = lane; e < r.E; e += kLanes) d[e] = 0.f;
+    }
+    float p[2], S = 0.f, dot = 0.f;
+    // sigmoids are taken relative to the largest where 32 bits cannot hold them
+    // themselves: below -60 they fall like exp(l)
+    const bool far = r.score == kSigmoid && r.renormalise && top < -60.f && top > -INFINITY;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      p[n] = !(l[n] > -INFINITY) ? 0.f : far ? expf(l[n] - top) : score_of(l[n], r.score, top) * inv;
+      S += p[n];
+      dot += p[n] * g[n];
+    }
+    S = row_sum<kLanes>(S);
+    dot = row_sum<kLanes>(dot);
+    const float over = !r.renormalise ? 1.f : S > 0.f && (!far || top > -745.f) ? 1.f / S : 0.f;
+    const float mean = r.renormalise ? dot * over : 0.f;
+    float across = 0.f;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      g[n] = id[n] >= 0 ? r.scale * over * (g[n] - mean) : 0.f;   // ds of the slot
+      if (dense) across += p[n] * g[n];
+      else g[n] *= p[n] * (r.score == kSigmoid && !far ? __builtin_amdgcn_rcpf(1.f + expf(l[n])) : 1.f);
+    }
+    if (dense) {
+      across = row_sum<kLanes>(across);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      // p first, as -p sum p ds; the picked ones' p ds follow
+      for (int e = lane; e < r.E; e += kLanes) d[e] *= -inv * across;
+#pragma unroll
+      for (int n = 0; n < 2; ++n) g[n] *= p[n];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int j = 0; j < r.top_k; ++j) {
+      const int n = j / kLanes;
+      if (lane == j % kLanes && (n ? id[1] : id[0]) >= 0) d[n ? id[1] : id[0]] += n ? g[1] : g[0];
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    if (t0 + mine < M) {
+      T *out = static_cast<T *>(d_logits) + static_cast<size_t>(t) * r.E;
+      struct __attribute__((packed, aligned(sizeof(T)))) Piece {
+        T v[16 / sizeof(T)];
+      };
+      constexpr int P = 16 / sizeof(T);
+      for (int e = lane * P; e < r.E; e += kLanes * P) {
+        if (e + P <= r.E) {
+          Piece o;
+#pragma unroll
+          for (int i = 0; i < P; ++i) o.v[i] = from_f32<DT>(d[e + i]);
+          *reinterpret_cast<Piece *>(out + e) = o;
+        } else {
+          for (int i = e; i < r.E; ++i) out[i] = from_f32<DT>(d[i]);
+        }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
 
 }  // namespace
 
-#define LBQ_SELECT_PER(DT, KERNEL, ...)                                                         \
-  do {                                                                                          \
-    if (r.E <= 64) hipLaunchKernelGGL((KERNEL<DT, 1>), grid, block, 0, s, __VA_ARGS__);         \
-    else if (r.E <= 256) hipLaunchKernelGGL((KERNEL<DT, 4>), grid, block, 0, s, __VA_ARGS__);   \
-    else hipLaunchKernelGGL((KERNEL<DT, 16>), grid, block, 0, s, __VA_ARGS__);                  \
-  } while (0)
-#define LBQ_SELECT(KERNEL, ...)                                              \
-  do {                                                                       \
-    const dim3 grid((M + kWaves - 1) / kWaves), block(kSelectThreads);       \
-    if (dtype == kF16) LBQ_SELECT_PER(kF16, KERNEL, __VA_ARGS__);            \
-    else if (dtype == kBF16) LBQ_SELECT_PER(kBF16, KERNEL, __VA_ARGS__);     \
-    else LBQ_SELECT_PER(kF32, KERNEL, __VA_ARGS__);                          \
-  } while (0)
+// tokens of a wavefront times its workgroup's four, and at most so many workgroups
+// that the bias is loaded a few times only
+static unsigned select_blocks(int M, int tokens) {
+  const int per = kWaves * tokens;
+  return static_cast<unsigned>(std::min((M + per - 1) / per, 4096));
+}
+
+template <int DT>
+static void select_go(const MoeSelect &r, const void *logits, int M, const float *bias, int32_t *ids, float *weights,
+                      hipStream_t s) {
+  const dim3 block(kSelectThreads);
+  if (r.groups > kMostGroups)
+    hipLaunchKernelGGL(moe_select_exact_kernel<DT>, dim3((M + kWaves - 1) / kWaves), block, 0, s, r, logits, M, bias, ids,
+                       weights);
+  else if (r.E <= 64)
+    hipLaunchKernelGGL((moe_select_kernel<DT, 16, 4>), dim3(select_blocks(M, 4)), block, 0, s, r, logits, M, bias, ids,
+                       weights);
+  else if (r.E <= 256)
+    hipLaunchKernelGGL((moe_select_kernel<DT, 16, 16>), dim3(select_blocks(M, 4)), block, 0, s, r, logits, M, bias, ids,
+                       weights);
+  else
+    hipLaunchKernelGGL((moe_select_kernel<DT, 64, 16>), dim3(select_blocks(M, 1)), block, 0, s, r, logits, M, bias, ids,
+                       weights);
+}
+
+template <int DT>
+static void select_backward_go(const MoeSelect &r, const float *d_w, const void *logits, int M, const int32_t *ids,
+                               void *d_logits, hipStream_t s) {
+  const dim3 grid(select_blocks(M, 4)), block(kSelectThreads);
+  if (r.E <= 64) hipLaunchKernelGGL((moe_select_backward_kernel<DT, 4>), grid, block, 0, s, r, d_w, logits, M, ids, d_logits);
+  else if (r.E <= 256) hipLaunchKernelGGL((moe_select_backward_kernel<DT, 16>), grid, block, 0, s, r, d_w, logits, M, ids, d_logits);
+  else hipLaunchKernelGGL((moe_select_backward_kernel<DT, 64>), grid, block, 0, s, r, d_w, logits, M, ids, d_logits);
+}
 
 hipError_t launch_moe_select(const MoeSelect &r, const void *logits, int dtype, int M, const float *bias, int32_t *ids,
                              float *weights, hipStream_t s) {
-  LBQ_SELECT(moe_select_kernel, r, logits, M, bias, ids, weights);
+  if (dtype == kF16) select_go<kF16>(r, logits, M, bias, ids, weights, s);
+  else if (dtype == kBF16) select_go<kBF16>(r, logits, M, bias, ids, weights, s);
+  else select_go<kF32>(r, logits, M, bias, ids, weights, s);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_select_backward(const MoeSelect &r, const float *d_w, const void *logits, int dtype, int M,
                                       const int32_t *ids, void *d_logits, hipStream_t s) {
-  LBQ_SELECT(moe_select_backward_kernel, r, d_w, logits, M, ids, d_logits);
+  if (dtype == kF16) select_backward_go<kF16>(r, d_w, logits, M, ids, d_logits, s);
+  else if (dtype == kBF16) select_backward_go<kBF16>(r, d_w, logits, M, ids, d_logits, s);
+  else select_backward_go<kF32>(r, d_w, logits, M, ids, d_logits, s);
   return hipGetLastError();
 }
 
