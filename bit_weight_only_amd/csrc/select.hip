@@ -21,18 +21,42 @@ using namespace mxfp4;
 constexpr int kSelectThreads = 256, kWaves = kSelectThreads / 64;
 constexpr double kNone = -__builtin_inf();
 
-template <class T, class F>
-__device__ __forceinline__ T wave_all(T v, F f) {
-  for (int x = 32; x > 0; x /= 2) v = f(v, __shfl_xor(v, x));
+// Value of the lane N further round in its row of 16.
+template <int N>
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x120 + N, 0xF, 0xF, false));
+}
+template <int N>
+__device__ __forceinline__ float turned(float v) {
+  return __uint_as_float(turned<N>(__float_as_uint(v)));
+}
+template <int N>
+__device__ __forceinline__ double turned(double v) {
+  return __hiloint2double(static_cast<int>(turned<N>(static_cast<uint32_t>(__double2hiint(v)))),
+                          static_cast<int>(turned<N>(static_cast<uint32_t>(__double2loint(v)))));
+}
+template <int X>
+__device__ __forceinline__ float crossed(float v) {
+  return __uint_as_float(xor_lane_u32<X>(__float_as_uint(v)));
+}
+template <int X>
+__device__ __forceinline__ double crossed(double v) {
+  return __hiloint2double(static_cast<int>(xor_lane_u32<X>(static_cast<uint32_t>(__double2hiint(v)))),
+                          static_cast<int>(xor_lane_u32<X>(static_cast<uint32_t>(__double2loint(v)))));
+}
+// Over the LANES lanes of a token, in each of them.
+template <int LANES, class T, class F>
+__device__ __forceinline__ T row_all(T v, F f) {
+  v = f(v, turned<8>(v));
+  v = f(v, turned<4>(v));
+  v = f(v, turned<2>(v));
+  v = f(v, turned<1>(v));
+  if constexpr (LANES == 64) {
+    v = f(v, crossed<16>(v));
+    v = f(v, crossed<32>(v));
+  }
   return v;
 }
-__device__ __forceinline__ double wave_sum(double v) {
-  return wave_all(v, [](double a, double b) { return a + b; });
-}
-__device__ __forceinline__ double wave_max(double v) {
-  return wave_all(v, [](double a, double b) { return a > b ? a : b; });
-}
-
 // Token t in 64 bits, by a whole wavefront: for the rare token whose order 32 bits leave
 // open (and for more groups than the fast form takes). cs, gs: LDS for E choice
 // values and the groups' values.
@@ -50,9 +74,9 @@ __device__ __forceinline__ void select_exactly(const MoeSelect &r, const void *_
   double top = kNone, sum = 0.;
   if (r.score == kSoftmax) {
     for (int e = lane; e < r.E; e += 64) top = fmax(top, logit(e));
-    top = wave_max(top);
+    top = row_all<64>(top, [](double a, double b) { return fmax(a, b); });
     for (int e = lane; e < r.E; e += 64) sum += logit(e) > kNone ? exp(logit(e) - top) : 0.;
-    sum = wave_sum(sum);
+    sum = row_all<64>(sum, [](double a, double b) { return a + b; });
   }
   auto score = [&](double l) {
     if (!(l > kNone)) return 0.;
@@ -87,7 +111,6 @@ __device__ __forceinline__ void select_exactly(const MoeSelect &r, const void *_
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   // lane j keeps pick j
-  double mine = 0., total = 0.;
   int id = -1;
   for (int j = 0; j < r.top_k; ++j) {
     double best = kNone;
@@ -97,24 +120,16 @@ __device__ __forceinline__ void select_exactly(const MoeSelect &r, const void *_
         best = cs[e];
         at = e;
       }
-    for (int x = 32; x > 0; x /= 2) {
-      const double o = __shfl_xor(best, x);
-      const int oe = __shfl_xor(at, x);
-      if (o > best || (o == best && oe < at)) {
-        best = o;
-        at = oe;
-      }
-    }
+    const double all = row_all<64>(best, [](double a, double b) { return fmax(a, b); });
+    // the lowest of those that have it: as a float, exact below 2^24
+    at = static_cast<int>(row_all<64>(best == all ? static_cast<float>(at) : 1e6f, [](float a, float b) { return fminf(a, b); }));
     if (at >= r.E) break;
-    const double p = score(logit(at));
-    total += p;
-    if (lane == j) {
-      mine = p;
-      id = at;
-    }
+    if (lane == j) id = at;
     if (lane == 0) cs[at] = kNone;
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
+  double mine = id >= 0 ? score(logit(id)) : 0.;
+  const double total = row_all<64>(mine, [](double a, double b) { return a + b; });
   if (lane < r.top_k) {
     if (r.renormalise) mine = total > 0. ? mine / total : 0.;
     ids[static_cast<size_t>(t) * r.top_k + lane] = id;
@@ -157,27 +172,17 @@ struct Row {
           for (int j = 0; j < P; ++j)
             if (j == i + skip) x = p.v[j];
         }
-        const float f = to_f32<DT>(x);
-        // NaN and experts past the last: none
-        v[k * P + i] = e + i < E && f > -INFINITY ? fminf(f, 3.4028234663852886e38f) : -INFINITY;
+        // NaN is none
+        v[k * P + i] = fminf(fmaxf(to_f32<DT>(x), -INFINITY), 3.4028234663852886e38f);
+      }
+      if (E < LANES * V) {   // experts past the last: none
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[k * P + i] = e + i < E ? v[k * P + i] : -INFINITY;
       }
     }
   }
 };
 
-// Over the LANES lanes of a token, in each of them.
-template <int LANES, class F>
-__device__ __forceinline__ float row_all(float v, F f) {
-  v = f(v, __uint_as_float(xor_lane_u32<1>(__float_as_uint(v))));
-  v = f(v, __uint_as_float(xor_lane_u32<2>(__float_as_uint(v))));
-  v = f(v, __uint_as_float(xor_lane_u32<4>(__float_as_uint(v))));
-  v = f(v, __uint_as_float(xor_lane_u32<8>(__float_as_uint(v))));
-  if constexpr (LANES == 64) {
-    v = f(v, __uint_as_float(xor_lane_u32<16>(__float_as_uint(v))));
-    v = f(v, __uint_as_float(xor_lane_u32<32>(__float_as_uint(v))));
-  }
-  return v;
-}
 template <int LANES>
 __device__ __forceinline__ float row_max(float v) {
   return row_all<LANES>(v, [](float a, float b) { return fmaxf(a, b); });
@@ -189,33 +194,22 @@ __device__ __forceinline__ float row_sum(float v) {
 
 // A choice value and its expert as one double that orders like the pair, larger
 // values first and of equal ones the lower expert: the whole number (value's order
-// << 10 | 1023 - expert) added to 2^52. One instruction compares it; 0 is none.
+// << 10 | 1023 - expert) added to 2^52. One instruction compares it. What is below
+// kFirst is the value -infinity: none.
 __device__ __forceinline__ double pair_of(float c, int e) {
   const uint32_t b = __float_as_uint(c + 0.f);   // -0 as 0
-  const uint32_t o = b & 0x80000000u ? ~b : b | 0x80000000u;
+  const uint32_t o = b ^ (static_cast<uint32_t>(static_cast<int>(b) >> 31) | 0x80000000u);
   return __hiloint2double(static_cast<int>(0x43300000u | o >> 22), static_cast<int>(o << 10 | (1023u - e)));
 }
+constexpr double kFirst = 4503599627370496. + 8388608. * 1024.;   // 2^52 + (0x00800000 << 10)
 __device__ __forceinline__ int expert_of(double d) { return 1023 - (__double2loint(d) & 1023); }
 __device__ __forceinline__ float value_of(double d) {
   const uint32_t o = static_cast<uint32_t>(__double2hiint(d)) << 22 | static_cast<uint32_t>(__double2loint(d)) >> 10;
   return __uint_as_float(o & 0x80000000u ? o & 0x7FFFFFFFu : ~o);
 }
-template <int X>
-__device__ __forceinline__ double max_xor(double v) {
-  return __builtin_fmax(v, __hiloint2double(static_cast<int>(xor_lane_u32<X>(static_cast<uint32_t>(__double2hiint(v)))),
-                                            static_cast<int>(xor_lane_u32<X>(static_cast<uint32_t>(__double2loint(v))))));
-}
 template <int LANES>
 __device__ __forceinline__ double row_best(double v) {
-  v = max_xor<1>(v);
-  v = max_xor<2>(v);
-  v = max_xor<4>(v);
-  v = max_xor<8>(v);
-  if constexpr (LANES == 64) {
-    v = max_xor<16>(v);
-    v = max_xor<32>(v);
-  }
-  return v;
+  return row_all<LANES>(v, [](double a, double b) { return __builtin_fmax(a, b); });
 }
 
 // Larger first: an odd-even merge network.
@@ -241,6 +235,14 @@ __device__ __forceinline__ float score_of(float l, int score, float top) {
   return expf(l - top);
 }
 
+// The same for the order alone: the argument's rounding counts for little, since p falls
+// faster than it grows (x p (1 - p) and x exp(-x) stay below 0.4).
+__device__ __forceinline__ float rough_score(float l, int score, float top) {
+  constexpr float kLog2E = 1.44269504f;
+  if (score == kSigmoid) return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2E * l));
+  return __builtin_amdgcn_exp2f(kLog2E * (l - top));
+}
+
 constexpr int kMostGroups = 64;
 
 // Each lane sorts its values once; then the heads of the lanes' lists are compared,
@@ -248,14 +250,15 @@ constexpr int kMostGroups = 64;
 //
 // 32 bits decide, but where two neighbours among the picks, or the last pick and
 // the next, or the last group kept and the next, lie nearer than 32 bits can tell:
-// then the token is done again in 64. A score is off by at most 2^-20 of the row's
-// largest (exp and the reciprocal a few roundings each; softmax's argument by
-// |l - top| 2^-24, where p falls with e^(top - l)), the sum with the bias by 2^-24 of
-// itself; `near` is twice that and more.
+// then the token is done again in 64. In units u = 2^-24: a sigmoid is off by at most
+// 4 u (exp's argument 0.5, exp 0.5, the sum 1, the reciprocal 2) and the sum with the
+// bias by u (1 + |b|), so that a difference is off by 10 u + 2 u |b|; a softmax by 4 u of the
+// row's largest score, and all of them together by their sum's up to 24 u; `near` is
+// twice the one and more than the other.
 //
 // What bounds it is instructions: 4 tokens a wavefront, (top_k + 1) rounds.
 template <int DT, int LANES, int V>
-__global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r, const void *__restrict__ logits, int M,
+__global__ void __launch_bounds__(kSelectThreads, 3) moe_select_kernel(MoeSelect r, const void *__restrict__ logits, int M,
                                                                     const float *__restrict__ bias,
                                                                     int32_t *__restrict__ ids,
                                                                     float *__restrict__ weights) {
@@ -263,12 +266,11 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r,
   using R = Row<DT, LANES, V>;
   constexpr int kTokens = 64 / LANES;   // of a wavefront
   __shared__ double lists[kWaves][V * 64];
-  __shared__ double picks[kWaves][kTokens][kMoeMaxTopK + 2];
-  __shared__ float groups[kWaves][kTokens][kMostGroups];
-  __shared__ double exact_groups[kWaves][kMostGroups];
+  constexpr int kPicks = kMoeMaxTopK + 2;
+  __shared__ double picks[kWaves][kTokens * kPicks > kMostGroups ? kTokens * kPicks : kMostGroups];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & (LANES - 1), mine = (threadIdx.x & 63) / LANES;
   double *list = lists[wave] + (threadIdx.x & 63);
-  double *pick = picks[wave][mine];
+  double *pick = picks[wave] + mine * kPicks;
   const bool by_logit = !bias && r.groups == 1;
   const bool whole = r.score == kSoftmax && (!by_logit || !r.renormalise);   // all scores of a row are needed
   float b[V], most = 0.f;
@@ -285,8 +287,12 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r,
   for (int t0 = (blockIdx.x * kWaves + wave) * kTokens; t0 < M; t0 += gridDim.x * kWaves * kTokens) {
     const int t = min(t0 + mine, M - 1);
     const T *row = static_cast<const T *>(logits) + static_cast<size_t>(t) * r.E;
+    // (a number that the compiler does not know to be the same every time: it would
+    // keep what follows from it, a register or a mask per value)
+    int here = lane;
+    asm volatile("" : "+v"(here));
     R l;
-    l.load(row, r.E, lane);
+    l.load(row, r.E, here);
     float top = 0.f, inv = 1.f;
     if (r.score == kSoftmax) {
       top = -INFINITY;
@@ -300,31 +306,36 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r,
       for (int i = 0; i < V; ++i) c[i] = l.v[i];
     }
     if (whole || !by_logit) {
-      float sum = 0.f;
+      // what is none has a score of 0 by itself (or, with nothing else there, NaN)
+      float p[V];
+      if (r.score == kSigmoid) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float p = l.v[i] > -INFINITY ? score_of(l.v[i], r.score, top) : 0.f;
-        sum += p;
-        if (!by_logit) c[i] = p;
-      }
-      if (r.score == kSoftmax) {
+        for (int i = 0; i < V; ++i) p[i] = rough_score(l.v[i], kSigmoid, 0.f);
+      } else {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          p[i] = rough_score(l.v[i], kSoftmax, top);
+          sum += p[i];
+        }
         sum = row_sum<LANES>(sum);
         inv = sum > 0.f ? 1.f / sum : 0.f;
       }
       if (!by_logit) {
+        // (a bias of -infinity stays)
 #pragma unroll
-        for (int i = 0; i < V; ++i) c[i] = l.v[i] > -INFINITY && b[i] > -INFINITY ? c[i] * inv + b[i] : -INFINITY;
+        for (int i = 0; i < V; ++i) c[i] = l.v[i] > -INFINITY ? fmaf(p[i], inv, b[i]) : -INFINITY;
       }
     }
-    const float near = 0x1p-18f * (r.score == kSoftmax ? inv : 1.f) + 0x1p-21f * most;
+    const float near = (r.score == kSoftmax ? 0x1p-18f * inv : 0x1.4p-20f) + 0x1p-22f * most;
     bool open = false;
     if (r.groups > 1) {
       // the choice values in LDS; a lane per group adds up its largest
       float *cs = reinterpret_cast<float *>(lists[wave]) + mine * (LANES * V);
 #pragma unroll
-      for (int i = 0; i < V; ++i) cs[R::expert(i, lane)] = c[i];
+      for (int i = 0; i < V; ++i) cs[R::expert(i, here)] = c[i];
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      float *gs = groups[wave][mine];
+      float *gs = reinterpret_cast<float *>(lists[wave]) + 64 * V + mine * kMostGroups;
       for (int g = lane; g < r.groups; g += LANES) {
         float first = -INFINITY, second = -INFINITY;
         for (int i = 0; i < each; ++i) {
@@ -361,26 +372,30 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r,
       kept = static_cast<uint64_t>(hi) << 32 | lo;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const uint32_t g = static_cast<uint32_t>(R::expert(i, lane)) * inverse >> 20;
+        const uint32_t g = static_cast<uint32_t>(R::expert(i, here)) * inverse >> 20;
         if (!(kept >> (g & 63) & 1)) c[i] = -INFINITY;
       }
     }
     double s[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) s[i] = c[i] > -INFINITY ? pair_of(c[i], R::expert(i, lane)) : 0.;
+    for (int i = 0; i < V; ++i) s[i] = pair_of(c[i], R::expert(i, here));
     sort_down<V>(s);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
 #pragma unroll
-    for (int i = 1; i < V; ++i) list[64 * i] = s[i];
-    double head = s[0];
-    int at = 1;
+    for (int i = 2; i < V; ++i) list[64 * i] = s[i];
+    // a lane's next value is there when the one before it wins
+    double head = s[0], next = V > 1 ? s[V > 1 ? 1 : 0] : 0.;
+    const double *after = list + 128;
+    int left = V - 2;
     // one round more than picks, for the one that was not taken
     for (int j = 0; j < r.top_k + !by_logit; ++j) {
       const double best = row_best<LANES>(head);
       if (lane == 0) pick[j] = best;
-      if (head == best && best != 0.) {
-        head = at < V ? list[64 * at] : 0.;
-        ++at;
+      if (head == best) {
+        head = next;
+        next = left > 0 ? *after : 0.;
+        after += 64;
+        --left;
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -389,11 +404,11 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r,
 #pragma unroll
     for (int n = 0; n < (LANES == 16 ? 2 : 1); ++n) {
       const int j = lane + LANES * n;
-      if (j >= r.top_k || pick[j] == 0.) continue;
+      if (j >= r.top_k || pick[j] < kFirst) continue;
       id[n] = expert_of(pick[j]);
       const float x = fminf(to_f32<DT>(row[id[n]]), 3.4028234663852886e38f);
       p[n] = score_of(x, r.score, top);
-      if (!by_logit && pick[j + 1] != 0. && !(value_of(pick[j]) - value_of(pick[j + 1]) > near)) {
+      if (!by_logit && pick[j + 1] >= kFirst && !(value_of(pick[j]) - value_of(pick[j + 1]) > near)) {
         // as near as that, but for the same logit and bias
         const int o = expert_of(pick[j + 1]);
         const float y = fminf(to_f32<DT>(row[o]), 3.4028234663852886e38f);
@@ -403,7 +418,7 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r,
     }
     total = row_sum<LANES>(total);
     // (sigmoids that 32 bits cannot hold still have a ratio)
-    open = open || (r.score == kSigmoid && r.renormalise && total < 0x1p-60f && pick[0] != 0.);
+    open = open || (r.score == kSigmoid && r.renormalise && total < 0x1p-60f && pick[0] >= kFirst);
     const float factor = r.scale * (!r.renormalise ? inv : total > 0.f ? 1.f / total : 0.f);
     const uint64_t opens = __ballot(open);
     constexpr uint64_t kRow = LANES == 64 ? ~0ull : (1ull << (LANES & 63)) - 1;
@@ -418,7 +433,7 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_kernel(MoeSelect r,
     }
     for (int n = 0; n < kTokens; ++n)
       if (t0 + n < M && (opens >> (n * LANES) & kRow))
-        select_exactly<DT>(r, logits, t0 + n, bias, lists[wave], exact_groups[wave], ids, weights);
+        select_exactly<DT>(r, logits, t0 + n, bias, lists[wave], picks[wave], ids, weights);
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
 }
@@ -565,6 +580,9 @@ static void select_go(const MoeSelect &r, const void *logits, int M, const float
                        weights);
   else if (r.E <= 64)
     hipLaunchKernelGGL((moe_select_kernel<DT, 16, 4>), dim3(select_blocks(M, 4)), block, 0, s, r, logits, M, bias, ids,
+                       weights);
+  else if (r.E <= 256 && M <= 2048)
+    hipLaunchKernelGGL((moe_select_kernel<DT, 64, 4>), dim3(select_blocks(M, 1)), block, 0, s, r, logits, M, bias, ids,
                        weights);
   else if (r.E <= 256)
     hipLaunchKernelGGL((moe_select_kernel<DT, 16, 16>), dim3(select_blocks(M, 4)), block, 0, s, r, logits, M, bias, ids,
