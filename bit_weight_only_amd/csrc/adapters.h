@@ -290,6 +290,13 @@ __device__ __forceinline__ void stage_tokens(const int32_t *__restrict__ perm, c
 template <class V, int AHEAD = 1, class LOAD, class COMPUTE>
 __device__ __forceinline__ void in_turn(int steps, LOAD load, COMPUTE compute) {
   V v[AHEAD + 1];
+  if constexpr (AHEAD == 0) {
+    for (int s = 0; s < steps; ++s) {
+      load(v[0], s);
+      compute(v[0], s);
+    }
+    return;
+  }
   load(v[0], 0);
   if (steps == 1) return compute(v[0], 0);
 #pragma unroll

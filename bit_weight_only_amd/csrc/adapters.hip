@@ -331,14 +331,19 @@ __device__ __forceinline__ void others(const int32_t *ids, int t0, int M, int L,
   if (base != y) copy_others<kThreads>(ids, t0, M, L, base, y, N, from, end, list);
 }
 
-// Few tokens: one tile of up to 16 a workgroup column, h the sum of the shares.
-template <int DT, int RC, bool BY_TOKEN, int RANK>
-__global__ void __launch_bounds__(kThreads) adapters_few_kernel(
-    const float *__restrict__ part, int splits, int M, int N, int r, const uint16_t *__restrict__ B,
+// Few tokens: one tile of up to 16 a workgroup column. FROM: h is the sum of the shares,
+// by token or by list entry, or (by token) is made here, by every workgroup for
+// itself: one launch less, for A's way to each of them from the caches (kOneBytes).
+enum { kByToken, kByEntry, kOneLaunch };
+template <int DT, int RC, int FROM, int RANK>
+__global__ void __launch_bounds__(FROM == kOneLaunch ? kManyThreads : kThreads) adapters_few_kernel(
+    const uint16_t *__restrict__ x, int K, const uint16_t *__restrict__ A, const float *__restrict__ part, int splits, int M, int N, int r, const uint16_t *__restrict__ B,
     const float *__restrict__ scales, int L, const int32_t *__restrict__ ids, const int32_t *__restrict__ offsets,
     const int32_t *__restrict__ perm, const uint16_t *base, const uint16_t *rows_of_base, uint16_t *y,
     float *__restrict__ h, int tiles, int steps) {
-  constexpr int kStride = 16 * RC + 4;
+  constexpr int kStride = 16 * RC + 4, kMine = FROM == kOneLaunch ? kManyThreads : kThreads, kW = kMine / 64;
+  constexpr int kSpan = 64 * kW;
+  constexpr bool BY_TOKEN = FROM != kByEntry;
   __shared__ float hs[16 * kStride];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const int from = blockIdx.y * steps * kSpan, end = min(from + steps * kSpan, N);
@@ -347,10 +352,10 @@ __global__ void __launch_bounds__(kThreads) adapters_few_kernel(
     const int t = blockIdx.x;
     tile = {adapter_of(ids, t, L), t, 1};
     if (tile.a < 0) {
-      for (int n = from + threadIdx.x; base != y && n < end; n += kThreads)
+      for (int n = from + threadIdx.x; base != y && n < end; n += kMine)
         y[static_cast<size_t>(t) * N + n] = base ? base[static_cast<size_t>(t) * N + n] : static_cast<uint16_t>(0);
       if (h && blockIdx.y == 0)
-        for (int j = threadIdx.x; j < r; j += kThreads) h[static_cast<size_t>(t) * r + j] = 0.f;
+        for (int j = threadIdx.x; j < r; j += kMine) h[static_cast<size_t>(t) * r + j] = 0.f;
       return;
     }
   } else {
@@ -364,24 +369,37 @@ __global__ void __launch_bounds__(kThreads) adapters_few_kernel(
   if constexpr (!BY_TOKEN) token = perm[token];
   const bool live = col < tile.n && token >= 0 && token < M;
   const size_t row = static_cast<size_t>(min(max(token, 0), M - 1));
-  // the shares added up; zeros past r and, so that nothing unset is read, past the
-  // tile's last token
-  for (int i = threadIdx.x; i < 16 * 16 * RC; i += kThreads) {
-    const int t = i / (16 * RC), j = i % (16 * RC);
-    float v = 0.f;
-    if (t < tile.n && j < r) {
-      const float *p = part + static_cast<size_t>(tile.i0 + t) * r + j;
-      float w[kMostShares];   // all under way at once
+  if constexpr (FROM == kOneLaunch) {
+    constexpr int kS = RC >= 4 ? 2 : 4;
+    constexpr size_t kLds = std::max(sizeof(float4_t) * kW * RC * 64, sizeof(uint16_t) * kW * kStage<1, RC, kS>);
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+    float4_t acc[1][RC];
+    shrink<DT, 1, RC, kS, kW, true>(x, M, K, r, A, perm, tile, 0, K / (32 * kS), reinterpret_cast<uint16_t *>(lds), acc);
+    __syncthreads();
+    join<1, RC, kW>(acc, reinterpret_cast<float4_t *>(lds), [&](int t, int j, float v) {
+      hs[t * kStride + j] = j < r ? v : 0.f;   // (the one token sixteen times)
+      if (h && blockIdx.y == 0 && t == 0 && j < r) h[static_cast<size_t>(tile.i0) * r + j] = v;
+    });
+  } else {
+    // the shares added up; zeros past r and, so that nothing unset is read, past the
+    // tile's last token
+    for (int i = threadIdx.x; i < 16 * 16 * RC; i += kThreads) {
+      const int t = i / (16 * RC), j = i % (16 * RC);
+      float v = 0.f;
+      if (t < tile.n && j < r) {
+        const float *p = part + static_cast<size_t>(tile.i0 + t) * r + j;
+        float w[kMostShares];   // all under way at once
 #pragma unroll
-      for (int s = 0; s < kMostShares; ++s) w[s] = s < splits ? p[static_cast<size_t>(s) * M * r] : 0.f;
+        for (int s = 0; s < kMostShares; ++s) w[s] = s < splits ? p[static_cast<size_t>(s) * M * r] : 0.f;
 #pragma unroll
-      for (int s = 0; s < kMostShares; ++s) v += w[s];
-      if (h && blockIdx.y == 0) {
-        const int at = BY_TOKEN ? tile.i0 : perm[tile.i0 + t];
-        if (at >= 0 && at < M) h[static_cast<size_t>(at) * r + j] = v;
+        for (int s = 0; s < kMostShares; ++s) v += w[s];
+        if (h && blockIdx.y == 0) {
+          const int at = BY_TOKEN ? tile.i0 : perm[tile.i0 + t];
+          if (at >= 0 && at < M) h[static_cast<size_t>(at) * r + j] = v;
+        }
       }
+      hs[t * kStride + j] = v;
     }
-    hs[t * kStride + j] = v;
   }
   __syncthreads();
   Oct hv[RC];
@@ -442,7 +460,10 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
     Rows<E, 4> y[TF];
     float4_t back[TF];
   };
-  in_turn<Step>(
+  // (a step ahead costs more registers than there are from rank 33 on: 8192 tokens, rank
+  // 64, 14336 columns with it 140 us, without 121)
+  constexpr int kAhead = RC >= 4 ? 0 : 1;
+  in_turn<Step, kAhead>(
       (c.n + kStep - 1) / kStep,
       [&](Step &v, int s) {
 #pragma unroll
@@ -488,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
 
 // How the forward pass is cut up.
 struct ForwardPlan {
-  bool few, by_token;
+  bool few, by_token, one;
   int tf, rf;           // 16-token and 16-value pieces of a tile
   int e;                // many tokens: columns of a lane
   int tiles;            // at most
@@ -498,6 +519,10 @@ struct ForwardPlan {
   size_t pieces, back, pad, total;   // where in the workspace (part at its start)
 };
 constexpr int kFewTokens = 64;
+// A's bytes that a workgroup reads to make h for itself, and such workgroups, at most:
+// one token of 4096 -> 4096 at rank 16 takes 10.6 us called one by one and 6.2 in a
+// graph, in two launches 14.7 and 5.6.
+constexpr long kOneBytes = 256 << 10, kOneGroups = 512;
 
 ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
   ForwardPlan p{};
@@ -509,23 +534,28 @@ ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
   // tokens of an adapter on average decide the tile
   p.tf = p.few || g.M / some <= 16 || p.rf == 8 ? 1 : 2;
   const int unit = 16 * p.tf, spans = (g.N + kSpan - 1) / kSpan;
-  p.tiles = p.few && p.by_token ? g.M : g.M / unit + some;
   p.e = p.rf <= 2 ? 8 : 4;
   if (p.few) {
     // (the same with and without an order: so is the result)
     p.splits = std::max(1, std::min({512 / std::max(1, g.M), (g.K / 128 + kWaves - 1) / kWaves, kMostShares}));
     p.steps = std::max(1, std::min(8, static_cast<int>(static_cast<long>(spans) * g.M / 512)));
+    p.one = p.rf < 8 && static_cast<long>(p.rf) * 32 * g.K <= kOneBytes && static_cast<long>(g.M) * ((spans + 1) / 2) <= kOneGroups;
+    if (p.one) {
+      p.by_token = true;
+      p.steps = 1;
+    }
   } else {
     const long rows = static_cast<long>(g.M) * ((g.N + 64 * p.e - 1) / (64 * p.e)) / 1024;
     p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, 128l), static_cast<long>(kMostTokens)));
     p.chunks = g.M / p.rows + some;
   }
+  p.tiles = p.few && p.by_token ? g.M : g.M / unit + some;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   if (!p.few) {
     p.back = up(static_cast<size_t>(p.tiles) * p.tf * p.rf * 64 * sizeof(Oct));
     p.pad = p.back + up(static_cast<size_t>(p.tiles) * unit * 4);
   } else {
-    p.pad = up(static_cast<size_t>(p.splits) * g.M * g.r * 4);
+    p.pad = p.one ? 0 : up(static_cast<size_t>(p.splits) * g.M * g.r * 4);
   }
   p.total = p.pad + (g.N < kNarrow ? static_cast<size_t>(g.M) * kNarrow * 2 : 0);
   return p;
@@ -552,17 +582,30 @@ void forward_rank(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
     auto go = [&](auto first, auto second, bool by_token) {
       hipLaunchKernelGGL(first, dim3(p.tiles, p.splits), block, 0, s, x, g.M, g.K, g.r, a, g.L, g.ids, g.offsets,
                          g.perm, part);
-      hipLaunchKernelGGL(second, dim3(p.tiles + (by_token ? 0 : rest), (spans + p.steps - 1) / p.steps), block, 0, s,
-                         part, p.splits, g.M, g.N, g.r, b, g.scales, g.L, g.ids, g.offsets, g.perm, base, wide, y, g.h,
+      hipLaunchKernelGGL(second, dim3(p.tiles + (by_token ? 0 : rest), (spans + p.steps - 1) / p.steps), block, 0, s, x,
+                         g.K, a, part, p.splits, g.M, g.N, g.r, b, g.scales, g.L, g.ids, g.offsets, g.perm, base, wide, y, g.h,
                          p.tiles, p.steps);
     };
     auto pick = [&](auto by_token) {
       constexpr bool kBy = decltype(by_token)::value;
+      constexpr int kFrom = kBy ? kByToken : kByEntry;
       auto first = adapters_shares_kernel<DT, RC, kBy>;
-      if (rank == kWhole) go(first, adapters_few_kernel<DT, RC, kBy, kWhole>, kBy);
-      else if (rank == kMore) go(first, adapters_few_kernel<DT, RC, kBy, kMore>, kBy);
-      else if constexpr (RC == 1) go(first, adapters_few_kernel<DT, RC, kBy, kLess>, kBy);
+      if (rank == kWhole) go(first, adapters_few_kernel<DT, RC, kFrom, kWhole>, kBy);
+      else if (rank == kMore) go(first, adapters_few_kernel<DT, RC, kFrom, kMore>, kBy);
+      else if constexpr (RC == 1) go(first, adapters_few_kernel<DT, RC, kFrom, kLess>, kBy);
     };
+    if constexpr (RC < 8) {
+      auto once = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(g.M, (spans + 1) / 2), dim3(kManyThreads), 0, s, x, g.K, a, nullptr, 0, g.M, g.N,
+                           g.r, b, g.scales, g.L, g.ids, nullptr, nullptr, base, wide, y, g.h, 0, 1);
+      };
+      if (p.one) {
+        if (rank == kWhole) once(adapters_few_kernel<DT, RC, kOneLaunch, kWhole>);
+        else if (rank == kMore) once(adapters_few_kernel<DT, RC, kOneLaunch, kMore>);
+        else if constexpr (RC == 1) once(adapters_few_kernel<DT, RC, kOneLaunch, kLess>);
+        return;
+      }
+    }
     if (p.by_token) pick(std::true_type{});
     else pick(std::false_type{});
     return;

@@ -137,15 +137,16 @@ __device__ __forceinline__ void put(float *out, float *part, const Chunk &c, siz
   else out[static_cast<size_t>(c.a) * size + at] = v * scale;
 }
 
-// Zeros to a slice of the gradient of an adapter without tokens: columns n0 .. n1;
-// value (n, j) at n * sn + j * sj.
+// `count` zeros, by a workgroup.
 template <int kThreads>
-__device__ __forceinline__ void clear(float *out, int r, int n0, int n1, size_t sn, size_t sj) {
-  const int n = max(n1 - n0, 0);
-  for (long i = threadIdx.x; i < static_cast<long>(n) * r; i += kThreads) {
-    const int a = sn == 1 ? static_cast<int>(i / n) : static_cast<int>(i % r);
-    const int b = sn == 1 ? static_cast<int>(i % n) : static_cast<int>(i / r);
-    out[(n0 + b) * sn + a * sj] = 0.f;
+__device__ __forceinline__ void clear(float *out, size_t count) {
+  struct __attribute__((packed, aligned(4))) Four {
+    float v[4];
+  };
+  for (size_t i = 4 * threadIdx.x; i < count; i += 4 * kThreads) {
+    if (i + 4 <= count) *reinterpret_cast<Four *>(out + i) = Four{{0.f, 0.f, 0.f, 0.f}};
+    else
+      for (size_t k = i; k < count; ++k) out[k] = 0.f;
   }
 }
 
@@ -204,9 +205,8 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
     int lo, hi;
     const int a = blockIdx.y - chunks;
     segment(offsets, a, M, lo, hi);
-    if (lo == hi)
-      clear<kDyThreads>(dB + static_cast<size_t>(a) * N * r, r, blockIdx.x * kSlice,
-                        min(N, static_cast<int>(blockIdx.x + 1) * kSlice), r, 1);
+    const int n0 = blockIdx.x * kSlice, n1 = min(N, n0 + kSlice);   // (no tokens: zeros)
+    if (lo == hi) clear<kDyThreads>(dB + (static_cast<size_t>(a) * N + n0) * r, static_cast<size_t>(n1 - n0) * r);
     return;
   }
   const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
@@ -346,7 +346,10 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     int lo, hi;
     const int a = blockIdx.y - chunks;
     segment(offsets, a, M, lo, hi);
-    if (lo == hi) clear<kThreads>(dA + static_cast<size_t>(a) * r * K, r, s0, s1, 1, K);
+    // (no tokens: zeros, an equal share of the adapter's to every slice)
+    const size_t all = static_cast<size_t>(r) * K / 4, from = all * blockIdx.x / gridDim.x;
+    if (lo == hi)
+      clear<kThreads>(dA + 4 * (all * a + from), 4 * (all * (blockIdx.x + 1) / gridDim.x - from));
     return;
   }
   const Chunk c = chunk_of(offsets, L, M, rows, kStep, max_steps, blockIdx.y);
@@ -383,7 +386,10 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     float back;
     float4_t token_back[2];
   };
-  in_turn<Step>(
+  // (a step ahead costs more registers than there are from rank 17 on: 4000 tokens of 96
+  // adapters, rank 32, with it 34 us, without 26; 8192 tokens, rank 64, 70 and 55)
+  constexpr int kAhead = RF >= 2 ? 0 : 1;
+  in_turn<Step, kAhead>(
       (c.n + kStep - 1) / kStep,
       [&](Step &v, int s) {
         const size_t step = c.step + s;

@@ -587,6 +587,9 @@ static void select_go(const MoeSelect &r, const void *logits, int M, const float
   else if (r.E <= 256)
     hipLaunchKernelGGL((moe_select_kernel<DT, 16, 16>), dim3(select_blocks(M, 4)), block, 0, s, r, logits, M, bias, ids,
                        weights);
+  else if (r.E <= 512)
+    hipLaunchKernelGGL((moe_select_kernel<DT, 64, 8>), dim3(select_blocks(M, 1)), block, 0, s, r, logits, M, bias, ids,
+                       weights);
   else
     hipLaunchKernelGGL((moe_select_kernel<DT, 64, 16>), dim3(select_blocks(M, 1)), block, 0, s, r, logits, M, bias, ids,
                        weights);
