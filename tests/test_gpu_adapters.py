@@ -126,6 +126,39 @@ def test_backward(L, dev, M, K, N, n, r, dtype):
     _check_backward(L, c, h, False, True)
 
 
+# several chunks of an adapter, every width of rank with many tokens, rows of fewer than eight values, more adapters
+# than lanes, as many as there may be
+FORMS = [(3000, 256, 2600, 1, 16), (2500, 512, 1100, 2, 64), (1500, 384, 520, 3, 128), (1300, 256, 777, 2, 30),
+         (90, 128, 5, 2, 9), (700, 256, 3, 1, 24), (66, 128, 7, 70, 3), (3, 256, 2, 2, 16), (300, 256, 100, 200, 8),
+         (1100, 128, 64, 1024, 4), (70, 14336, 64, 3, 16), (2, 14336, 520, 2, 16), (64, 1024, 4096, 3, 70)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N,n,r", FORMS)
+def test_forms(L, dev, M, K, N, n, r, dtype):
+    say(f"adapters forms M={M} K={K} N={N} L={n} r={r} {dtype}")
+    c = Case(L, M, K, N, n, r, dtype, item=9, runs=bool(n % 2))
+    _, h = _check_forward(L, c, True, True, True)
+    _check_forward(L, c, True, False, False)
+    _check_backward(L, c, h, True, True)
+
+
+def test_one_adapter_has_nearly_all_tokens(L, dev):
+    """Chunks of one adapter next to adapters of one token and of none."""
+    import torch
+
+    c = Case(L, 1777, 256, 300, 9, 16, "bfloat16", item=10)
+    c.ids_h[:] = 4
+    c.ids_h[[3, 700, 1776]] = [0, 8, 5]
+    c.ids = torch.from_numpy(c.ids_h).cuda()
+    _, off, perm, _ = L.moe_sort(c.ids[:, None].contiguous(), 9)
+    c.order = (off, perm)
+    _, h = _check_forward(L, c, True, True, True)
+    _, da, db = _check_backward(L, c, h, True, False)
+    for i in (1, 2, 3, 6, 7):
+        assert not da[i].any() and not db[i].any()
+
+
 @pytest.mark.parametrize("M,K,N,n,r", [(1, 128, 24, 2, 4), (50, 256, 100, 3, 16), (700, 256, 200, 4, 20)])
 def test_none_has_an_adapter(L, dev, M, K, N, n, r):
     import torch

@@ -256,6 +256,31 @@ def test_many_tokens(L, dev):
     assert float(((w.double() - s).abs() / s).max()) <= 46 * A.U
 
 
+# more tokens than go to a wavefront each
+@pytest.mark.parametrize("m,E,k,G,tg,gp", [(2100, 256, 8, 8, 4, 2), (2049, 200, 17, 10, 5, 2), (2060, 72, 32, 1, 1, 1)])
+def test_more_tokens_than_wavefronts(L, dev, m, E, k, G, tg, gp):
+    bias = (0.1 * synth.rng(88, E, synth.ROLE_X).standard_normal(E)).astype(np.float32)
+    lg = _logits(m, E, "bfloat16", m)
+    lg[5, 2:] = float("-inf")
+    for score in (0, 1):
+        for b in (None, bias, np.zeros(E, np.float32)):
+            _check(L, lg, k, b, score=score, groups=G, top_groups=tg, group_picks=gp)
+
+
+def test_far_below_zero(L, dev):
+    """Sigmoids that 32 bits cannot hold still have a ratio, and a gradient."""
+    import torch
+
+    for shift in (-50.0, -95.0, -300.0):
+        lg = _logits(40, 96, "float32", 3) + shift
+        ids, _ = _check(L, lg, 6, score=1)
+        g = synth.rng(89, 0, synth.ROLE_X).standard_normal((40, 6)).astype(np.float32)
+        d = L.moe_select_backward(torch.from_numpy(g).cuda(), lg.cuda(), ids, score=1)
+        want, bound = A.select_backward(g.astype(np.float64), lg.double().numpy(), ids.cpu().numpy(), 1)
+        # (the argument of exp is off by its own rounding)
+        assert np.all(np.abs(d.double().cpu().numpy() - want) <= bound * (1.01 + abs(shift) / 4) + 1e-30)
+
+
 def test_refusals(L, dev):
     import torch
 
