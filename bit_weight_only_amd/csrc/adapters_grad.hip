@@ -37,13 +37,15 @@ constexpr int kPieces = DT == kF16 ? 2 : 3;
 
 // The operands that one step's tokens give, in the order in which lanes load them:
 //   over  [steps][RF][pieces][64 lanes]: value 16 g + l % 16 of tokens 8 (l / 16) .. + 7,
-//         times over_to[step]: the side of the sums over tokens;
+//         times a power of two of the step's value: the side of the sums over tokens (a
+//         value's tokens meet one another only, so that small values lose nothing beside
+//         large ones);
 //   along [steps][2][RF][64 lanes]: token 16 f + l % 16, its values 16 c + 8 (l / 16 % 2) ..
 //         + 7, first pieces for l < 32 and second ones from there, times the token's
 //         own power of two: the side of u A.
 struct Pieces {
   Oct *over, *along;
-  float *over_back, *along_back;   // [steps], [steps][kStep]: the inverse powers
+  float *over_back, *along_back;   // [steps][16 RF], [steps][kStep]: the inverse powers
 };
 
 // One workgroup per step: v[t][j] = scale * sum of `shares` shares (share s at src +
@@ -55,12 +57,10 @@ __global__ void __launch_bounds__(kPieceThreads) adapters_pieces_kernel(const fl
                                                                    const int32_t *__restrict__ perm, Pieces out) {
   constexpr int kP = kPieces<DT>, kCols = 16 * RF, kStride = kCols + 4;
   __shared__ float v[kStep * kStride];
-  __shared__ float top[kPieceThreads / 64];
   const Chunk c = chunk_of(offsets, L, M, kStep, kStep, gridDim.x, blockIdx.x);
   if (c.a < 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   const float sa = OF_H ? 1.f : scales[c.a];
-  float m = 0.f;
   for (int i = threadIdx.x; i < kStep * kCols; i += kPieceThreads) {
     const int t = i / kCols, j = i % kCols;
     float s = 0.f;
@@ -83,19 +83,21 @@ __global__ void __launch_bounds__(kPieceThreads) adapters_pieces_kernel(const fl
       }
     }
     v[t * kStride + j] = s;
-    m = fmaxf(m, fabsf(s));
   }
-  for (int d = 32; d > 0; d /= 2) m = fmaxf(m, __shfl_xor(m, d));
-  if (lane == 0) top[wave] = m;
   __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kPieceThreads / 64; ++w) m = fmaxf(m, top[w]);
-  const Scale sc = scale_for<DT>(m);
-  if (threadIdx.x == 0) out.over_back[c.step] = sc.back;
   for (int g = wave; g < RF; g += kPieceThreads / 64) {
-    float w[8];
+    float w[8], m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = v[(8 * q + i) * kStride + 16 * g + col] * sc.to;
+    for (int i = 0; i < 8; ++i) {
+      w[i] = v[(8 * q + i) * kStride + 16 * g + col];
+      m = fmaxf(m, fabsf(w[i]));
+    }
+    m = fmaxf(m, __uint_as_float(xor_lane_u32<16>(__float_as_uint(m))));
+    m = fmaxf(m, __uint_as_float(xor_lane_u32<32>(__float_as_uint(m))));
+    const Scale sc = scale_for<DT>(m);
+    if (q == 0) out.over_back[static_cast<size_t>(c.step) * kCols + 16 * g + col] = sc.back;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] *= sc.to;
     Oct o[kP];
     split8<DT, kP>(w, o);
 #pragma unroll
@@ -199,6 +201,7 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
   __shared__ float red[kDyWaves][kStep * kStride];
   __shared__ __attribute__((aligned(16))) uint16_t tile[kDyWaves][kStep * kCols];
   __shared__ Oct hs[RF * kP * 64];
+  __shared__ float backs[16 * RF];
   __shared__ __attribute__((aligned(16))) int tokens[kMostTokens];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
   if (static_cast<int>(blockIdx.y) >= chunks) {
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
         for (int i = 0; i < 8; ++i) row[i] = static_cast<size_t>(max(tokens[s * kStep + 8 * q + i], 0)) * width;
         load_rows(v.x, dy, row, min(n0 + E * col, width - E));
         v.h.load(h.over + step * RF * kP * 64);
-        if constexpr (DT == kF16) v.back = h.over_back[step];
+        if constexpr (DT == kF16) v.back = h.over_back[step * 16 * RF + min(static_cast<int>(threadIdx.x), 16 * RF - 1)];
       },
       [&](Step &v, int s) {
         const int i0 = c.i0 + s * kStep, n = min(c.n - s * kStep, kStep);
@@ -260,6 +263,7 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
               make_uint2(v.x.w[i][0], v.x.w[i][1]);
         }
         v.h.lay(hs);
+        if (DT == kF16 && threadIdx.x < 16 * RF) backs[threadIdx.x] = v.back;
         lds_barrier();
         // this wavefront's share of u
         float *mine = red[wave];
@@ -295,10 +299,11 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
             }
           }
           if constexpr (DT == kF16) {
+            const float back = backs[16 * g + col];
 #pragma unroll
             for (int e = 0; e < E; ++e)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[e][i], v.back, acc[e][g][i]);
+              for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[e][i], back, acc[e][g][i]);
           }
         }
         // the slice's share of u (what it reads, and hs, is written again behind the
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     float *__restrict__ part) {
   constexpr int E = kE, kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves;
   __shared__ Oct over[RF * kP * 64], along[2 * RF * 64];
+  __shared__ __attribute__((aligned(16))) float backs[16 * RF];
   __shared__ __attribute__((aligned(16))) int tokens[kMostTokens];
   __shared__ int list[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, q = lane >> 4;
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
         v.over.load(u.over + step * RF * kP * 64);
         v.along.load(u.along + step * 2 * RF * 64);
         if constexpr (DT == kF16) {
-          v.back = u.over_back[step];
+          v.back = u.over_back[step * 16 * RF + min(static_cast<int>(threadIdx.x), 16 * RF - 1)];
 #pragma unroll
           for (int f = 0; f < 2; ++f)
             v.token_back[f] = *reinterpret_cast<const float4_t *>(u.along_back + step * kStep + 16 * f + 4 * q);
@@ -423,6 +429,7 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
         lds_barrier();   // the step before has read its operands
         v.over.lay(over);
         v.along.lay(along);
+        if (DT == kF16 && threadIdx.x < 16 * RF) backs[threadIdx.x] = v.back;
         lds_barrier();
         if (n < kStep) drop_rows(v.x, 8 * q, n);
         Oct xv[E];
@@ -441,10 +448,11 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
             }
           }
           if constexpr (DT == kF16) {
+            const float4_t back = *reinterpret_cast<const float4_t *>(backs + 16 * g + 4 * q);
 #pragma unroll
             for (int e = 0; e < E; ++e)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[e][i], v.back, acc[e][g][i]);
+              for (int i = 0; i < 4; ++i) acc[e][g][i] = fmaf(d[e][i], back[i], acc[e][g][i]);
           }
         }
 #pragma unroll
@@ -545,7 +553,7 @@ Plan plan_of(const AdapterArgs &g) {
   };
   p.over = take(static_cast<size_t>(p.steps) * p.rf * pieces * 64 * sizeof(Oct));
   p.along = take(static_cast<size_t>(p.steps) * 2 * p.rf * 64 * sizeof(Oct));
-  p.over_back = take(static_cast<size_t>(p.steps) * 4);
+  p.over_back = take(static_cast<size_t>(p.steps) * 16 * p.rf * 4);
   p.along_back = take(static_cast<size_t>(p.steps) * kStep * 4);
   p.u_part = take(static_cast<size_t>(p.slices_y) * g.M * g.r * 4);
   const size_t sums_y = g.M > p.rows_y ? 2 * (static_cast<size_t>(g.M) / (p.rows_y / 2) + 1) * g.N * g.r * 4 : 0;

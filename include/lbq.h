@@ -621,6 +621,10 @@ lbq_status lbq_adapters_backward_workspace(const lbq_adapters *ad, int32_t M, in
  *     order serves every layer of a batch. Contents that are not ids' order give
  *     wrong rows, never an access out of bounds.
  *   h: fp32 [M][r], written for the backward pass, or NULL.
+ * Outputs and workspace overlap no input, but y may be base. A token whose h is
+ * infinite or NaN gets NaN; no other token's row changes. h enters the second
+ * product to 2^-21 (fp16) or 2^-16 (bf16) of each value, fp16 with 2^-39 of the
+ * token's largest at least.
  * Repeat calls give identical bits. Errors as lbq_mx_matmul. */
 lbq_status lbq_adapters_forward(const lbq_adapters *ad, const void *x, int32_t M, const int32_t *ids,
                                 const int32_t *offsets, const int32_t *perm, const void *base, void *y, float *h,
@@ -633,7 +637,8 @@ lbq_status lbq_adapters_forward(const lbq_adapters *ad, const void *x, int32_t M
  *     an adapter),
  *   d_a [L][r][K] = sum over a's tokens of u_t^T x_t, d_b [L][N][r] = scales[a] times
  *     the sum of dy_t^T h_t, both fp32, zeros for an adapter without tokens.
- * d_a and d_b are written, not added to. Sums have a fixed order. */
+ * d_a and d_b are written, not added to. Sums have a fixed order. Outputs and
+ * workspace overlap no input, but dx may be base. */
 lbq_status lbq_adapters_backward(const lbq_adapters *ad, const void *dy, const void *x, const float *h, int32_t M,
                                  const int32_t *ids, const int32_t *offsets, const int32_t *perm, const void *base,
                                  void *dx, float *d_a, float *d_b, void *ws, size_t ws_bytes, void *stream);

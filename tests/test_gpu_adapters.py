@@ -243,6 +243,49 @@ def test_values_of_other_tokens_stay_there(L, dev, M):
     assert bool(torch.isnan(da[1]).any()) and bool(torch.isnan(db[1]).any())
 
 
+@pytest.mark.parametrize("M", [3, 40, 90])
+@pytest.mark.parametrize("r", [9, 64])
+def test_values_of_very_different_sizes(L, dev, M, r):
+    """fp16: rows of A from 2^-12 to 2^15, columns of B the other way round, so that every value of h counts as much.
+
+    A token's h is brought to at least 2^14 by one power of two for the product with B, and what two pieces leave out
+    is below half the smallest fp16 number, 2^-25: 2^-39 of the token's largest h, in each of its r values; the same of u
+    for dx. In the sums over tokens a value has its own power of two: 2^-39 of its largest over 32 tokens."""
+    import torch
+
+    c = Case(L, M, 1024, 96, 2, r, "float16", item=5)
+    size = 2.0 ** np.round(np.linspace(-12, 15, r))
+    c.a.copy_((c.a.double().cpu() * torch.from_numpy(size)[None, :, None]).to(c.a.dtype))
+    c.b.copy_((c.b.double().cpu() / torch.from_numpy(size)[None, None, :]).to(c.b.dtype))
+    c.a64, c.b64 = c.a.double().cpu().numpy(), c.b.double().cpu().numpy()
+    h = torch.empty(M, r, device="cuda")
+    y = L.adapters_forward(c.ad, c.x, c.ids, base=c.base, order=c.order, h=h)
+    wy, wh, by, bh = A.forward(c.x64, c.a64, c.b64, c.s64, c.ids_h, c.base64, c.dtype)
+    _near(h, wh, bh + np.abs(wh) * A.U, None, "h")
+    h64 = h.double().cpu().numpy()
+    on = [t for t in range(M) if 0 <= c.ids_h[t] < c.n]
+    for t in on:
+        i = c.ids_h[t]
+        by[t] += 2.0 ** -39 * np.abs(h64[t]).max() * c.s64[i] * np.abs(c.b64[i]).sum(1)
+    _near(y, wy, by, c.dtype, "y")
+    dx, da, db = L.adapters_backward(c.ad, c.dy, c.x, h, c.ids, base=c.dbase, order=c.order)
+    w, bd = A.backward(c.dy64, c.x64, h64, c.a64, c.b64, c.s64, c.ids_h, c.dbase64, c.dtype)
+    for t in on:
+        i = c.ids_h[t]
+        u = np.abs(c.s64[i] * (c.dy64[t] @ c.b64[i]))
+        bd[0][t] += 2.0 ** -38 * u.max() * np.abs(c.a64[i]).sum(0)
+    for i in range(c.n):
+        t = np.nonzero(c.ids_h == i)[0]
+        if len(t) == 0:
+            continue
+        u = np.abs(c.s64[i] * (c.dy64[t] @ c.b64[i])).max(0)
+        bd[1][i] += 2.0 ** -38 * u[:, None] * np.abs(c.x64[t]).sum(0)
+        bd[2][i] += 2.0 ** -39 * c.s64[i] * np.abs(h64[t]).max(0) * np.abs(c.dy64[t]).sum(0)[:, None]
+    _near(dx, w[0], bd[0], c.dtype, "dx")
+    _near(da, w[1], bd[1] + np.abs(w[1]) * A.U, None, "d_a")
+    _near(db, w[2], bd[2] + np.abs(w[2]) * A.U, None, "d_b")
+
+
 @pytest.mark.parametrize("M", [2, 40, 300])
 @pytest.mark.parametrize("size", [2.0 ** -9, 2.0 ** 9])
 def test_small_and_large_values(L, dev, M, size):
