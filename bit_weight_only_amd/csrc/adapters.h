@@ -313,7 +313,8 @@ __device__ __forceinline__ void in_turn(int steps, LOAD load, COMPUTE compute) {
 
 // Copies columns from .. end of the tokens t0 .. t0 + 63 that have no adapter from base
 // (null: zeros) to y, rows of C; kThreads threads, eight columns and four rows of
-// them under way each. `list` is LDS.
+// them under way each; the last eight may start earlier, and be some that are copied
+// elsewhere too. `list` is LDS.
 template <int kThreads>
 __device__ __forceinline__ void copy_others(const int32_t *__restrict__ ids, int t0, int M, int L, const uint16_t *base,
                                             uint16_t *y, int C, int from, int end, int (&list)[64]) {
@@ -331,7 +332,7 @@ __device__ __forceinline__ void copy_others(const int32_t *__restrict__ ids, int
     int n[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int u = u0 + i * kThreads, c = from + u % units * 8;
+      const int u = u0 + i * kThreads, c = max(min(from + u % units * 8, end - 8), 0);
       n[i] = u < total ? min(end - c, 8) : 0;
       at[i] = u < total ? static_cast<size_t>(list[u / units]) * C + c : 0;
       v[i] = Oct{{0, 0, 0, 0}};

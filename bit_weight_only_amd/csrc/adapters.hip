@@ -324,10 +324,12 @@ __device__ __forceinline__ void others(const int32_t *ids, int t0, int M, int L,
                                        uint16_t *y, float *h, int from, int end) {
   __shared__ int list[64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  if (h && from == 0)
-    for (int t = t0 + wave; t < min(t0 + 64, M); t += kWaves)
-      if (adapter_of(ids, t, L) < 0)
-        for (int j = lane; j < r; j += 64) h[static_cast<size_t>(t) * r + j] = 0.f;
+  if (h && from == 0) {
+    const uint64_t none = __ballot(t0 + lane < M && adapter_of(ids, min(t0 + lane, M - 1), L) < 0);
+    for (int t = wave; t < 64; t += kWaves)
+      if (none >> t & 1)
+        for (int j = lane; j < r; j += 64) h[static_cast<size_t>(t0 + t) * r + j] = 0.f;
+  }
   if (base != y) copy_others<kThreads>(ids, t0, M, L, base, y, N, from, end, list);
 }
 
@@ -545,8 +547,13 @@ ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
       p.steps = 1;
     }
   } else {
-    const long rows = static_cast<long>(g.M) * ((g.N + 64 * p.e - 1) / (64 * p.e)) / 1024;
-    p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, 128l), static_cast<long>(kMostTokens)));
+    // chunks so long that 1024 workgroups have one each, but at least 128 tokens (4000
+    // tokens of 96 adapters, 2048 columns 13.6 us, with 32 18.9), or 32 where that is
+    // still no more than a workgroup a compute unit (257 tokens, 2047 columns 16.2 us with
+    // 128, 11.0 with 32)
+    const long groups = (g.N + 64 * p.e - 1) / (64 * p.e), rows = g.M * groups / 1024;
+    const long least = (g.M / 32 + some) * groups <= 256 ? 32 : 128;
+    p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, least), static_cast<long>(kMostTokens)));
     p.chunks = g.M / p.rows + some;
   }
   p.tiles = p.few && p.by_token ? g.M : g.M / unit + some;
