@@ -3,7 +3,11 @@
 //
 //   h_t = x_t A_a^T        y_t = base_t + s_a h_t B_a^T
 //
-// in two launches; nothing uses atomics, so repeated calls give identical bits.
+// in two launches, or one; nothing uses atomics, so repeated calls give identical bits.
+//
+// The products are thin (r values): what bounds them is reading x and base and writing
+// y, or, for few tokens, a load's latency and the launches. h stays fp32 between
+// them.
 #include "adapters.h"
 
 #include <algorithm>
@@ -163,7 +167,9 @@ __device__ __forceinline__ void join(const float4_t (&acc)[TF][RF], float4_t *re
 
 // Few tokens: part[s][row][j] = the sum over the s-th share of K, a tile per
 // workgroup column. BY_TOKEN: every token is a tile of its own, and a row its
-// number; else rows are list entries.
+// number; else rows are list entries. Bound by latency (64 tokens on 64 adapters of 4096
+// columns, rank 16: 5.0 us for 9 MB), which is why K is cut up until there are about
+// 512 workgroups, with at most kMostShares shares, that the next launch reads at once.
 template <int DT, int RF, bool BY_TOKEN>
 __global__ void __launch_bounds__(kThreads) adapters_shares_kernel(const uint16_t *__restrict__ x, int M, int K, int r,
                                                                    const uint16_t *__restrict__ A, int L,
@@ -191,7 +197,9 @@ __global__ void __launch_bounds__(kThreads) adapters_shares_kernel(const uint16_
   });
 }
 
-// Many tokens: a workgroup takes a tile's whole K, and leaves h as the operands
+// Many tokens, bound by reading x (8192 tokens of 14336, rank 8: 235 MB in 44.5 us, 5.3
+// TB/s; 1777 tokens of 5120, rank 64: 18.2 us, 71 workgroups' latency): a workgroup
+// takes a tile's whole K, and leaves h as the operands
 // that the second product loads: pieces[(tile TF + f) RC + c][lane], back[tile 16 TF + t].
 // Shares of K with their sums made in the second product, once per 2048 columns, cost
 // more than they gave (1777 tokens, 5120 -> 17408, rank 64: both kernels 134 us).
@@ -333,7 +341,9 @@ __device__ __forceinline__ void others(const int32_t *ids, int t0, int M, int L,
   if (base != y) copy_others<kThreads>(ids, t0, M, L, base, y, N, from, end, list);
 }
 
-// Few tokens: one tile of up to 16 a workgroup column. FROM: h is the sum of the shares,
+// Few tokens: one tile of up to 16 a workgroup column, bound by reading B (64 tokens on
+// 64 adapters, 28672 columns, rank 16: 12.6 us, 4.6 TB/s) or, for a few tokens, by
+// latency (one token, 4096 columns 6.2 us in one launch). FROM: h is the sum of the shares,
 // by token or by list entry, or (by token) is made here, by every workgroup for
 // itself: one launch less, for A's way to each of them from the caches (kOneBytes).
 enum { kByToken, kByEntry, kOneLaunch };
@@ -432,7 +442,10 @@ __global__ void __launch_bounds__(FROM == kOneLaunch ? kManyThreads : kThreads) 
 // Many tokens: a wavefront takes 16 E columns, whose part of B stays in registers,
 // and goes through a chunk of an adapter's tokens, 16 TF a step. D's rows are tokens,
 // so that a lane holds E neighbouring columns of four of them. UNIT: tokens of the
-// tiles in which h's operands were made.
+// tiles in which h's operands were made. Slices of columns are neighbours in the grid, so
+// that rows are read and written whole by workgroups that run together. Bound by
+// HBM: 8192 tokens, 14336 columns, rank 16 87 us for 470 MB, 5.4 TB/s; rank 64, 119
+// us, 4.0, of which the matrix cores' part no longer hides.
 template <int DT, int E, int TF, int RC, int RANK>
 __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
     const Oct *__restrict__ pieces, const float *__restrict__ backs, int unit, int M, int N, int r,
@@ -520,6 +533,7 @@ struct ForwardPlan {
   int rows, chunks;     // many tokens: of a chunk, at most
   size_t pieces, back, pad, total;   // where in the workspace (part at its start)
 };
+// up to so many tokens a call has no sort and no operands laid out between its launches
 constexpr int kFewTokens = 64;
 // A's bytes that a workgroup reads to make h for itself, and such workgroups, at most:
 // one token of 4096 -> 4096 at rank 16 takes 10.6 us called one by one and 6.2 in a
@@ -533,7 +547,8 @@ ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
   const int frags = (g.r + 15) / 16;
   p.rf = frags <= 1 ? 1 : frags <= 2 ? 2 : frags <= 4 ? 4 : 8;
   const int some = std::max(1, std::min(g.L, g.M));
-  // tokens of an adapter on average decide the tile
+  // tokens of an adapter on average decide the tile: two pieces of 16 tokens share A's
+  // operands, where they would not mostly be empty (rank above 64: registers)
   p.tf = p.few || g.M / some <= 16 || p.rf == 8 ? 1 : 2;
   const int unit = 16 * p.tf, spans = (g.N + kSpan - 1) / kSpan;
   p.e = p.rf <= 2 ? 8 : 4;

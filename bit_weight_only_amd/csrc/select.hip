@@ -256,7 +256,11 @@ constexpr int kMostGroups = 64;
 // row's largest score, and all of them together by their sum's up to 24 u; `near` is
 // twice the one and more than the other.
 //
-// What bounds it is instructions: 4 tokens a wavefront, (top_k + 1) rounds.
+// What bounds it is instructions: (top_k + 1) rounds, for 4 tokens at once with 16 lanes
+// a token (131072 tokens of 256 experts, 8 picks, sigmoid with bias: 102 us, 276
+// instructions a token, 0.8 TB/s). Few tokens take a wavefront each, whose lists are
+// shorter: softmax over 256 experts 5.8 us against 7.2 for 2048 tokens, 7.8 against
+// 7.4 for 4096 (32 tokens 5.4 us).
 template <int DT, int LANES, int V>
 __global__ void __launch_bounds__(kSelectThreads, 3) moe_select_kernel(MoeSelect r, const void *__restrict__ logits, int M,
                                                                     const float *__restrict__ bias,
@@ -438,7 +442,8 @@ __global__ void __launch_bounds__(kSelectThreads, 3) moe_select_kernel(MoeSelect
   }
 }
 
-// All tokens in 64 bits.
+// All tokens in 64 bits: for more than kMostGroups groups, a bit each of a mask in the
+// fast form.
 template <int DT>
 __global__ void __launch_bounds__(kSelectThreads) moe_select_exact_kernel(MoeSelect r, const void *__restrict__ logits,
                                                                           int M, const float *__restrict__ bias,
@@ -458,6 +463,7 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_exact_kernel(MoeSel
 // but for plain softmax a token's row is zeros and a few values, and of the logits
 // only the picked are read. What bounds it then is writing the rows.
 //
+// 131072 rows of 256 bf16 values 24.8 us (67 MB written, parts of as much read).
 // 16 lanes a token; the row is put together in LDS, slot after slot, so that an expert
 // named twice gets both.
 template <int DT, int V>
