@@ -20,6 +20,8 @@ using namespace mxfp4;
 
 constexpr int kSelectThreads = 256, kWaves = kSelectThreads / 64;
 constexpr double kNone = -__builtin_inf();
+// Softmax scores of logits this much below their row's largest are 0 in 64 bits.
+constexpr double kNothing = -745.;
 
 // Value of the lane N further round in its row of 16.
 template <int N>
@@ -129,6 +131,12 @@ __device__ __forceinline__ void select_exactly(const MoeSelect &r, const void *_
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
   double mine = id >= 0 ? score(logit(id)) : 0.;
+  if (r.renormalise && r.score == kSoftmax) {
+    // the ratio of scores that keep few bits themselves
+    const double l = id >= 0 ? logit(id) : kNone;
+    const double most = row_all<64>(l, [](double a, double b) { return fmax(a, b); });
+    mine = l - top > kNothing ? exp(l - most) : 0.;
+  }
   const double total = row_all<64>(mine, [](double a, double b) { return a + b; });
   if (lane < r.top_k) {
     if (r.renormalise) mine = total > 0. ? mine / total : 0.;
@@ -403,21 +411,31 @@ __global__ void __launch_bounds__(kSelectThreads, 3) moe_select_kernel(MoeSelect
       }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    float p[2] = {0.f, 0.f}, total = 0.f;
+    float p[2] = {0.f, 0.f}, x[2] = {-INFINITY, -INFINITY}, total = 0.f;
     int id[2] = {-1, -1};
 #pragma unroll
     for (int n = 0; n < (LANES == 16 ? 2 : 1); ++n) {
       const int j = lane + LANES * n;
       if (j >= r.top_k || pick[j] < kFirst) continue;
       id[n] = expert_of(pick[j]);
-      const float x = fminf(to_f32<DT>(row[id[n]]), 3.4028234663852886e38f);
-      p[n] = score_of(x, r.score, top);
+      x[n] = fminf(to_f32<DT>(row[id[n]]), 3.4028234663852886e38f);
       if (!by_logit && pick[j + 1] >= kFirst && !(value_of(pick[j]) - value_of(pick[j + 1]) > near)) {
         // as near as that, but for the same logit and bias
         const int o = expert_of(pick[j + 1]);
         const float y = fminf(to_f32<DT>(row[o]), 3.4028234663852886e38f);
-        open = open || x != y || (bias && bias[id[n]] != bias[o]);
+        open = open || x[n] != y || (bias && bias[id[n]] != bias[o]);
       }
+    }
+    // a ratio of softmax scores is taken relative to the largest pick, which a bias can keep
+    // far below the row's largest (64 bits know where such scores end)
+    float from = top;
+    if (r.score == kSoftmax && r.renormalise && !by_logit) {
+      from = row_max<LANES>(fmaxf(x[0], x[1]));
+      open = open || (from > -INFINITY && top - from > 600.f);
+    }
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      if (id[n] >= 0) p[n] = score_of(x[n], r.score, from);
       total += p[n];
     }
     total = row_sum<LANES>(total);
@@ -456,16 +474,48 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_exact_kernel(MoeSel
 
 // ------------------------------------------------------------------ gradient
 
+// The largest of E <= 16 V logits, NaN being none, in each of a token's 16 lanes. All
+// loads are under way at once; a piece that would reach past the last starts earlier.
+template <int DT, int V>
+__device__ __forceinline__ float row_top(const typename Elem<DT>::type *row, int E, int lane) {
+  using T = typename Elem<DT>::type;
+  constexpr int P = 16 / sizeof(T), kPieces = (V + P - 1) / P;
+  struct __attribute__((packed, aligned(sizeof(T)))) Piece {
+    T v[P];
+  };
+  float top = -INFINITY;
+  if (E >= P) {
+    Piece p[kPieces];
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k)
+      if (k * 16 * P < E) p[k] = *reinterpret_cast<const Piece *>(row + min((k * 16 + lane) * P, E - P));
+#pragma unroll
+    for (int k = 0; k < kPieces; ++k) {
+      if (k * 16 * P >= E) continue;
+#pragma unroll
+      for (int i = 0; i < P; ++i) top = fmaxf(top, to_f32<DT>(p[k].v[i]));
+    }
+  } else {
+    top = fmaxf(top, to_f32<DT>(row[min(lane, E - 1)]));
+  }
+  return fminf(row_max<16>(top), 3.4028234663852886e38f);
+}
+
 // d_logits of the weights' gradient: with S = sum of the picked p (renormalised) or
 // 1, ds_j = scale (g_j - [renormalised] sum_i p_i g_i / S) / S, then the score's own
 // derivative: sigmoid p (1 - p) ds, softmax p_e (ds_e - sum p ds). With renormalised
 // softmax the last sum is zero, and the logits that were not picked fall out of it: so
-// but for plain softmax a token's row is zeros and a few values, and of the logits
-// only the picked are read. What bounds it then is writing the rows.
+// but for plain softmax a token's row is zeros and a few values. What bounds it then is
+// writing the rows.
 //
-// 131072 rows of 256 bf16 values 24.8 us (67 MB written, parts of as much read).
+// Sigmoid, of whose logits only the picked are read: 131072 rows of 256 bf16 values 24.8
+// us (67 MB written, parts of as much read).
 // 16 lanes a token; the row is put together in LDS, slot after slot, so that an expert
 // named twice gets both.
+//
+// Renormalised softmax takes the picks relative to their largest, and reads the whole row
+// for the largest there: what 64 bits hold as 0 has no weight, and no gradient (131072
+// rows of 256 bf16 values 30.6 us; 24.1 without that).
 template <int DT, int V>
 __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
     MoeSelect r, const float *__restrict__ d_w, const void *logits, int M, const int32_t *__restrict__ ids,
@@ -483,6 +533,8 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
       const float v = to_f32<DT>(row[e]);
       return v > -INFINITY ? fminf(v, 3.4028234663852886e38f) : -INFINITY;
     };
+    float most = -INFINITY;
+    if (r.score == kSoftmax && r.renormalise) most = row_top<DT, V>(row, r.E, lane);
     int id[2];
     float l[2], g[2], top = -INFINITY;
 #pragma unroll
@@ -519,6 +571,7 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       p[n] = !(l[n] > -INFINITY) ? 0.f : far ? expf(l[n] - top) : score_of(l[n], r.score, top) * inv;
+      if (r.score == kSoftmax && r.renormalise && !(static_cast<double>(l[n]) - most > kNothing)) p[n] = 0.f;
       S += p[n];
       dot += p[n] * g[n];
     }

@@ -568,7 +568,9 @@ typedef struct {
  *   ids[t][j] = the expert with the j-th largest c in those groups, ties to the
  *   lower id; weights[t][j] = scale p_id / (renormalise ? sum over the picks of
  *   p : 1), fp32 (0 where that sum is 0).
- * Larger is decided as 64-bit arithmetic decides it. An expert whose logit is
+ * Larger is decided as 64-bit arithmetic decides it. Softmax scores of logits 745 or
+ * more below the row's largest count as 0; others keep their ratio, where a bias
+ * leaves only such small ones to be picked too. An expert whose logit is
  * -infinity or NaN has p = 0 and is not picked, nor is one whose bias is; a
  * token with fewer experts than top_k has ids -1 and weights 0 behind them (no
  * picks to lbq_moe_sort). Logits of +infinity count as the largest fp32 value.
@@ -585,7 +587,7 @@ lbq_status lbq_moe_select(const lbq_router *r, const void *logits, int32_t dtype
  *   ds_j = scale (d_weights_j - [renormalise] sum_i p_i d_weights_i / S) / S,
  * summed over the slots of an expert, and d_l_e = p_e (1 - p_e) ds_e (sigmoid) or
  * p_e (ds_e - sum_i p_i ds_i) (softmax). The choice itself has no gradient, nor
- * has the bias. Slots with ids outside [0, E) count nothing, whatever their
+ * has the bias, and a score that counts as 0 gives 0. Slots with ids outside [0, E) count nothing, whatever their
  * d_weights. Experts that may not be picked get 0. d_logits may be logits. */
 lbq_status lbq_moe_select_backward(const lbq_router *r, const float *d_weights, const void *logits, int32_t dtype,
                                    const int32_t *ids, int32_t M, void *d_logits, void *stream);

@@ -296,3 +296,55 @@ def test_refusals(L, dev):
     for f in bad:
         with pytest.raises(L.LbqError):
             f()
+
+
+# (tokens, experts, picks, groups, top groups, group picks): every form of the kernel
+FAR_SHAPES = [(9, 40, 3, 1, 1, 1), (9, 48, 4, 6, 3, 2), (12, 256, 8, 1, 1, 1), (2052, 200, 5, 1, 1, 1), (2049, 256, 8, 8, 4, 2),
+              (10, 300, 32, 1, 1, 1), (7, 1000, 13, 1, 1, 1), (5, 960, 6, 80, 30, 2)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,E,k,G,tg,gp", FAR_SHAPES)
+def test_picks_far_below_the_rows_largest(L, dev, m, E, k, G, tg, gp, dtype):
+    """Softmax: where the bias keeps the row's largest from being picked, the picks' weights still have their ratio, and
+    the gradient is that ratio's. More than 745 below it 64 bits hold their p as 0: weights and gradient are 0."""
+    import torch
+
+    g = synth.rng(93, E, synth.ROLE_X)
+    bias = (0.1 * g.standard_normal(E)).astype(np.float32)
+    dw = g.standard_normal((m, k)).astype(np.float32)
+    first = E // 3
+    for gap in (60, 80, 90, 100, 110, 300, 690, 800):
+        say(f"moe_select far below m={m} E={E} groups={G} {dtype} gap={gap}")
+        lg = _logits(m, E, dtype, 17, spread=1.0)
+        lg[:, first] = lg.amax(1) + gap
+        for b0 in (-np.inf, -3.0):
+            b = bias.copy()
+            b[first] = b0
+            how = dict(score=0, groups=G, top_groups=tg, group_picks=gp)
+            ids, w = _check(L, lg, k, b, **how)
+            assert not bool((ids == first).any())
+            assert bool((w.sum(1) == 0).all()) if gap == 800 else np.all(np.abs(w.sum(1) - 1) <= 16 * A.U)
+            d = L.moe_select_backward(torch.from_numpy(dw).cuda(), lg.cuda(), ids, score=0)
+            want, bound = A.select_backward(dw.astype(np.float64), lg.double().numpy(), ids.cpu().numpy(), 0)
+            err = np.abs(d.double().cpu().numpy() - want)
+            assert np.all(err <= bound * 1.01 + HALF[dtype] * np.abs(want) + TINY[dtype] + 2.0 ** -120), err.max()
+            _check(L, lg, k, b, renormalise=False, **how)
+
+
+def test_one_pick_past_the_border(L, dev):
+    """One pick just inside what 64 bits hold, the other outside."""
+    import torch
+
+    lg = torch.tensor([[0.0, -740.0, -750.0, -751.0], [0.0, -80.0, -120.0, -800.0]])
+    b = np.array([-np.inf, 0.3, 0.2, 0.1], np.float32)
+    g = np.array([[1.0, 0.5], [-0.5, 1.0]], np.float32)
+    ids, w = _check(L, lg, 2, b)
+    assert ids.tolist() == [[1, 2], [1, 2]] and w[0].tolist() == [1.0, 0.0]
+    d = L.moe_select_backward(torch.from_numpy(g).cuda(), lg.cuda(), ids).double().cpu().numpy()
+    # w (g - sum w g): with S = 4e-322 the oracle's g / S overflows
+    _, w = A.select(lg.double().numpy(), 2, b.astype(np.float64))
+    want, bound = np.zeros((2, 4)), np.zeros((2, 4))
+    want[:, 1:3] = w * (g - (w * g).sum(1, keepdims=True))
+    bound[:, 1:3] = w * (np.abs(g) + (w * np.abs(g)).sum(1, keepdims=True)) * (42 + 4 * 80) * A.U
+    assert np.all(np.abs(d - want) <= bound * 1.01 + A.U * np.abs(want) + 2.0 ** -120)
