@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import numpy as np
@@ -850,12 +851,18 @@ def moe_combine_backward(dy, o, pos, weights, d_o=None, d_weights=None, stream=N
 
 # ------------------------------------------------------------------ expert selection
 
-@functools.lru_cache(maxsize=256)
 def _router(E, top_k, score, groups, top_groups, group_picks, renormalise, scale):
+    """The struct of these settings, kept by their values: what can change in place (a tensor as scale) is read now."""
+    at = operator.index
+    return _router_of(E, at(top_k), at(score), at(groups), at(top_groups), at(group_picks), bool(renormalise), float(scale))
+
+
+@functools.lru_cache(maxsize=256)
+def _router_of(E, top_k, score, groups, top_groups, group_picks, renormalise, scale):
     for n in (E, top_k, score, groups, top_groups, group_picks):
         if not -_MOST <= n <= _MOST:
             raise LbqError(-2, f"router: {n}")
-    return ctypes.byref(Router(E, top_k, score, groups, top_groups, group_picks, bool(renormalise), scale))
+    return ctypes.byref(Router(E, top_k, score, groups, top_groups, group_picks, renormalise, scale))
 
 
 def moe_select(logits, top_k: int, bias=None, score: int = SCORE_SOFTMAX, groups: int = 1, top_groups: int = 1,

@@ -125,3 +125,19 @@ def test_binding_refuses_cpu_tensors_and_shapes(L):
         L.Adapters(torch.zeros(4, 128).half(), torch.zeros(2, 16, 4).half(), torch.ones(2))
     with pytest.raises(L.LbqError):
         L.moe_select(torch.zeros(4, 8), 2 ** 40)
+
+
+def test_router_holds_what_its_arguments_are_now(L):
+    """A tensor or array as scale or switch that changes in place between calls, and settings that are equal as keys."""
+    import numpy as np
+    import torch
+
+    for of in (torch.tensor, np.array):
+        scale, k, on = of(2.0), of(4), of(True)
+        for v in ((2.0, 4, True), (3.0, 5, False), (2.0, 4, True)):
+            scale[()], k[()], on[()] = v
+            s = L._router(64, k, 1, 8, 2, 2, on, scale)._obj
+            assert (s.scale, s.top_k, s.renormalise) == v
+    assert L._router(64, 4, 1, 8, 2, 2, 2, 1)._obj.renormalise == 1
+    with pytest.raises(TypeError):
+        L._router(64, 4.5, 1, 8, 2, 2, True, 1.0)
