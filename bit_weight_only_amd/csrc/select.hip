@@ -22,6 +22,8 @@ constexpr int kSelectThreads = 256, kWaves = kSelectThreads / 64;
 constexpr double kNone = -__builtin_inf();
 // Softmax scores of logits this much below their row's largest are 0 in 64 bits.
 constexpr double kNothing = -745.;
+// Sigmoids from this logit down are 0 in 64 bits: exp(-l) is infinite there.
+constexpr float kNoSigmoid = -709.7827f;
 
 // Value of the lane N further round in its row of 16.
 template <int N>
@@ -570,14 +572,14 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
     const bool far = r.score == kSigmoid && r.renormalise && top < -60.f && top > -INFINITY;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      p[n] = !(l[n] > -INFINITY) ? 0.f : far ? expf(l[n] - top) : score_of(l[n], r.score, top) * inv;
+      p[n] = !(l[n] > -INFINITY) ? 0.f : far ? (l[n] > kNoSigmoid ? expf(l[n] - top) : 0.f) : score_of(l[n], r.score, top) * inv;
       if (r.score == kSoftmax && r.renormalise && !(static_cast<double>(l[n]) - most > kNothing)) p[n] = 0.f;
       S += p[n];
       dot += p[n] * g[n];
     }
     S = row_sum<kLanes>(S);
     dot = row_sum<kLanes>(dot);
-    const float over = !r.renormalise ? 1.f : S > 0.f && (!far || top > -745.f) ? 1.f / S : 0.f;
+    const float over = !r.renormalise ? 1.f : S > 0.f ? 1.f / S : 0.f;
     const float mean = r.renormalise ? dot * over : 0.f;
     float across = 0.f;
 #pragma unroll

@@ -568,12 +568,13 @@ typedef struct {
  *   ids[t][j] = the expert with the j-th largest c in those groups, ties to the
  *   lower id; weights[t][j] = scale p_id / (renormalise ? sum over the picks of
  *   p : 1), fp32 (0 where that sum is 0).
- * Larger is decided as 64-bit arithmetic decides it. Softmax scores of logits 745 or
- * more below the row's largest count as 0; others keep their ratio, where a bias
- * leaves only such small ones to be picked too. An expert whose logit is
- * -infinity or NaN has p = 0 and is not picked, nor is one whose bias is; a
- * token with fewer experts than top_k has ids -1 and weights 0 behind them (no
- * picks to lbq_moe_sort). Logits of +infinity count as the largest fp32 value.
+ * Larger is decided as 64-bit arithmetic decides it. What it holds as 0 counts as 0:
+ * softmax scores of logits 745 or more below the row's largest, sigmoids of logits
+ * below -709.78; smaller picks than fp32 holds keep their ratio up to there. An
+ * expert whose logit is -infinity or NaN has p = 0 and is not picked, nor is one
+ * whose bias is; a token with fewer experts than top_k has ids -1 and weights 0
+ * behind them (no picks to lbq_moe_sort). Logits of +infinity count as the largest
+ * fp32 value.
  *   bias: fp32 [E] or NULL; ids: int32 [M][top_k]; weights: fp32 [M][top_k];
  *   M * top_k <= 2^24. logits 16-byte aligned.
  * Errors, before any launch: LBQ_ERR_NULL, _SHAPE, _FORMAT (dtype, score),

@@ -348,3 +348,40 @@ def test_one_pick_past_the_border(L, dev):
     want[:, 1:3] = w * (g - (w * g).sum(1, keepdims=True))
     bound[:, 1:3] = w * (np.abs(g) + (w * np.abs(g)).sum(1, keepdims=True)) * (42 + 4 * 80) * A.U
     assert np.all(np.abs(d - want) <= bound * 1.01 + A.U * np.abs(want) + 2.0 ** -120)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("shift", [-690.0, -720.0, -800.0])
+def test_sigmoids_that_64_bits_cannot_hold(L, dev, shift, dtype):
+    """1 / (1 + exp(-l)) is 0 in 64 bits from l = -709.78 down: weights and gradient end at the same place."""
+    import torch
+
+    for bias in (None, (0.1 * synth.rng(94, 0, synth.ROLE_X).standard_normal(96)).astype(np.float32)):
+        lg = (_logits(40, 96, "float32", 3) + shift).to(getattr(torch, dtype))
+        ids, w = _check(L, lg, 6, bias, score=1)
+        assert np.all(w == 0) if shift < -710 else np.all(np.abs(w.sum(1) - 1) <= 16 * A.U)
+        g = synth.rng(89, 0, synth.ROLE_X).standard_normal((40, 6)).astype(np.float32)
+        d = L.moe_select_backward(torch.from_numpy(g).cuda(), lg.cuda(), ids, score=1).double().cpu().numpy()
+        want, bound = A.select_backward(g.astype(np.float64), lg.double().numpy(), ids.cpu().numpy(), 1)
+        # (the argument of exp is off by its own rounding)
+        assert np.all(np.abs(d - want) <= bound * (1.01 + abs(shift) / 4) + HALF[dtype] * np.abs(want) + 1e-30)
+
+
+def test_sigmoids_around_the_border(L, dev):
+    """Some picks on this side of it, some on the other."""
+    import torch
+
+    edge = np.float32(-709.7827)                               # the last that 64 bits hold is one step above
+    lg = torch.tensor([[-709.0, -710.0, -711.0], [float(np.nextafter(edge, np.float32(0))), float(edge), -800.0],
+                       [float(edge), -710.0, -720.0], [-100.0, -705.0, -715.0]])
+    g = np.array([[1.0, 0.5], [-0.5, 1.0], [1.0, 2.0], [3.0, -1.0]], np.float32)
+    ids, w = _check(L, lg, 2, score=1)
+    assert w.tolist()[:3] == [[1.0, 0.0], [1.0, 0.0], [0.0, 0.0]]
+    d = L.moe_select_backward(torch.from_numpy(g).cuda(), lg.cuda(), ids, score=1).double().cpu().numpy()
+    # w (1 - p) (g - sum w g), 1 - p = 1 here: with S = 6e-309 the oracle's g / S overflows
+    _, w = A.select(lg.double().numpy(), 2, score=1)
+    want, bound = np.zeros((4, 3)), np.zeros((4, 3))
+    want[:, :2] = w * (g - (w * g).sum(1, keepdims=True))
+    bound[:, :2] = w * (np.abs(g) + (w * np.abs(g)).sum(1, keepdims=True)) * 42 * A.U
+    # (the argument of exp is off by its own rounding)
+    assert np.all(np.abs(d - want) <= bound * (1.01 + 720 / 4) + A.U * np.abs(want) + 1e-30)
