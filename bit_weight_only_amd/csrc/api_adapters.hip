@@ -75,12 +75,17 @@ AdapterLayout adapter_layout(const AdapterArgs &g, bool sorts, bool backward) {
   return l;
 }
 
+// Whether a call makes the order itself; the query and the calls ask here.
+bool makes_order(const AdapterArgs &g, bool given, bool backward) {
+  return !given && (backward || adapters_forward_by_list(g));
+}
+
 lbq_status workspace(const lbq_adapters *ad, int32_t M, int32_t sorted, bool backward, size_t *bytes) {
   if (!bytes) return LBQ_ERR_NULL;
   const lbq_status st = check_adapters(ad, M);
   if (st != LBQ_OK) return st;
   const AdapterArgs g = adapter_args(ad, M);
-  *bytes = adapter_layout(g, !sorted && (backward || adapters_forward_by_list(g)), backward).total;
+  *bytes = adapter_layout(g, makes_order(g, sorted != 0, backward), backward).total;
   return LBQ_OK;
 }
 
@@ -144,7 +149,7 @@ lbq_status lbq_adapters_forward(const lbq_adapters *ad, const void *x, int32_t M
       !aligned(offsets, 4) || !aligned(perm, 4) || !aligned(ws, 16))
     return LBQ_ERR_ALIGN;
   AdapterArgs g = adapter_args(ad, M);
-  const bool sorts = !offsets && adapters_forward_by_list(g);
+  const bool sorts = makes_order(g, offsets != nullptr, false);
   const AdapterLayout l = adapter_layout(g, sorts, false);
   if (l.total > 0 && !ws) return LBQ_ERR_NULL;
   if (ws_bytes < l.total) return LBQ_ERR_WORKSPACE;
@@ -169,7 +174,7 @@ lbq_status lbq_adapters_backward(const lbq_adapters *ad, const void *dy, const v
       !aligned(ws, 16))
     return LBQ_ERR_ALIGN;
   AdapterArgs g = adapter_args(ad, M);
-  const bool sorts = M == 0 || !offsets;
+  const bool sorts = makes_order(g, offsets != nullptr, true);   // (M = 0: offsets alone, of whatever values)
   const AdapterLayout l = adapter_layout(g, sorts, true);
   if (l.total > 0 && !ws) return LBQ_ERR_NULL;
   if (ws_bytes < l.total) return LBQ_ERR_WORKSPACE;

@@ -500,3 +500,25 @@ def test_other_device_index_is_refused(L, dev):
         with pytest.raises(L.LbqError):
             g()
             raise AssertionError(i)
+
+
+def test_no_tokens_with_an_order(L, dev):
+    """An empty batch whose program keeps an order: the gradients are zeros, in the workspace that the query names."""
+    import torch
+
+    c = Case(L, 3, 128, 40, 2, 4, "float16")
+    e = torch.empty(0, 128, device="cuda", dtype=torch.float16)
+    ids = torch.empty(0, dtype=torch.int32, device="cuda")
+    _, off, perm, _ = L.moe_sort(ids[:, None].contiguous(), 2)
+    assert off.tolist() == [0, 0, 0] and perm.numel() == 0
+    need = c.ad.workspace_bytes(0, True, True)
+    for ws in (None, torch.empty(need, dtype=torch.uint8, device="cuda")):
+        for order in ((off, perm), None, (torch.tensor([0, 5, 9], dtype=torch.int32, device="cuda"), perm)):
+            if order is None and ws is not None:
+                ws = torch.empty(c.ad.workspace_bytes(0, False, True), dtype=torch.uint8, device="cuda")
+            h = torch.empty(0, 4, device="cuda")
+            assert L.adapters_forward(c.ad, e, ids, h=h, order=order).shape == (0, 40)
+            dx, da, db = L.adapters_backward(c.ad, e.new_empty(0, 40), e, h, ids, order=order, ws=ws,
+                                             d_a=torch.ones(2, 4, 128, device="cuda"),
+                                             d_b=torch.ones(2, 40, 4, device="cuda"))
+            assert dx.shape == (0, 128) and not da.any() and not db.any()

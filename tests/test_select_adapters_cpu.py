@@ -141,3 +141,15 @@ def test_router_holds_what_its_arguments_are_now(L):
     assert L._router(64, 4, 1, 8, 2, 2, 2, 1)._obj.renormalise == 1
     with pytest.raises(TypeError):
         L._router(64, 4.5, 1, 8, 2, 2, True, 1.0)
+
+
+def test_no_tokens_take_the_workspace_of_the_query(L):
+    """M = 0: the gradients ask for what their query names (the call itself, with zeros to write, needs a GPU)."""
+    n, ad = ctypes.c_size_t(), _ad(L)
+    q = L.lib().lbq_adapters_backward_workspace
+    assert q(ad, 0, 1, ctypes.byref(n)) == OK and n.value == 0
+    assert q(ad, 0, 0, ctypes.byref(n)) == OK and n.value > 0
+    assert _backward(L, ad, M=0, off=None, perm=None, size=n.value - 1) == WORKSPACE
+    assert _backward(L, ad, M=0, off=None, perm=None, ws=None) == NULL
+    for name in ("da", "db"):
+        assert _backward(L, ad, M=0, **{name: None}) == NULL
