@@ -90,6 +90,11 @@ struct Staged {
   }
 };
 
+// Between a wavefront's writes to LDS and its lanes' reads of one another's, and back. No
+// instruction: a wavefront's accesses stay in order by themselves, if the compiler keeps
+// them so. Of LDS alone: loads from memory stay under way.
+__device__ __forceinline__ void lds_exchange() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local"); }
+
 // The sums over blocks lo + wave, lo + wave + WAVES, .. below hi of a tile of up to
 // 16 TF tokens and 16 RF values. Rows and values past the last are copies of the
 // last (their results are dropped), so nothing is masked.
@@ -131,6 +136,7 @@ __device__ __forceinline__ void shrink(const uint16_t *__restrict__ x, int M, in
       [&](const Block &v, int) {
         v.x.lay(xl);
         v.w.lay(wl);
+        lds_exchange();
 #pragma unroll
         for (int s = 0; s < S; ++s) {
           Oct a[TF];
@@ -143,6 +149,7 @@ __device__ __forceinline__ void shrink(const uint16_t *__restrict__ x, int M, in
             for (int f = 0; f < TF; ++f) acc[f][g] = mfma<DT>(a[f], w, acc[f][g]);
           }
         }
+        lds_exchange();   // the next block's values go to the same place
       });
 }
 
