@@ -52,8 +52,8 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 
 // PIECES 16-bit values whose sum is v[i] to 11 or 8 bits each (f16, bf16): out[p] holds
 // the p-th pieces of the eight values. An fp32 sum enters a second product so, and
-// loses no more than the second sum's own roundings (two pieces: 2^-21 and 2^-16 of
-// it, below the result's own 2^-11 and 2^-8; three pieces of bf16: 2^-23).
+// loses no more than the second sum's own roundings (two pieces of fp16 2^-21 of it,
+// three of bf16 2^-23).
 template <int DT, int PIECES>
 __device__ __forceinline__ void split8(const float v[8], Oct out[PIECES]) {
 #pragma unroll
@@ -69,6 +69,50 @@ __device__ __forceinline__ void split8(const float v[8], Oct out[PIECES]) {
       }
     }
   }
+}
+
+// Pieces of a sum that enters another product.
+template <int DT>
+constexpr int kPieces = DT == kF16 ? 2 : 3;
+
+// h (or u) as operands of a product with B (or A), whose operand c has values 16 c + 8
+// (q % 2) .. + 7 in lanes q = lane / 16, so each of 16 values twice along the instruction's
+// k: its first pieces meet the one, its second pieces the other. The third pieces of bf16 are
+// operands of their own: of 32 values at once, where there are as many, against halves of
+// two of the other side's operands.
+template <int DT, int RC>
+constexpr int kOperands = RC + (DT == kBF16 ? (RC + 1) / 2 : 0);
+__host__ __device__ constexpr int operands_of(int dtype, int rc) { return rc + (dtype == kBF16 ? (rc + 1) / 2 : 0); }
+
+// From a lane's eight values of each 16, as above.
+template <int DT, int RC>
+__device__ __forceinline__ void lay_operands(const float (&v)[RC][8], int q, Oct (&out)[kOperands<DT, RC>]) {
+#pragma unroll
+  for (int c = 0; c < RC; ++c) {
+    Oct p[kPieces<DT>];
+    split8<DT, kPieces<DT>>(v[c], p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out[c].w[i] = q < 2 ? p[0].w[i] : p[1].w[i];
+      if constexpr (DT == kBF16) {
+        uint32_t &third = out[RC + c / 2].w[i];
+        if (c % 2 == 0) third = q < 2 ? p[2].w[i] : 0u;
+        else third = q < 2 ? third : p[2].w[i];
+      }
+    }
+  }
+}
+
+// Operand k of the other side for operand k of h, k < kOperands.
+template <int RC>
+__device__ __forceinline__ Oct beside(const Oct (&b)[RC], int k, int q) {
+  if (k < RC) return b[k];
+  const int c = 2 * (k - RC);
+  if (RC == 1) return b[0];   // (against zeros from q = 2 on)
+  Oct o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o.w[i] = q < 2 ? b[c].w[i] : b[RC == 1 ? 0 : c + 1].w[i];
+  return o;
 }
 
 // A power of two that brings magnitudes up to m into fp16's range with all of its

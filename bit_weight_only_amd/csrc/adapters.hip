@@ -30,12 +30,11 @@ __device__ __forceinline__ int adapter_of(const int32_t *ids, int t, int L) {
 // the row. Of those read twice (below j) h gives zeros.
 __device__ __forceinline__ int first_value(int j, int r) { return r > 8 && r % 8 != 0 ? min(j, r - 8) : j; }
 
-// One lane's share of h as an operand: values from j = 16 c + 8 (q % 2) on of a row of
-// h in LDS, in two 16-bit pieces: the first for q < 2, their rests for the others;
-// times a power of two of the token, whose inverse is `back`. Lane q's partner
+// One lane's share of h as operands: values from j = 16 c + 8 (q % 2) on of a row of
+// h in LDS, times a power of two of the token, whose inverse is `back`. Lane q's partner
 // holds the row's other values.
 template <int DT, int RC>
-__device__ __forceinline__ void pieces_of(const float *row, int r, int q, Oct (&out)[RC], float &back) {
+__device__ __forceinline__ void pieces_of(const float *row, int r, int q, Oct (&out)[kOperands<DT, RC>], float &back) {
   float v[RC][8], top = 0.f;
 #pragma unroll
   for (int c = 0; c < RC; ++c)
@@ -49,14 +48,10 @@ __device__ __forceinline__ void pieces_of(const float *row, int r, int q, Oct (&
   const Scale sc = scale_for<DT>(top);
   back = sc.back;
 #pragma unroll
-  for (int c = 0; c < RC; ++c) {
-    Oct p[2];
+  for (int c = 0; c < RC; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[c][i] *= sc.to;
-    split8<DT, 2>(v[c], p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) out[c].w[i] = q < 2 ? p[0].w[i] : p[1].w[i];
-  }
+  lay_operands<DT, RC>(v, q, out);
 }
 
 // ------------------------------------------------------------------ x A^T
@@ -204,10 +199,10 @@ __global__ void __launch_bounds__(kThreads) adapters_shares_kernel(const uint16_
   });
 }
 
-// Many tokens, bound by reading x (8192 tokens of 14336, rank 8: 235 MB in 44.5 us, 5.3
-// TB/s; 1777 tokens of 5120, rank 64: 18.2 us, 71 workgroups' latency): a workgroup
+// Many tokens, bound by reading x (8192 tokens of 14336, rank 8: 235 MB in 47.0 us, 5.0
+// TB/s; 1777 tokens of 5120, rank 64: 19.0 us, 71 workgroups' latency): a workgroup
 // takes a tile's whole K, and leaves h as the operands
-// that the second product loads: pieces[(tile TF + f) RC + c][lane], back[tile 16 TF + t].
+// that the second product loads: pieces[(tile TF + f) kOperands + k][lane], back[tile 16 TF + t].
 // Shares of K with their sums made in the second product, once per 2048 columns, cost
 // more than they gave (1777 tokens, 5120 -> 17408, rank 64: both kernels 134 us).
 constexpr int kManyThreads = 512;
@@ -232,12 +227,12 @@ __global__ void __launch_bounds__(kManyThreads) adapters_h_kernel(const uint16_t
   __syncthreads();
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   if (wave < TF) {
-    Oct o[RF];
+    Oct o[kOperands<DT, RF>];
     float b;
     pieces_of<DT, RF>(hs + (16 * wave + (lane & 15)) * kStride, r, lane >> 4, o, b);
     const size_t at = static_cast<size_t>(blockIdx.x) * TF + wave;
 #pragma unroll
-    for (int c = 0; c < RF; ++c) pieces[(at * RF + c) * 64 + lane] = o[c];
+    for (int k = 0; k < kOperands<DT, RF>; ++k) pieces[(at * kOperands<DT, RF> + k) * 64 + lane] = o[k];
     if (lane < 16) back[16 * at + lane] = b;
   }
   if (h)
@@ -253,9 +248,7 @@ __global__ void __launch_bounds__(kManyThreads) adapters_h_kernel(const uint16_t
 // ------------------------------------------------------------------ base + s h B^T
 
 // y[t] = base[t] + s_a h_t B_a^T for a tile of tokens, kSpan = 256 columns a step (64 a
-// wave); h_t in two 16-bit
-// pieces side by side along the instruction's k: 16 values of h and their rests
-// against the same 16 values of B twice.
+// wave); h_t in 16-bit pieces (see kOperands).
 //
 // D's rows are columns of y, in an order that leaves a lane eight neighbours:
 // row 4 q + i of instruction m is column 8 q + 4 m + i. A piece of eight columns, or
@@ -293,16 +286,16 @@ __device__ __forceinline__ void load_weights(Oct (&b)[RC], const uint16_t *__res
 // The 64 columns from n0 of 16 tokens: base + back (h B^T), stored to the token's row
 // `to` where it is live. y: base's values, 32 columns each.
 template <int DT, int RC>
-__device__ __forceinline__ void add_product(const Oct (&b)[4][RC], const Oct (&hv)[RC], float back, const Oct (&y)[2],
+__device__ __forceinline__ void add_product(const Oct (&b)[4][RC], const Oct (&hv)[kOperands<DT, RC>], float back, const Oct (&y)[2],
                                             uint16_t *to, bool live, int n0, int N, int width) {
   const int q = threadIdx.x >> 4 & 3;
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     float4_t d[2] = {};
 #pragma unroll
-    for (int c = 0; c < RC; ++c)
+    for (int c = 0; c < kOperands<DT, RC>; ++c)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) d[m] = mfma<DT>(b[2 * k + m][c], hv[c], d[m]);
+      for (int m = 0; m < 2; ++m) d[m] = mfma<DT>(beside(b[2 * k + m], c, q), hv[c], d[m]);
     Oct o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -349,7 +342,7 @@ __device__ __forceinline__ void others(const int32_t *ids, int t0, int M, int L,
 }
 
 // Few tokens: one tile of up to 16 a workgroup column, bound by reading B (64 tokens on
-// 64 adapters, 28672 columns, rank 16: 12.6 us, 4.6 TB/s) or, for a few tokens, by
+// 64 adapters, 28672 columns, rank 16: 13.2 us, 4.4 TB/s) or, for a few tokens, by
 // latency (one token, 4096 columns 6.2 us in one launch). FROM: h is the sum of the shares,
 // by token or by list entry, or (by token) is made here, by every workgroup for
 // itself: one launch less, for A's way to each of them from the caches (kOneBytes).
@@ -421,7 +414,7 @@ __global__ void __launch_bounds__(FROM == kOneLaunch ? kManyThreads : kThreads) 
     }
   }
   __syncthreads();
-  Oct hv[RC];
+  Oct hv[kOperands<DT, RC>];
   float back;
   pieces_of<DT, RC>(hs + col * kStride, r, q, hv, back);
   back *= scales[tile.a];
@@ -451,8 +444,9 @@ __global__ void __launch_bounds__(FROM == kOneLaunch ? kManyThreads : kThreads) 
 // so that a lane holds E neighbouring columns of four of them. UNIT: tokens of the
 // tiles in which h's operands were made. Slices of columns are neighbours in the grid, so
 // that rows are read and written whole by workgroups that run together. Bound by
-// HBM: 8192 tokens, 14336 columns, rank 16 87 us for 470 MB, 5.4 TB/s; rank 64, 119
-// us, 4.0, of which the matrix cores' part no longer hides.
+// HBM: 8192 tokens, 14336 columns, rank 16, bf16 91 us for 470 MB, 5.2 TB/s (with two pieces of
+// h, which lose bits where base and h B^T cancel, 87); rank 64, 146 us, 3.2, of which the
+// matrix cores' part no longer hides (with two pieces 119).
 template <int DT, int E, int TF, int RC, int RANK>
 __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
     const Oct *__restrict__ pieces, const float *__restrict__ backs, int unit, int M, int N, int r,
@@ -477,8 +471,9 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
 #pragma unroll
   for (int e = 0; e < E; ++e) load_weights<RC, RANK>(b[e], B + (static_cast<size_t>(c.a) * N + min(n + e, N - 1)) * r, r);
   const float sa = scales[c.a];
+  constexpr int kOps = kOperands<DT, RC>;
   struct Step {
-    Oct h[TF][RC];
+    Oct h[TF][kOps];
     Rows<E, 4> y[TF];
     float4_t back[TF];
   };
@@ -503,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
           }
           v.back[f] = *reinterpret_cast<const float4_t *>(backs + 16 * at + 4 * q);
 #pragma unroll
-          for (int k = 0; k < RC; ++k) v.h[f][k] = pieces[(at * RC + k) * 64 + lane];
+          for (int k = 0; k < kOps; ++k) v.h[f][k] = pieces[(at * kOps + k) * 64 + lane];
         }
       },
       [&](const Step &v, int s) {
@@ -511,9 +506,9 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
         for (int f = 0; f < TF; ++f) {
           float4_t d[E] = {};
 #pragma unroll
-          for (int k = 0; k < RC; ++k)
+          for (int k = 0; k < kOps; ++k)
 #pragma unroll
-            for (int e = 0; e < E; ++e) d[e] = mfma<DT>(v.h[f][k], b[e][k], d[e]);
+            for (int e = 0; e < E; ++e) d[e] = mfma<DT>(v.h[f][k], beside(b[e], k, q), d[e]);
           size_t row[4];
           bool live[4];
 #pragma unroll
@@ -581,7 +576,7 @@ ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
   p.tiles = p.few && p.by_token ? g.M : g.M / unit + some;
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   if (!p.few) {
-    p.back = up(static_cast<size_t>(p.tiles) * p.tf * p.rf * 64 * sizeof(Oct));
+    p.back = up(static_cast<size_t>(p.tiles) * p.tf * operands_of(g.dtype, p.rf) * 64 * sizeof(Oct));
     p.pad = p.back + up(static_cast<size_t>(p.tiles) * unit * 4);
   } else {
     p.pad = p.one ? 0 : up(static_cast<size_t>(p.splits) * g.M * g.r * 4);
@@ -649,7 +644,11 @@ void forward_rank(const AdapterArgs &g, const ForwardPlan &p, hipStream_t s) {
                        p.chunks, p.tiles);
   };
   auto pick = [&](auto tf) {
-    constexpr int kTF = RC != 2 && RC != 8 ? decltype(tf)::value : 1, kE = RC <= 2 ? 8 : 4;
+    // two pieces of 16 tokens a step where the registers allow it (bf16 up to rank 16, whose
+    // third pieces take some: 8192 tokens, 4096 columns, both launches with two 83 us, with one 79;
+    // rank 64, 2000 tokens, 14336 columns with two 49, with one 55)
+    constexpr bool kTwo = RC == 4 || (RC == 1 && DT == kF16);
+    constexpr int kTF = kTwo ? decltype(tf)::value : 1, kE = RC <= 2 ? 8 : 4;
     auto first = adapters_h_kernel<DT, decltype(tf)::value, RC>;
     if (rank == kWhole) go(first, adapters_y_kernel<DT, kE, kTF, RC, kWhole>);
     else if (rank == kMore) go(first, adapters_y_kernel<DT, kE, kTF, RC, kMore>);

@@ -12,7 +12,7 @@
 // it eight rows of each of its E columns, the operand of E instructions.
 //
 // What bounds them is dy, x and dx, read and written once (8192 tokens, 4096 -> 14336,
-// rank 16, bf16: 437 MB with dx's base, 143 us for all six launches).
+// rank 16, bf16: 437 MB with dx's base, 144 us for all six launches).
 #include "adapters.h"
 
 #include <algorithm>
@@ -30,11 +30,6 @@ constexpr int kE = 4;                                        // columns of a lan
 constexpr int kPieceThreads = 512;
 constexpr int kStep = 32;   // tokens of one step: the instruction's k
 
-// Pieces of h and u in the sums over tokens, which stay fp32: as exact as fp32
-// itself (two pieces of fp16 hold 22 bits, of bf16 only 16).
-template <int DT>
-constexpr int kPieces = DT == kF16 ? 2 : 3;
-
 // ------------------------------------------------------------------ pieces
 
 // The operands that one step's tokens give, in the order in which lanes load them:
@@ -42,9 +37,8 @@ constexpr int kPieces = DT == kF16 ? 2 : 3;
 //         times a power of two of the step's value: the side of the sums over tokens (a
 //         value's tokens meet one another only, so that small values lose nothing beside
 //         large ones);
-//   along [steps][2][RF][64 lanes]: token 16 f + l % 16, its values 16 c + 8 (l / 16 % 2) ..
-//         + 7, first pieces for l < 32 and second ones from there, times the token's
-//         own power of two: the side of u A.
+//   along [steps][2][kOperands][64 lanes]: token 16 f + l % 16, its values as operands of a
+//         product along them, times the token's own power of two: the side of u A.
 struct Pieces {
   Oct *over, *along;
   float *over_back, *along_back;   // [steps][16 RF], [steps][kStep]: the inverse powers
@@ -121,16 +115,14 @@ __global__ void __launch_bounds__(kPieceThreads) adapters_pieces_kernel(const fl
       const Scale st = scale_for<DT>(mt);
       if (q == 0) out.along_back[static_cast<size_t>(c.step) * kStep + t] = st.back;
 #pragma unroll
-      for (int k = 0; k < RF; ++k) {
-        Oct o[2];
+      for (int k = 0; k < RF; ++k)
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[k][i] *= st.to;
-        split8<DT, 2>(w[k], o);
-        Oct mine;
+      Oct o[kOperands<DT, RF>];
+      lay_operands<DT, RF>(w, q, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mine.w[i] = q < 2 ? o[0].w[i] : o[1].w[i];
-        out.along[((static_cast<size_t>(c.step) * 2 + f) * RF + k) * 64 + lane] = mine;
-      }
+      for (int k = 0; k < kOperands<DT, RF>; ++k)
+        out.along[((static_cast<size_t>(c.step) * 2 + f) * kOperands<DT, RF> + k) * 64 + lane] = o[k];
     }
   }
 }
@@ -343,15 +335,15 @@ __global__ void __launch_bounds__(64 * dy_waves(RF), RF == 1 ? 4 : RF <= 4 ? 2 :
 
 // Workgroup (chunk, slice of 256 columns) as above; A's operands stay in registers, a
 // step's operands of u go through LDS to the four wavefronts. Bound by HBM: 8192
-// tokens, 4096 columns 44 us at rank 16 (201 MB with base, 4.6 TB/s), 55 at rank 64.
+// tokens, 4096 columns 44 us at rank 16 (201 MB with base, 4.6 TB/s), 58 at rank 64.
 template <int DT, int RF>
 __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     const uint16_t *__restrict__ x, int M, int K, int r, const uint16_t *__restrict__ A, int L,
     const int32_t *__restrict__ ids, const int32_t *__restrict__ offsets, const int32_t *__restrict__ perm, int rows,
     int chunks, int max_steps, Pieces u, const uint16_t *base, uint16_t *dx, float *__restrict__ dA,
     float *__restrict__ part) {
-  constexpr int E = kE, kP = kPieces<DT>, kCols = 16 * E, kSlice = kCols * kWaves;
-  __shared__ Oct over[RF * kP * 64], along[2 * RF * 64];
+  constexpr int E = kE, kP = kPieces<DT>, kOps = kOperands<DT, RF>, kCols = 16 * E, kSlice = kCols * kWaves;
+  __shared__ Oct over[RF * kP * 64], along[2 * kOps * 64];
   __shared__ __attribute__((aligned(16))) float backs[16 * RF];
   __shared__ __attribute__((aligned(16))) int tokens[kMostTokens];
   __shared__ int list[64];
@@ -399,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     Rows<E> x;
     Rows<E, 4> base[2];
     Shared<RF * kP, kWaves> over;
-    Shared<2 * RF, kWaves> along;
+    Shared<2 * kOps, kWaves> along;
     float back;
     float4_t token_back[2];
   };
@@ -427,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
           v.base[0] = v.base[1] = Rows<E, 4>{};
         }
         v.over.load(u.over + step * RF * kP * 64);
-        v.along.load(u.along + step * 2 * RF * 64);
+        v.along.load(u.along + step * 2 * kOps * 64);
         if constexpr (DT == kF16) {
           v.back = u.over_back[step * 16 * RF + min(static_cast<int>(threadIdx.x), 16 * RF - 1)];
 #pragma unroll
@@ -471,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
           // D's rows are tokens: a lane holds columns k0 + E col .. of tokens 4 q .. + 3
           float4_t d[E] = {};
 #pragma unroll
-          for (int g = 0; g < RF; ++g) {
-            const Oct w = along[(f * RF + g) * 64 + lane];
+          for (int k = 0; k < kOps; ++k) {
+            const Oct w = along[(f * kOps + k) * 64 + lane];
 #pragma unroll
-            for (int e = 0; e < E; ++e) d[e] = mfma<DT>(w, av[e][g], d[e]);
+            for (int e = 0; e < E; ++e) d[e] = mfma<DT>(w, beside(av[e], k, q), d[e]);
           }
           size_t at[4];
           bool live[4];
@@ -564,7 +556,7 @@ Plan plan_of(const AdapterArgs &g) {
     return here;
   };
   p.over = take(static_cast<size_t>(p.steps) * p.rf * pieces * 64 * sizeof(Oct));
-  p.along = take(static_cast<size_t>(p.steps) * 2 * p.rf * 64 * sizeof(Oct));
+  p.along = take(static_cast<size_t>(p.steps) * 2 * operands_of(g.dtype, p.rf) * 64 * sizeof(Oct));
   p.over_back = take(static_cast<size_t>(p.steps) * 16 * p.rf * 4);
   p.along_back = take(static_cast<size_t>(p.steps) * kStep * 4);
   p.u_part = take(static_cast<size_t>(p.slices_y) * g.M * g.r * 4);

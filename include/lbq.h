@@ -626,8 +626,8 @@ lbq_status lbq_adapters_backward_workspace(const lbq_adapters *ad, int32_t M, in
  *   h: fp32 [M][r], written for the backward pass, or NULL.
  * Outputs and workspace overlap no input, but y may be base. A token whose h is
  * infinite or NaN gets NaN; no other token's row changes. h enters the second
- * product to 2^-21 (fp16) or 2^-16 (bf16) of each value, fp16 with 2^-39 of the
- * token's largest at least.
+ * product to 2^-21 (fp16) or 2^-23 (bf16) of each value, fp16 with 2^-39 of the
+ * token's largest at least; so do h and u below enter theirs.
  * Repeat calls give identical bits. Errors as lbq_mx_matmul. */
 lbq_status lbq_adapters_forward(const lbq_adapters *ad, const void *x, int32_t M, const int32_t *ids,
                                 const int32_t *offsets, const int32_t *perm, const void *base, void *y, float *h,

@@ -522,3 +522,79 @@ def test_no_tokens_with_an_order(L, dev):
                                              d_a=torch.ones(2, 4, 128, device="cuda"),
                                              d_b=torch.ones(2, 40, 4, device="cuda"))
             assert dx.shape == (0, 128) and not da.any() and not db.any()
+
+
+def _whole(rows, n, g, r):
+    """[rows][r][n] whole numbers 59 .. 121, of which row j + r // 2 is row j but for steps of one at eight places."""
+    v = g.integers(60, 121, (rows, r, n))
+    half = r // 2
+    for i in range(rows):
+        for j in range(half):
+            at = g.choice(n, 8, replace=False)
+            v[i, half + j] = v[i, j]
+            v[i, half + j, at] += g.integers(0, 2, 8) * 2 - 1
+    v[:, 2 * half:] = 0
+    return v
+
+
+# every form of the forward, every width of rank
+WHOLE = [(1, 1024, 40, 2, 2), (2, 1024, 600, 2, 16), (3, 1024, 24, 2, 34), (5, 8192, 100, 3, 9), (40, 1024, 264, 9, 64),
+         (30, 1024, 130, 4, 128), (64, 2048, 72, 3, 24), (90, 1024, 5, 2, 6), (300, 1024, 515, 3, 16), (200, 1024, 264, 5, 30),
+         (700, 1024, 300, 2, 64), (150, 1024, 97, 3, 128), (1100, 1024, 136, 70, 12)]
+
+
+@pytest.mark.parametrize("order", [True, False])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("M,K,N,n,r", WHOLE)
+def test_h_and_u_keep_their_bits(L, dev, M, K, N, n, r, dtype, order):
+    """Whole numbers of 20 and more bits as h and u, whose differences of a few bits are what y and dx are: all sums are
+    below 2^24, exact in 32 bits in any order, and so have to be the results."""
+    import torch
+
+    say(f"adapters whole numbers M={M} K={K} N={N} L={n} r={r} {dtype} order={order}")
+    g = synth.rng(95, M + K + N + r, synth.ROLE_X)
+    dt = getattr(torch, dtype)
+
+    def up(v):
+        t = torch.from_numpy(np.ascontiguousarray(v).astype(np.float32)).to(dt)
+        assert np.array_equal(t.double().numpy(), v)
+        return t.cuda()
+
+    half = r // 2
+    ids = g.integers(-1, n, M).astype(np.int32)
+    if M == 1:
+        ids[:] = 0
+    idc = torch.from_numpy(ids).cuda()
+    _, off, perm, _ = L.moe_sort(idc[:, None].contiguous(), n)
+    o = (off, perm) if order else None
+    sc = torch.ones(n, device="cuda")
+    on = (ids >= 0)[:, None]
+    few = min(K, 1024)                             # so many values at most, and zeros
+    for back in (False, True):
+        if back and N < 8:
+            continue
+        long, short = (min(N, 1024), K) if back else (few, N)
+        rows = np.zeros((n, r, N if back else K))
+        place = np.sort(g.choice(rows.shape[2], long, replace=False))
+        rows[:, :, place] = _whole(n, long, g, r)
+        x = g.integers(8, 16, (M, rows.shape[2]))
+        pick = np.zeros((n, short, r))
+        pair = g.integers(0, half, short)
+        pick[:, np.arange(short), pair], pick[:, np.arange(short), half + pair] = 1, -1
+        base = g.integers(-8, 9, (M, short))
+        at = ids.clip(0)
+        mid = np.einsum("tk,tjk->tj", x.astype(np.float64), rows[at]) * on
+        want = base + np.einsum("tj,tnj->tn", mid, pick[at]) * on
+        assert np.abs(mid).max() < 2 ** 24 and np.abs(want).max() <= 256
+        if not back:
+            h = torch.empty(M, r, device="cuda")
+            y = L.adapters_forward(L.Adapters(up(rows), up(pick), sc), up(x), idc, base=up(base), h=h, order=o)
+            assert np.array_equal(h.double().cpu().numpy(), mid)
+            got = y
+        else:
+            # B's rows are rows' columns; A's are pick's
+            ad = L.Adapters(up(pick.transpose(0, 2, 1)), up(rows.transpose(0, 2, 1)), sc)
+            got = L.adapters_backward(ad, up(x), torch.zeros(M, K, device="cuda", dtype=dt), torch.zeros(M, r, device="cuda"),
+                                      idc, base=up(base), order=o)[0]
+        bad = got.double().cpu().numpy() != want
+        assert not bad.any(), f"{'dx' if back else 'y'}: {bad.sum()} of {bad.size}"
