@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, RC <= 4 ? 2 : 1) adapters_y_kernel(
     float4_t back[TF];
   };
   // (a step ahead costs more registers than there are from rank 33 on: 8192 tokens, rank
-  // 64, 14336 columns with it 140 us, without 121)
+  // 64, 14336 columns, both launches with it fp16 155 and bf16 255 us, without 141 and 165)
   constexpr int kAhead = RC >= 4 ? 0 : 1;
   in_turn<Step, kAhead>(
       (c.n + kStep - 1) / kStep,
@@ -537,9 +537,12 @@ struct ForwardPlan {
 };
 // up to so many tokens a call has no sort and no operands laid out between its launches
 constexpr int kFewTokens = 64;
-// A's bytes that a workgroup reads to make h for itself, and such workgroups, at most:
-// one token of 4096 -> 4096 at rank 16 takes 10.6 us called one by one and 6.2 in a
-// graph, in two launches 14.7 and 5.6.
+// A's bytes that a workgroup reads to make h for itself, and such workgroups, at most.
+// Called one by one, one launch saves what the other costs the caller (4096 -> 4096, rank 16, 1 to
+// 32 tokens 7.3 us against 11.8, 64 tokens 8.3 and 11.5). From a graph the two are equal up to 32
+// tokens (6.0), then A's reads count: 64 tokens 8.6 and 7.7, 16 tokens of 8192 columns 8.1 and
+// 6.1. At both limits at once one launch is the slower either way (64 tokens of 2048 columns,
+// rank 64, 21.4 and 20.1, 22.6 and 20.7).
 constexpr long kOneBytes = 256 << 10, kOneGroups = 512;
 
 ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
@@ -567,7 +570,8 @@ ForwardPlan forward_plan(const AdapterArgs &g, bool by_list) {
     // chunks so long that 1024 workgroups have one each, but at least 128 tokens (4000
     // tokens of 96 adapters, 2048 columns 13.6 us, with 32 18.9), or 32 where that is
     // still no more than a workgroup a compute unit (257 tokens, 2047 columns 16.2 us with
-    // 128, 11.0 with 32)
+    // 128, 11.0 with 32; both launches of 500 tokens, 8 adapters, 4096 columns 18.8 and 14.4;
+    // of 1000 tokens, 32 adapters, 14336 columns 25.4 and 27.5)
     const long groups = (g.N + 64 * p.e - 1) / (64 * p.e), rows = g.M * groups / 1024;
     const long least = (g.M / 32 + some) * groups <= 256 ? 32 : 128;
     p.rows = static_cast<int>(std::min(std::max((rows + 31) / 32 * 32, least), static_cast<long>(kMostTokens)));

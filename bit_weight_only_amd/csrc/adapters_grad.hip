@@ -395,8 +395,9 @@ __global__ void __launch_bounds__(kThreads, RF <= 4 ? 2 : 1) adapters_x_kernel(
     float back;
     float4_t token_back[2];
   };
-  // (a step ahead costs more registers than there are from rank 17 on: 4000 tokens of 96
-  // adapters, rank 32, with it 34 us, without 26; 8192 tokens, rank 64, 70 and 55)
+  // (a step ahead costs more registers than there are from rank 17 on: all launches of 4000
+  // tokens of 96 adapters, rank 32, with it 80 us, without 70; 8192 tokens, rank 64, bf16, 347
+  // and 260)
   constexpr int kAhead = RF >= 2 ? 0 : 1;
   in_turn<Step, kAhead>(
       (c.n + kStep - 1) / kStep,
@@ -530,7 +531,9 @@ struct Plan {
 
 // Tokens of a chunk: so many that the workgroups of all slices fill `slots` once, and
 // one step at least (257 tokens, 2048 columns, rank 5: dy 11.4 and x 10.7 us with at
-// least 128, 7.3 and 6.9 with 32; 4000 tokens of 96 adapters the same).
+// least 128, 7.3 and 6.9 with 32; 2000 tokens on two adapters, 4096 columns, rank 64 all
+// launches 79 and 74). Where tokens lie together by many adapters a larger least would
+// have fewer sums to add up: 4000 tokens on 96, 2048 columns, rank 32 62 and 84.
 int chunk_rows(int M, int slices, int slots) {
   const long rows = (static_cast<long>(M) * slices + slots - 1) / slots;
   return static_cast<int>(std::min<long>(std::max<long>((rows + kStep - 1) / kStep * kStep, 32), kMostTokens));

@@ -538,7 +538,7 @@ def _whole(rows, n, g, r):
 
 
 # every form of the forward, every width of rank
-WHOLE = [(1, 1024, 40, 2, 2), (2, 1024, 600, 2, 16), (3, 1024, 24, 2, 34), (5, 8192, 100, 3, 9), (40, 1024, 264, 9, 64),
+WHOLE = [(7, 16384, 40, 3, 16), (9, 8192, 72, 2, 20), (10, 8192, 50, 3, 40), (1, 1024, 40, 2, 2), (2, 1024, 600, 2, 16), (3, 1024, 24, 2, 34), (5, 8192, 100, 3, 9), (40, 1024, 264, 9, 64),
          (30, 1024, 130, 4, 128), (64, 2048, 72, 3, 24), (90, 1024, 5, 2, 6), (300, 1024, 515, 3, 16), (200, 1024, 264, 5, 30),
          (700, 1024, 300, 2, 64), (150, 1024, 97, 3, 128), (1100, 1024, 136, 70, 12)]
 
