@@ -269,8 +269,9 @@ constexpr int kMostGroups = 64;
 // What bounds it is instructions: (top_k + 1) rounds, for 4 tokens at once with 16 lanes
 // a token (131072 tokens of 256 experts, 8 picks, sigmoid with bias: 102 us, 276
 // instructions a token, 0.8 TB/s). Few tokens take a wavefront each, whose lists are
-// shorter: softmax over 256 experts 5.8 us against 7.2 for 2048 tokens, 7.8 against
-// 7.4 for 4096 (32 tokens 5.4 us).
+// shorter: 2048 tokens of 256 experts, bf16, softmax 5.9 us against 6.8, sigmoid with bias
+// 11.6 and 13.5, that in groups 16.9 and 19.0; 4096 tokens 7.8 and 6.8, 14.0 and 13.9, 19.5
+// and 19.2 (32 tokens 5.4 us).
 template <int DT, int LANES, int V>
 __global__ void __launch_bounds__(kSelectThreads, 3) moe_select_kernel(MoeSelect r, const void *__restrict__ logits, int M,
                                                                     const float *__restrict__ bias,
@@ -517,8 +518,9 @@ __device__ __forceinline__ float row_top(const typename Elem<DT>::type *row, int
 //
 // Renormalised softmax takes the picks relative to their largest, and reads the whole row
 // for the largest there: what 64 bits hold as 0 has no weight, and no gradient (131072
-// rows of 256 bf16 values 30.6 us; 24.1 without that).
-template <int DT, int V>
+// rows of 256 bf16 values 29.9 us; 24.1 without that): RATIO, a kernel of its own, since the
+// others are a microsecond slower with the code for it.
+template <int DT, int V, bool RATIO>
 __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
     MoeSelect r, const float *__restrict__ d_w, const void *logits, int M, const int32_t *__restrict__ ids,
     void *d_logits) {
@@ -536,7 +538,7 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
       return v > -INFINITY ? fminf(v, 3.4028234663852886e38f) : -INFINITY;
     };
     float most = -INFINITY;
-    if (r.score == kSoftmax && r.renormalise) most = row_top<DT, V>(row, r.E, lane);
+    if constexpr (RATIO) most = row_top<DT, V>(row, r.E, lane);
     int id[2];
     float l[2], g[2], top = -INFINITY;
 #pragma unroll
@@ -573,7 +575,7 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       p[n] = !(l[n] > -INFINITY) ? 0.f : far ? (l[n] > kNoSigmoid ? expf(l[n] - top) : 0.f) : score_of(l[n], r.score, top) * inv;
-      if (r.score == kSoftmax && r.renormalise && !(static_cast<double>(l[n]) - most > kNothing)) p[n] = 0.f;
+      if (RATIO && !(static_cast<double>(l[n]) - most > kNothing)) p[n] = 0.f;
       S += p[n];
       dot += p[n] * g[n];
     }
@@ -659,10 +661,18 @@ static void select_go(const MoeSelect &r, const void *logits, int M, const float
 template <int DT>
 static void select_backward_go(const MoeSelect &r, const float *d_w, const void *logits, int M, const int32_t *ids,
                                void *d_logits, hipStream_t s) {
-  const dim3 grid(select_blocks(M, 4)), block(kSelectThreads);
-  if (r.E <= 64) hipLaunchKernelGGL((moe_select_backward_kernel<DT, 4>), grid, block, 0, s, r, d_w, logits, M, ids, d_logits);
-  else if (r.E <= 256) hipLaunchKernelGGL((moe_select_backward_kernel<DT, 16>), grid, block, 0, s, r, d_w, logits, M, ids, d_logits);
-  else hipLaunchKernelGGL((moe_select_backward_kernel<DT, 64>), grid, block, 0, s, r, d_w, logits, M, ids, d_logits);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(select_blocks(M, 4)), dim3(kSelectThreads), 0, s, r, d_w, logits, M, ids, d_logits);
+  };
+  if (r.score == kSoftmax && r.renormalise) {
+    if (r.E <= 64) go(moe_select_backward_kernel<DT, 4, true>);
+    else if (r.E <= 256) go(moe_select_backward_kernel<DT, 16, true>);
+    else go(moe_select_backward_kernel<DT, 64, true>);
+  } else {
+    if (r.E <= 64) go(moe_select_backward_kernel<DT, 4, false>);
+    else if (r.E <= 256) go(moe_select_backward_kernel<DT, 16, false>);
+    else go(moe_select_backward_kernel<DT, 64, false>);
+  }
 }
 
 hipError_t launch_moe_select(const MoeSelect &r, const void *logits, int dtype, int M, const float *bias, int32_t *ids,
