@@ -342,7 +342,7 @@ __device__ __forceinline__ void others(const int32_t *ids, int t0, int M, int L,
 }
 
 // Few tokens: one tile of up to 16 a workgroup column, bound by reading B (64 tokens on
-// 64 adapters, 28672 columns, rank 16: 13.2 us, 4.4 TB/s) or, for a few tokens, by
+// 64 adapters, 28672 columns, rank 16: 12.9 us, 4.5 TB/s) or, for a few tokens, by
 // latency (one token, 4096 columns 6.2 us in one launch). FROM: h is the sum of the shares,
 // by token or by list entry, or (by token) is made here, by every workgroup for
 // itself: one launch less, for A's way to each of them from the caches (kOneBytes).
