@@ -240,9 +240,12 @@ __device__ __forceinline__ void sort_down(double (&v)[V]) {
           }
 }
 
+// A score times exp(-top): softmax up to its sum, sigmoid for top <= 0. Scores of one top
+// keep their ratio where fp32 does not hold them themselves.
 __device__ __forceinline__ float score_of(float l, int score, float top) {
-  if (score == kSigmoid) return __builtin_amdgcn_rcpf(1.f + expf(-l));
-  return expf(l - top);
+  if (score == kSoftmax) return expf(l - top);
+  const float one = __builtin_amdgcn_rcpf(1.f + expf(-fabsf(l)));
+  return l > 0.f ? one : expf(l - top) * one;
 }
 
 // The same for the order alone: the argument's rounding counts for little, since p falls
@@ -429,12 +432,14 @@ __global__ void __launch_bounds__(kSelectThreads, 3) moe_select_kernel(MoeSelect
         open = open || x[n] != y || (bias && bias[id[n]] != bias[o]);
       }
     }
-    // a ratio of softmax scores is taken relative to the largest pick, which a bias can keep
-    // far below the row's largest (64 bits know where such scores end)
+    // a ratio is taken relative to the largest pick, whose score can be a small one: a sigmoid
+    // far below zero, a softmax that a bias keeps far below the row's largest (64 bits
+    // know where such scores end)
     float from = top;
-    if (r.score == kSoftmax && r.renormalise && !by_logit) {
-      from = row_max<LANES>(fmaxf(x[0], x[1]));
-      open = open || (from > -INFINITY && top - from > 600.f);
+    if (r.renormalise && !(r.score == kSoftmax && by_logit)) {
+      const float most = row_max<LANES>(fmaxf(x[0], x[1]));
+      from = r.score == kSoftmax ? most : fminf(most, 0.f);
+      open = open || (most > -INFINITY && top - from > 600.f);
     }
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
@@ -442,8 +447,6 @@ __global__ void __launch_bounds__(kSelectThreads, 3) moe_select_kernel(MoeSelect
       total += p[n];
     }
     total = row_sum<LANES>(total);
-    // (sigmoids that 32 bits cannot hold still have a ratio)
-    open = open || (r.score == kSigmoid && r.renormalise && total < 0x1p-60f && pick[0] >= kFirst);
     const float factor = r.scale * (!r.renormalise ? inv : total > 0.f ? 1.f / total : 0.f);
     const uint64_t opens = __ballot(open);
     constexpr uint64_t kRow = LANES == 64 ? ~0ull : (1ull << (LANES & 63)) - 1;
@@ -569,12 +572,10 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
       for (int e = lane; e < r.E; e += kLanes) d[e] = 0.f;
     }
     float p[2], S = 0.f, dot = 0.f;
-    // sigmoids are taken relative to the largest where 32 bits cannot hold them
-    // themselves: below -60 they fall like exp(l)
-    const bool far = r.score == kSigmoid && r.renormalise && top < -60.f && top > -INFINITY;
+    if (r.score == kSigmoid) top = r.renormalise ? fminf(top, 0.f) : 0.f;
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-      p[n] = !(l[n] > -INFINITY) ? 0.f : far ? (l[n] > kNoSigmoid ? expf(l[n] - top) : 0.f) : score_of(l[n], r.score, top) * inv;
+      p[n] = l[n] > (r.score == kSigmoid ? kNoSigmoid : -INFINITY) ? score_of(l[n], r.score, top) * inv : 0.f;
       if (RATIO && !(static_cast<double>(l[n]) - most > kNothing)) p[n] = 0.f;
       S += p[n];
       dot += p[n] * g[n];
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(kSelectThreads) moe_select_backward_kernel(
     for (int n = 0; n < 2; ++n) {
       g[n] = id[n] >= 0 ? r.scale * over * (g[n] - mean) : 0.f;   // ds of the slot
       if (dense) across += p[n] * g[n];
-      else g[n] *= p[n] * (r.score == kSigmoid && !far ? __builtin_amdgcn_rcpf(1.f + expf(l[n])) : 1.f);
+      else g[n] *= p[n] * (r.score == kSigmoid ? __builtin_amdgcn_rcpf(1.f + expf(l[n])) : 1.f);
     }
     if (dense) {
       across = row_sum<kLanes>(across);

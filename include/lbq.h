@@ -588,8 +588,9 @@ lbq_status lbq_moe_select(const lbq_router *r, const void *logits, int32_t dtype
  *   ds_j = scale (d_weights_j - [renormalise] sum_i p_i d_weights_i / S) / S,
  * summed over the slots of an expert, and d_l_e = p_e (1 - p_e) ds_e (sigmoid) or
  * p_e (ds_e - sum_i p_i ds_i) (softmax). The choice itself has no gradient, nor
- * has the bias, and a score that counts as 0 gives 0. Slots with ids outside [0, E) count nothing, whatever their
- * d_weights. Experts that may not be picked get 0. d_logits may be logits. */
+ * has the bias, and a score that counts as 0 gives 0. Slots with ids outside [0, E)
+ * count nothing, whatever their d_weights. Experts that may not be picked get 0.
+ * d_logits may be logits. */
 lbq_status lbq_moe_select_backward(const lbq_router *r, const float *d_weights, const void *logits, int32_t dtype,
                                    const int32_t *ids, int32_t M, void *d_logits, void *stream);
 

@@ -385,3 +385,24 @@ def test_sigmoids_around_the_border(L, dev):
     bound[:, :2] = w * (np.abs(g) + (w * np.abs(g)).sum(1, keepdims=True)) * 42 * A.U
     # (the argument of exp is off by its own rounding)
     assert np.all(np.abs(d - want) <= bound * (1.01 + 720 / 4) + A.U * np.abs(want) + 1e-30)
+
+
+@pytest.mark.parametrize("m,E,k", [(40, 24, 6), (60, 256, 32), (2070, 200, 8), (30, 700, 12)])
+def test_sigmoids_of_very_different_sizes(L, dev, m, E, k):
+    """Picks whose own sigmoid fp32 cannot hold, beside others: their ratio may be one that it can. Logits are multiples of
+    1/8, whose differences are exact."""
+    import torch
+
+    g = synth.rng(96, E, synth.ROLE_X)
+    v = np.round(g.standard_normal((m, E)) * 8 * g.choice([8.0, 30.0, 60.0], (m, 1)) + 8 * g.choice([0.0, -41.0, -90.0], (m, 1))) / 8
+    keep = np.argsort(g.random((m, E)), 1) < np.minimum(E, g.integers(1, 2 * k, (m, 1)))
+    keep[:, 0] = True
+    v[0, :3], keep[0] = (-41.0, -95.0, -120.0), np.arange(E) < 3
+    lg = torch.from_numpy(np.where(keep, v, -np.inf).astype(np.float32))
+    ids, w = _check(L, lg, k, score=1)
+    dw = g.standard_normal((m, k)).astype(np.float32)
+    d = L.moe_select_backward(torch.from_numpy(dw).cuda(), lg.cuda(), ids, score=1).double().cpu().numpy()
+    want, bound = A.select_backward(dw.astype(np.float64), lg.double().numpy(), ids.cpu().numpy(), 1)
+    assert np.all(np.abs(d - want) <= bound * 1.01 + HALF["float32"] * np.abs(want) + 2.0 ** -120)
+    _check(L, lg, k, (0.1 * g.standard_normal(E)).astype(np.float32), score=1)
+    _check(L, lg, k, score=1, renormalise=False)
