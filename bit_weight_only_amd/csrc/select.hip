@@ -270,7 +270,7 @@ constexpr int kMostGroups = 64;
 // twice the one and more than the other.
 //
 // What bounds it is instructions: (top_k + 1) rounds, for 4 tokens at once with 16 lanes
-// a token (131072 tokens of 256 experts, 8 picks, sigmoid with bias: 105 us, 279
+// a token (131072 tokens of 256 experts, 8 picks, sigmoid with bias: 105 us, 286
 // instructions a token, 0.7 TB/s). Few tokens take a wavefront each, whose lists are
 // shorter: 2048 tokens of 256 experts, bf16, softmax 5.9 us against 6.8, sigmoid with bias
 // 11.6 and 13.5, that in groups 16.9 and 19.0; 4096 tokens 7.8 and 6.8, 14.0 and 13.9, 19.5
